@@ -288,6 +288,46 @@ int mx_router_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, int64
                   float* dw, float* dlogits, mx_stream_t stream);
 
 /*
+ * The whole SwiGLU MoE layer for a few tokens (decoding): what the layer of
+ * mx_route_topk .. mx_combine computes, in two launches, for at most 64
+ * tokens.  Weights are those of the layer's forward GEMMs; activations stay
+ * in bf16 (they are not quantized: with this few tokens the stream of weights
+ * is the cost), so the result is nearer to the real-valued layer than the
+ * MXFP8 path's.
+ *   out[t] = RNE_bf16(residual[t] + sum_j W2_e (w[t,j] silu(g) * u)),
+ *   [g; u] = W1_e x[t],  e the topk largest logits of token t (equal logits to
+ *   the lower id), w the softmax of their logits, in fp32; w silu(g) u is
+ *   rounded to bf16 once.
+ *   x        bf16 [tokens, H]; logits fp32 [tokens, num_experts].  A logit of
+ *            -inf is never chosen; a token whose logits are all -inf (padding)
+ *            reads no expert and gets out[t] = residual[t], or zero.  NaN and
+ *            +inf logits make the token's row NaN.
+ *   w1       MX rowwise [num_experts, 2F, H] (gate rows [0, F), up rows
+ *            [F, 2F)), scales of [num_experts * 2F, H]; w2 MX rowwise
+ *            [num_experts, H, F], scales of [num_experts * H, F]
+ *   residual optional bf16 [tokens, H]; out bf16 [tokens, H] (may be residual)
+ *   workspace >= mx_moe_tokens_workspace_size(...) bytes, written and read
+ *            within the call; calls that overlap in time need their own
+ * The result does not depend on the schedule (bit-identical between calls),
+ * and a token's row not on the other tokens beyond the order of its fp32 sums.
+ * Requires H % 32 == 0, F % 32 == 0, 1 <= topk <= num_experts; x, w1, w2 and
+ * the workspace 16-byte aligned.  MX_EUNSUPPORTED (and a workspace size of 0)
+ * above 64 tokens, 1024 experts or top-64, and for one expert's matrix or the
+ * scales of 2^31 bytes or more.
+ */
+size_t mx_moe_tokens_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t F);
+
+int mx_moe_tokens(const uint16_t* x, const float* logits, int64_t tokens, int32_t topk, int32_t num_experts,
+                  int64_t H, int64_t F, const uint8_t* w1_q, const uint8_t* w1_s, const uint8_t* w2_q,
+                  const uint8_t* w2_s, const uint16_t* residual, uint16_t* out, void* workspace,
+                  size_t workspace_bytes, mx_stream_t stream);
+
+/* The same with bf16 weights w1 [num_experts, 2F, H], w2 [num_experts, H, F]. */
+int mx_bf16_moe_tokens(const uint16_t* x, const float* logits, int64_t tokens, int32_t topk, int32_t num_experts,
+                       int64_t H, int64_t F, const uint16_t* w1, const uint16_t* w2, const uint16_t* residual,
+                       uint16_t* out, void* workspace, size_t workspace_bytes, mx_stream_t stream);
+
+/*
  * BF16 baseline of the expert step: the same permute and grouped GEMMs with
  * bf16 operands, so the MXFP8 path can be timed against the BF16 MoE layer
  * the digest page compares with (Overview and Key Statistics & Figures: the

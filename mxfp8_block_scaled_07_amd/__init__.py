@@ -42,6 +42,10 @@ _SIGNATURES = {
                                                _vp]),
     "mx_route_topk": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _vp, _vp]),
     "mx_router_bwd": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "mx_moe_tokens_workspace_size": (_sz, [_i64, _i32, _i32, _i64]),
+    "mx_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                     _vp]),
+    "mx_bf16_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mx_bf16_gather": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
     "mx_bf16_grouped_gemm_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_dgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
@@ -173,6 +177,23 @@ def mx_router_bwd(dout, y, y_rows, H, dst_row, expert_ids, weights, tokens, num_
                   stream=None):
     _check(lib().mx_router_bwd(_p(dout), _p(y), y_rows, H, _p(dst_row), _p(expert_ids), _p(weights), tokens,
                                num_experts, topk, _p(dw), _p(dlogits), _s(stream)), "mx_router_bwd")
+
+
+def mx_moe_tokens_workspace_size(tokens, topk, num_experts, F):
+    return int(lib().mx_moe_tokens_workspace_size(tokens, topk, num_experts, F))
+
+
+def mx_moe_tokens(x, logits, tokens, topk, num_experts, H, F, w1_q, w1_s, w2_q, w2_s, residual, out, workspace,
+                  workspace_bytes, stream=None):
+    _check(lib().mx_moe_tokens(_p(x), _p(logits), tokens, topk, num_experts, H, F, _p(w1_q), _p(w1_s), _p(w2_q),
+                               _p(w2_s), _p(residual), _p(out), _p(workspace), workspace_bytes, _s(stream)),
+           "mx_moe_tokens")
+
+
+def mx_bf16_moe_tokens(x, logits, tokens, topk, num_experts, H, F, w1, w2, residual, out, workspace,
+                       workspace_bytes, stream=None):
+    _check(lib().mx_bf16_moe_tokens(_p(x), _p(logits), tokens, topk, num_experts, H, F, _p(w1), _p(w2), _p(residual),
+                                    _p(out), _p(workspace), workspace_bytes, _s(stream)), "mx_bf16_moe_tokens")
 
 
 def mx_bf16_gather(x, batch, rows, cols, gather, rows_out, out_rows, out_cols, stream=None):
