@@ -328,6 +328,48 @@ int mx_bf16_moe_tokens(const uint16_t* x, const float* logits, int64_t tokens, i
                        uint16_t* out, void* workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * AdamW step over many tensors: the update that takes the layer's weight
+ * gradients.  Per element, t = *step (>= 1; counted up by the caller before
+ * the call; a smaller value counts as 1), fp32:
+ *   g = grad * (grad_scale ? *grad_scale : 1)
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * lr, step and grad_scale (optional: an unscale or clip factor) are read on
+ * the device, so a captured step follows them.
+ *   param   fp32 or bf16 (param_dtype) [n]; bf16 is rounded stochastically
+ *   grad    fp32 or bf16 (grad_dtype) [n]
+ *   m, v    state_bits 32: fp32 [n].  state_bits 8: MX blocks of 32
+ *           consecutive elements, E4M3 codes [n] with E8M0 scales m_scale,
+ *           v_scale [ceil(n / 32)]; v holds the ROOT of the second moment.
+ *           A block's scale is the smallest with which its largest value is
+ *           not above 448; codes are rounded stochastically, a positive root
+ *           never to zero; non-finite values are stored as NaN.  A new state
+ *           is all zero bytes (codes and scales).
+ *   copy    optional bf16 [n]: the new parameter rounded to nearest (for the
+ *           quantize or the GEMMs); of a bf16 parameter, its value
+ * The random bits depend on (seed, *step, the tensor's index in the call, the
+ * element) alone: a step repeated from the same state gives the same bits.
+ * Tensors must not overlap each other; each is updated in place and nothing
+ * past element n is touched.  Tensors with n == 0 are skipped.  All but the
+ * scales 16-byte aligned; 0 <= beta < 1, eps >= 0.  `tensors` is host memory,
+ * read before the call returns.  One launch per 48 tensors.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale; /* state_bits 8 only */
+  uint8_t* v_scale;
+  uint16_t* copy;   /* or NULL */
+  int64_t n;
+} mx_adamw_tensor_t;
+
+int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t param_dtype, int32_t grad_dtype,
+             int32_t state_bits, const float* lr, const int32_t* step, const float* grad_scale, double beta1,
+             double beta2, double eps, double weight_decay, uint64_t seed, mx_stream_t stream);
+
+/*
  * BF16 baseline of the expert step: the same permute and grouped GEMMs with
  * bf16 operands, so the MXFP8 path can be timed against the BF16 MoE layer
  * the digest page compares with (Overview and Key Statistics & Figures: the

@@ -22,6 +22,7 @@ MX_OUT_BF16, MX_OUT_F32 = 0, 1
 _lib = None
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_f64 = ctypes.c_double
 _SIGNATURES = {
     "mx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "mx_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
@@ -46,11 +47,19 @@ _SIGNATURES = {
     "mx_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                      _vp]),
     "mx_bf16_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mx_adamw": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _f64, _f64, _f64, _f64, ctypes.c_uint64,
+                                _vp]),
     "mx_bf16_gather": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
     "mx_bf16_grouped_gemm_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_dgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
 }
+
+
+class AdamwTensor(ctypes.Structure):
+    """mx_adamw_tensor_t: one tensor of an AdamW step (device addresses)."""
+    _fields_ = [("param", _vp), ("grad", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp),
+                ("copy", _vp), ("n", _i64)]
 
 
 class MXError(RuntimeError):
@@ -194,6 +203,13 @@ def mx_bf16_moe_tokens(x, logits, tokens, topk, num_experts, H, F, w1, w2, resid
                        workspace_bytes, stream=None):
     _check(lib().mx_bf16_moe_tokens(_p(x), _p(logits), tokens, topk, num_experts, H, F, _p(w1), _p(w2), _p(residual),
                                     _p(out), _p(workspace), workspace_bytes, _s(stream)), "mx_bf16_moe_tokens")
+
+
+def mx_adamw(tensors, count, param_dtype, grad_dtype, state_bits, lr, step, grad_scale, beta1, beta2, eps,
+             weight_decay, seed, stream=None):
+    """tensors: an array of AdamwTensor (see adamw_table)."""
+    _check(lib().mx_adamw(tensors, count, param_dtype, grad_dtype, state_bits, _p(lr), _p(step), _p(grad_scale),
+                          beta1, beta2, eps, weight_decay, seed, _s(stream)), "mx_adamw")
 
 
 def mx_bf16_gather(x, batch, rows, cols, gather, rows_out, out_rows, out_cols, stream=None):
@@ -349,3 +365,23 @@ def router_bwd(dout, y, dst_row, expert_ids, weights, num_experts, stream=None):
         mx_router_bwd(dout, y, y.shape[0], y.shape[1], dst_row, expert_ids, weights, T, num_experts, topk, dw, dl,
                       stream)
     return dw, dl
+
+
+def adamw_table(rows):
+    """The host table mx_adamw takes, from (param, grad, m, v, m_scale, v_scale, copy) per tensor (contiguous device
+    tensors; None for what is not there).  It keeps its tensors alive and can be used for every step."""
+    table = (AdamwTensor * len(rows))()
+    for t, row in zip(table, rows):
+        param, grad, m, v, m_scale, v_scale, copy = row
+        n = param.numel()
+        for x in row:
+            if x is not None and not x.is_contiguous():
+                raise ValueError("adamw_table: tensors must be contiguous")
+        for x, want in ((grad, n), (m, n), (v, n), (copy, n), (m_scale, -(-n // 32)), (v_scale, -(-n // 32))):
+            if x is not None and x.numel() != want:
+                raise ValueError(f"adamw_table: {x.numel()} elements where {want} belong to a parameter of {n}")
+        t.param, t.grad, t.m, t.v = (x.data_ptr() for x in (param, grad, m, v))
+        t.m_scale, t.v_scale, t.copy = (None if x is None else x.data_ptr() for x in (m_scale, v_scale, copy))
+        t.n = n
+    table.tensors = rows
+    return table
