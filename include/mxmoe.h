@@ -370,6 +370,50 @@ int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t param_dtyp
              double beta2, double eps, double weight_decay, uint64_t seed, mx_stream_t stream);
 
 /*
+ * Dense bf16 product with bias, activation and residual in its epilogue: the
+ * gate product whose logits mx_route_topk takes (out_dtype MX_OUT_F32), and
+ * the dense projections around the expert layer.
+ *   z = x w^T + bias,  out = act(z) + residual          (fp32 sums)
+ *   x        bf16 [rows, k]; w bf16 [n, k]
+ *   bias     optional fp32 [n]; residual optional bf16 [rows, n]
+ *   act      MX_ACT_*: none, relu, gelu (erf), gelu_tanh, silu; of the
+ *            unrounded z
+ *   z        optional bf16 [rows, n]: z for the backward (RNE)
+ *   out      [rows, n], bf16 (RNE) or fp32; a bf16 out may be the residual
+ *   workspace >= mx_bf16_linear_workspace_size(rows, n, k) bytes (0: may be
+ *            NULL); calls that overlap in time need their own
+ * Any rows >= 0 and n >= 1 (n % 8 == 0 takes wide stores); k % 32 == 0; all
+ * but the bias 16-byte aligned.  MX_EUNSUPPORTED for n or k >= 2^21 or
+ * rows >= 2^31.  Repeated calls give the same bits.
+ */
+enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_GELU = 2, MX_ACT_GELU_TANH = 3, MX_ACT_SILU = 4 };
+
+size_t mx_bf16_linear_workspace_size(int64_t rows, int64_t n, int64_t k);
+
+int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual, int64_t rows,
+                   int64_t n, int64_t k, int32_t act, uint16_t* z, void* out, int32_t out_dtype, void* workspace,
+                   size_t workspace_bytes, mx_stream_t stream);
+
+/*
+ * Backward of mx_bf16_linear (the residual's gradient is dout itself):
+ *   dz = dout act'(z);  dx = dz w + dx_add;  dw = dz^T x;  dbias = sum_rows dz
+ *   dout     [rows, n] bf16 or fp32 (dout_dtype); z bf16 [rows, n] as kept by
+ *            the forward (not read for MX_ACT_NONE); x, w as in the forward
+ *   dx_add   optional bf16 [rows, k], a gradient of x from elsewhere
+ *   dx       bf16 [rows, k], dw bf16 [n, k], dbias fp32 [n]; any may be NULL,
+ *            not all; a dx may be its dx_add
+ * dz is rounded to bf16 once for the two products (the matrix instruction's
+ * operand); dbias sums the unrounded dz.  fp32 sums; repeated calls give the
+ * same bits.  rows == 0 gives zero dw and dbias.  Sizes and alignment as in
+ * the forward; workspace >= mx_bf16_linear_bwd_workspace_size(...) bytes.
+ */
+size_t mx_bf16_linear_bwd_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t act);
+
+int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const uint16_t* z, const uint16_t* x, const uint16_t* w,
+                       const uint16_t* dx_add, int64_t rows, int64_t n, int64_t k, int32_t act, uint16_t* dx,
+                       uint16_t* dw, float* dbias, void* workspace, size_t workspace_bytes, mx_stream_t stream);
+
+/*
  * BF16 baseline of the expert step: the same permute and grouped GEMMs with
  * bf16 operands, so the MXFP8 path can be timed against the BF16 MoE layer
  * the digest page compares with (Overview and Key Statistics & Figures: the

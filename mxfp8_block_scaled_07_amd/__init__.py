@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libmxmoe.so")
 
 MX_OK, MX_EINVAL, MX_EUNSUPPORTED, MX_EHIP = 0, -1, -2, -3
 MX_OUT_BF16, MX_OUT_F32 = 0, 1
+MX_ACT_NONE, MX_ACT_RELU, MX_ACT_GELU, MX_ACT_GELU_TANH, MX_ACT_SILU = 0, 1, 2, 3, 4
 
 _lib = None
 
@@ -49,6 +50,11 @@ _SIGNATURES = {
     "mx_bf16_moe_tokens": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mx_adamw": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _f64, _f64, _f64, _f64, ctypes.c_uint64,
                                 _vp]),
+    "mx_bf16_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "mx_bf16_linear": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "mx_bf16_linear_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "mx_bf16_linear_bwd": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp,
+                                          _sz, _vp]),
     "mx_bf16_gather": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
     "mx_bf16_grouped_gemm_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_dgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
@@ -203,6 +209,26 @@ def mx_bf16_moe_tokens(x, logits, tokens, topk, num_experts, H, F, w1, w2, resid
                        workspace_bytes, stream=None):
     _check(lib().mx_bf16_moe_tokens(_p(x), _p(logits), tokens, topk, num_experts, H, F, _p(w1), _p(w2), _p(residual),
                                     _p(out), _p(workspace), workspace_bytes, _s(stream)), "mx_bf16_moe_tokens")
+
+
+def mx_bf16_linear_workspace_size(rows, n, k):
+    return int(lib().mx_bf16_linear_workspace_size(rows, n, k))
+
+
+def mx_bf16_linear(x, w, bias, residual, rows, n, k, act, z, out, out_dtype, workspace, workspace_bytes, stream=None):
+    _check(lib().mx_bf16_linear(_p(x), _p(w), _p(bias), _p(residual), rows, n, k, act, _p(z), _p(out), out_dtype,
+                                _p(workspace), workspace_bytes, _s(stream)), "mx_bf16_linear")
+
+
+def mx_bf16_linear_bwd_workspace_size(rows, n, k, act):
+    return int(lib().mx_bf16_linear_bwd_workspace_size(rows, n, k, act))
+
+
+def mx_bf16_linear_bwd(dout, dout_dtype, z, x, w, dx_add, rows, n, k, act, dx, dw, dbias, workspace, workspace_bytes,
+                       stream=None):
+    _check(lib().mx_bf16_linear_bwd(_p(dout), dout_dtype, _p(z), _p(x), _p(w), _p(dx_add), rows, n, k, act, _p(dx),
+                                    _p(dw), _p(dbias), _p(workspace), workspace_bytes, _s(stream)),
+           "mx_bf16_linear_bwd")
 
 
 def mx_adamw(tensors, count, param_dtype, grad_dtype, state_bits, lr, step, grad_scale, beta1, beta2, eps,

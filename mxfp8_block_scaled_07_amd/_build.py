@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxmoe.so")
 SOURCES = ["quantize.hip", "permute.hip", "gemm.hip", "glue.hip", "router.hip", "bf16.hip", "ceiling.hip",
-           "tokens.hip", "adamw.hip"]
+           "tokens.hip", "linear.hip", "adamw.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,791 @@
+// The dense bf16 product with an epilogue, and its backward (gfx950):
+//
+//   z = x w^T + bias,  out = act(z) + residual            (x [M, K], w [N, K])
+//   dz = dout act'(z), dx = dz w (+ dx_add), dw = dz^T x, dbias = sum_m dz
+//
+// All three products are C[i, j] = sum_c A(i, c) B(j, c) and run in one
+// kernel: an operand is stored either with c contiguous ("rows": x and w in
+// the forward, dz in dx) or with i or j contiguous ("columns": w in dx, dz and
+// x in dw).  Tiles of 64 c come into LDS by LDS-direct loads in their stored
+// layout.  Rows are read as fragments with 16-byte LDS reads, columns with
+// the transposing reads (ds_read_b64_tr_b16), so no operand is ever
+// transposed in memory.
+//
+// Up to 64 tokens the forward streams w once through the code of skinny.h.
+// Sums are fp32 in a fixed order; where the tiles are too few for the card
+// the contraction is split over workgroups, whose fp32 partial sums are
+// added in order by a second launch with the same epilogue.
+
+#include "skinny.h"
+
+#pragma clang diagnostic ignored "-Winline-asm"
+
+namespace mx {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kCus = 256;                    // MI355X
+constexpr int kXcds = 8;
+constexpr int kC = 64;                       // contraction elements of an LDS tile
+constexpr uint32_t kOob = 0x80000000u;       // an offset that reads as zero
+constexpr int kSkinny = 64;                  // most rows of the streaming form
+
+// ---------------------------------------------------------------- activations
+// sigmoid(x) and sigmoid(-x) from e^-|x| in (0, 1]: neither is a difference.
+__device__ __forceinline__ float sigmoid2(float x, float& minus) {
+  const float e = expf(-fabsf(x));
+  const float r = 1.0f / (1.0f + e), q = e * r;
+  minus = x >= 0.0f ? q : r;
+  return x >= 0.0f ? r : q;
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  float m;
+  return sigmoid2(x, m);
+}
+
+constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case MX_ACT_RELU: return z > 0.0f ? z : (z == z ? 0.0f : z);
+    case MX_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    // 0.5 (1 + tanh(y)) = sigmoid(2 y)
+    case MX_ACT_GELU_TANH: return z * sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    case MX_ACT_SILU: return z * sigmoid(z);
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case MX_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+    case MX_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case MX_ACT_GELU_TANH: {
+      if (fabsf(z) > 20.0f) return z > 0.0f ? 1.0f : 0.0f;   // to fp32 (and z^3 could overflow)
+      float m;
+      const float s = sigmoid2(2.0f * kGeluC * (z + kGeluA * z * z * z), m);
+      return s + z * s * m * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    }
+    case MX_ACT_SILU: {
+      float m;
+      const float s = sigmoid2(z, m);
+      return s * (1.0f + z * m);
+    }
+    default: return 1.0f;
+  }
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float bf1(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// ---------------------------------------------------------------- epilogue
+struct Epi {
+  const float* bias;         // [J] or null
+  const uint16_t* residual;  // [I, J] or null
+  uint16_t* z;               // [I, J] or null
+  void* out;                 // [I, J]
+  int32_t act;
+  bool f32;
+  bool wide;                 // J % 8 == 0: 16-byte accesses
+};
+
+// 8 consecutive columns of one row from their fp32 sums.
+__device__ __forceinline__ void finish8(const Epi& e, float (&v)[8], int64_t i, int64_t j, int64_t J) {
+  if (j >= J) return;
+  const int n = J - j < 8 ? (int)(J - j) : 8;
+  if (e.bias) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) v[k] += e.bias[j + k];
+  }
+  const int64_t at = i * J + j;
+  if (e.z) {
+    if (e.wide) {
+      *reinterpret_cast<uint4*>(e.z + at) =
+          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    } else {
+      for (int k = 0; k < n; ++k) e.z[at + k] = (uint16_t)bf16x2_rne(v[k], v[k]);
+    }
+  }
+  if (e.act != MX_ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], e.act);
+  }
+  if (e.residual) {
+    if (e.wide) {
+      const uint4 r = *reinterpret_cast<const uint4*>(e.residual + at);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] += bf_lo(w[k]);
+        v[2 * k + 1] += bf_hi(w[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) v[k] += bf1(e.residual[at + k]);
+    }
+  }
+  if (e.f32) {
+    float* o = static_cast<float*>(e.out) + at;
+    if (e.wide) {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) o[k] = v[k];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(e.out) + at;
+    if (e.wide) {
+      *reinterpret_cast<uint4*>(o) =
+          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) o[k] = (uint16_t)bf16x2_rne(v[k], v[k]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tiled product
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;        // elements between stored rows
+};
+
+struct Product {
+  Operand a, b;
+  int64_t I, J, C;       // rows and columns of the result, contraction length
+  int32_t tiles_i, tiles_j, splits;
+  int32_t split_tiles;   // LDS tiles (64 c) per split
+  float* part;           // splits > 1: fp32 partial sums [splits, I, J]
+  Epi epi;
+};
+
+__device__ __forceinline__ v4u rsrc(const void* base, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t n = bytes <= 0 ? 0u : (bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes);
+  return v4u{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, n, 0x00020000u};
+}
+
+// One LDS-direct load of 16 bytes per lane, to LDS byte lds + 16 lane.  Inline
+// asm, so that the compiler puts no wait of its own before LDS reads: every
+// wait on these loads is an explicit vmcnt before a barrier.
+__device__ __forceinline__ void dma16(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "m0", "memory");
+}
+
+constexpr int waitcnt_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+
+// Swizzles of 16-byte chunks.  Rows: 128-byte LDS rows, chunk ^ (r >> 1) & 7,
+// so the 16-byte reads of 32 consecutive rows spread over all banks.  Columns:
+// an LDS row is one c with R columns; a transposing read takes 64 bytes of 4
+// consecutive c at once, which the swizzle moves to different 64-byte banks.
+__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
+template <int R>
+__device__ __forceinline__ int col_swizzle(int c) { return R >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2; }
+
+// The LDS-direct loads of one operand tile: kLoads per wave and 64-c tile.
+template <bool kRows, int R, int kNw>
+struct TileLoads {
+  static constexpr int kLoads = R / 8 / kNw;
+  static_assert(R % (8 * kNw) == 0, "whole loads per wave");
+  uint32_t voff[kLoads];
+  int32_t kc;   // rows: the lane's first c in a tile
+  const uint8_t* base;
+  int64_t bytes, step;
+
+  // first: the tile's first row (i or j), n: rows of the operand, C: contraction length
+  __device__ void init(const Operand& o, int64_t first, int64_t n, int64_t C) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (kRows) {
+      const int64_t rows = n - first < R ? n - first : R;
+      base = reinterpret_cast<const uint8_t*>(o.p + first * o.ld);
+      bytes = rows * o.ld * 2;
+      step = 0;
+      kc = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = 8 * (w + kNw * i) + (lane >> 3);
+        const int ch = (lane & 7) ^ row_swizzle(r);
+        kc = 8 * ch;   // the same for every i (kNw is even)
+        voff[i] = (uint32_t)r * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch;
+      }
+    } else {
+      base = reinterpret_cast<const uint8_t*>(o.p + first);
+      bytes = C * o.ld * 2 - first * 2;
+      step = kC * o.ld * 2;
+      kc = 0;
+      constexpr int kPer = R / 8;          // chunks per LDS row
+      constexpr int kRowsPer = 64 / kPer;  // LDS rows of one load
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int c = kRowsPer * (w + kNw * i) + lane / kPer;
+        const int ch = (lane % kPer) ^ col_swizzle<R>(c);
+        // columns past the operand's are other rows' data, or past the end: masked
+        voff[i] = first + 8 * ch < n ? (uint32_t)c * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch : kOob;
+      }
+    }
+  }
+
+  // tile: index of the 64-c tile
+  __device__ void issue(int64_t tile, int64_t C, uint32_t lds) const {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (kRows) {
+      const v4u r = rsrc(base, bytes);
+      const uint32_t soff = (uint32_t)(tile * kC * 2);
+      const bool ok = tile * kC + kc < C;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) dma16(r, lds + 1024u * (uint32_t)(w + kNw * i), ok ? voff[i] : kOob, soff);
+    } else {
+      const v4u r = rsrc(base + tile * step, bytes - tile * step);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) dma16(r, lds + 1024u * (uint32_t)(w + kNw * i), voff[i], 0);
+    }
+  }
+};
+
+// Lane offsets of a 32 (i) x 16 (c) fragment; kk = 0..3 in a 64-c tile.
+template <bool kRows, int R>
+struct FragAt {
+  int row, sw, lo, hi;
+  __device__ void init() {
+    const int lane = threadIdx.x & 63;
+    if constexpr (kRows) {
+      row = (lane & 31) * 128;
+      sw = row_swizzle(lane & 31);
+      lo = lane >> 5;
+    } else {
+      const int l = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
+      const int c = 8 * h + (l >> 2);
+      row = c * (2 * R);
+      sw = col_swizzle<R>(c);
+      lo = 2 * half + ((l & 3) >> 1);   // 16-byte chunk inside the fragment's 32 columns
+      hi = 8 * (l & 1);
+    }
+  }
+  // i0: the fragment's first row inside the tile, a multiple of 32
+  __device__ v8bf_s read(const uint8_t* tile, int i0, int kk) const {
+    if constexpr (kRows) {
+      return *reinterpret_cast<const v8bf_s*>(tile + i0 * 128 + row + 16 * ((2 * kk + lo) ^ sw));
+    } else {
+      const uint8_t* p = tile + kk * 16 * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
+      // c .. c + 3 and c + 4 .. c + 7: the swizzle depends on c & 3 only
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * R));
+      return __builtin_bit_cast(v8bf_s, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// BM x BN result tile, kWm x kWn waves, kSlots LDS tiles in flight.
+template <int BM, int BN, int kWm, int kWn, int kSlots, bool kARows, bool kBRows>
+__global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
+  constexpr int kNw = kWm * kWn;
+  constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
+  constexpr int kABytes = BM * kC * 2, kSlot = (BM + BN) * kC * 2;
+  // the epilogue's slice of a wave: 32 rows of W fp32 columns
+  constexpr int W = TN < 64 ? TN : 64, kPitch = W * 4 + 16;
+  constexpr int kLds = kSlots * kSlot > kNw * 32 * kPitch ? kSlots * kSlot : kNw * 32 * kPitch;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / kWn, wn = wave % kWn;
+
+  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous range of tiles,
+  // walked in bands of 8 row tiles, so that neighbours share operands in its L2.
+  const int64_t total = (int64_t)p.tiles_i * p.tiles_j * p.splits;
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t L = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || L >= total) return;
+  const int32_t tiles = p.tiles_i * p.tiles_j;
+  const int32_t split = (int32_t)(L / tiles), q = (int32_t)(L % tiles);
+  constexpr int kBand = 8;
+  const int32_t band = q / (kBand * p.tiles_j), in = q % (kBand * p.tiles_j);
+  const int32_t rows_in = p.tiles_i - band * kBand < kBand ? p.tiles_i - band * kBand : kBand;
+  const int64_t i0 = (int64_t)(band * kBand + in % rows_in) * BM;
+  const int64_t j0 = (int64_t)(in / rows_in) * BN;
+
+  const int64_t all = (p.C + kC - 1) / kC;
+  const int64_t t0 = (int64_t)split * p.split_tiles;
+  const int64_t t1 = t0 + p.split_tiles < all ? t0 + p.split_tiles : all;
+
+  TileLoads<kARows, BM, kNw> la;
+  TileLoads<kBRows, BN, kNw> lb;
+  la.init(p.a, i0, p.I, p.C);
+  lb.init(p.b, j0, p.J, p.C);
+  constexpr int kLoads = TileLoads<kARows, BM, kNw>::kLoads + TileLoads<kBRows, BN, kNw>::kLoads;
+  const uint32_t base = (uint32_t)(uintptr_t)(const lds_void*)lds;
+  FragAt<kARows, BM> fa;
+  FragAt<kBRows, BN> fb;
+  fa.init();
+  fb.init();
+
+  v16f acc[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
+
+#pragma unroll
+  for (int s = 0; s < kSlots - 1; ++s)
+    if (t0 + s < t1) {
+      la.issue(t0 + s, p.C, base + s * kSlot);
+      lb.issue(t0 + s, p.C, base + s * kSlot + kABytes);
+    }
+  int slot = 0;
+  for (int64_t t = t0; t < t1; ++t) {
+    // this wave's loads of tile t are done (the kSlots - 2 tiles after it may
+    // be in flight; near the end fewer are, so everything is waited for) ...
+    if (t + kSlots - 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 2)));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    asm volatile("" ::: "memory");
+    // ... and after the barrier every wave's, and every wave has read tile t - 1
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int64_t nt = t + kSlots - 1;
+    if (nt < t1) {
+      const int ns = slot == 0 ? kSlots - 1 : slot - 1;   // the slot of tile t - 1
+      la.issue(nt, p.C, base + ns * kSlot);
+      lb.issue(nt, p.C, base + ns * kSlot + kABytes);
+    }
+    const uint8_t* A = lds + slot * kSlot;
+    const uint8_t* B = A + kABytes;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      v8bf_s a[FM], b[FN];
+#pragma unroll
+      for (int n = 0; n < FN; ++n) b[n] = fb.read(B, wn * TN + 32 * n, kk);
+#pragma unroll
+      for (int m = 0; m < FM; ++m) a[m] = fa.read(A, wm * TM + 32 * m, kk);
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[n], a[m], acc[m][n], 0, 0, 0);
+    }
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    // this wave's LDS reads are done before it reaches the next barrier
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));
+    asm volatile("" ::: "memory");
+  }
+  __syncthreads();
+
+  // Epilogue through LDS (a wave's own slice): the accumulators hold 4
+  // consecutive columns of one row per lane; rows of 8 columns per lane go out.
+  uint8_t* slice = lds + wave * 32 * kPitch;
+  const int wr = lane & 31, h = lane >> 5;
+  constexpr int kLpr = W / 8, kRpp = 64 / kLpr;   // lanes per row, rows per pass
+  const int rr = lane / kLpr, c8 = lane % kLpr;
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+#pragma unroll
+    for (int n0 = 0; n0 < FN; n0 += W / 32) {
+#pragma unroll
+      for (int n = 0; n < W / 32; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(slice + wr * kPitch + (32 * n + 8 * g + 4 * h) * 4) =
+              make_float4(acc[m][n0 + n][4 * g], acc[m][n0 + n][4 * g + 1], acc[m][n0 + n][4 * g + 2],
+                          acc[m][n0 + n][4 * g + 3]);
+      // exchanged between the wave's lanes, whose LDS accesses run in order
+      asm volatile("" ::: "memory");
+#pragma unroll 1
+      for (int it = 0; it < 32 / kRpp; ++it) {
+        const int row = kRpp * it + rr;
+        const float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8);
+        const float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8 + 16);
+        const int64_t i = i0 + wm * TM + 32 * m + row, j = j0 + wn * TN + 32 * n0 + 8 * c8;
+        if (i < p.I && j < p.J) {
+          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          if (p.splits > 1) {
+            float* o = p.part + ((int64_t)split * p.I + i) * p.J + j;
+            if (p.epi.wide) {
+              *reinterpret_cast<float4*>(o) = x;
+              *reinterpret_cast<float4*>(o + 4) = y;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (j + k < p.J) o[k] = v[k];
+            }
+          } else {
+            finish8(p.epi, v, i, j, p.J);
+          }
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+}
+
+// The partial sums of a split contraction, in order, then the epilogue.
+__global__ void __launch_bounds__(256) k_join(const float* __restrict__ part, int32_t splits, int64_t I, int64_t J,
+                                              Epi epi) {
+  const int64_t groups = (J + 7) / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= I * groups) return;
+  const int64_t i = at / groups, j = 8 * (at - i * groups);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + ((int64_t)s * I + i) * J + j;
+    if (epi.wide) {
+      const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j + k < J) v[k] += p[k];
+    }
+  }
+  finish8(epi, v, i, j, J);
+}
+
+// ---------------------------------------------------------------- few rows
+// A workgroup owns 16 rows of w; its eight waves take steps of 128 k in turn.
+constexpr int kSkWaves = 8;
+
+template <int NT>
+__global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __restrict__ x,
+                                                          const uint16_t* __restrict__ w, int64_t M, int64_t N,
+                                                          int64_t K, Epi epi) {
+  __shared__ float red[kSkWaves][NT][4][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15;
+  const int64_t n0 = 16 * (int64_t)blockIdx.x;
+  const int64_t rows = N - n0 < 16 ? N - n0 : 16;
+  WRows<false> wr;
+  wr.q = buf(w + n0 * K, rows * K * 2);
+  const __amdgpu_buffer_rsrc_t xr = buf(x, M * K * 2);
+  uint32_t off[NT];
+  v4f_s acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = 16 * t + r;
+    off[t] = m < M ? 2u * (uint32_t)m * (uint32_t)K : kNoRow;
+    acc[t] = v4f_s{0.f, 0.f, 0.f, 0.f};
+  }
+  const int steps = (int)((K + kStepK - 1) / kStepK);
+  for (int s = wave; s < steps; s += kSkWaves) {
+    WStep<false> ws;
+    XStep xs[NT];
+    load_w<false>(ws, wr, (uint32_t)r, (uint32_t)K, (uint32_t)(s * kStepK), r < rows);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) load_x(xs[t], xr, off[t], (uint32_t)K, (uint32_t)(s * kStepK));
+    mma_step<false, NT>(acc, ws, xs);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][t][i][lane] = acc[t][i];
+  __syncthreads();
+  // thread: 8 of the 16 columns of one row
+  for (int q = tid; q < 2 * M; q += 64 * kSkWaves) {
+    const int m = q >> 1, c0 = 8 * (q & 1);
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = c0 + k;
+      v[k] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kSkWaves; ++g) v[k] += red[g][m >> 4][c & 3][16 * (c >> 2) + (m & 15)];
+    }
+    finish8(epi, v, m, n0 + c0, N);
+  }
+}
+
+// ---------------------------------------------------------------- dz and dbias
+// dz = dout act'(z) in bf16 with rows of pitch elements (zeros past N), and
+// fp32 column sums of the unrounded dz over the block's rows: `part`
+// [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
+template <bool kF32>
+__global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const uint16_t* __restrict__ z, int64_t M,
+                                            int64_t N, int64_t pitch, int32_t act, int32_t ct, int64_t rows_per,
+                                            uint16_t* __restrict__ dz, float* __restrict__ part) {
+  __shared__ float sum[256][8];
+  const int cg = threadIdx.x % ct, rl = threadIdx.x / ct, rt = 256 / ct;
+  const int64_t j = 8 * ((int64_t)blockIdx.x * ct + cg);
+  const int64_t r0 = (int64_t)blockIdx.y * rows_per;
+  const int64_t r1 = r0 + rows_per < M ? r0 + rows_per : M;
+  const bool wide = N % 8 == 0;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (j < N) {
+    const int n = N - j < 8 ? (int)(N - j) : 8;
+    for (int64_t r = r0 + rl; r < r1; r += rt) {
+      float v[8];
+      const int64_t at = r * N + j;
+      if (wide) {
+        if constexpr (kF32) {
+          const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at);
+          const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at + 4);
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+          const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dout) + at);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] = bf_lo(w[k]);
+            v[2 * k + 1] = bf_hi(w[k]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[k] = 0.0f;
+          if (k < n) v[k] = kF32 ? static_cast<const float*>(dout)[at + k] : bf1(static_cast<const uint16_t*>(dout)[at + k]);
+        }
+      }
+      if (act != MX_ACT_NONE) {
+        if (wide) {
+          const uint4 a = *reinterpret_cast<const uint4*>(z + at);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] *= act_slope(bf_lo(w[k]), act);
+            v[2 * k + 1] *= act_slope(bf_hi(w[k]), act);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < n) v[k] *= act_slope(bf1(z[at + k]), act);
+        }
+      }
+      if (dz)
+        *reinterpret_cast<uint4*>(dz + r * pitch + j) = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                                                   bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += v[k];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[threadIdx.x][k] = s[k];
+  __syncthreads();
+  // one thread per column sums the row lanes in order
+  for (int c = threadIdx.x; c < 8 * ct; c += 256) {
+    const int64_t col = 8 * (int64_t)blockIdx.x * ct + c;
+    if (col >= N) continue;
+    float t = 0.0f;
+    for (int l = 0; l < rt; ++l) t += sum[l * ct + (c >> 3)][c & 7];
+    part[(int64_t)blockIdx.y * N + col] = t;
+  }
+}
+
+// dbias: the blocks' sums in order.
+__global__ void __launch_bounds__(256) k_dbias(const float* __restrict__ part, int32_t blocks, int64_t N,
+                                               float* __restrict__ dbias) {
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= N) return;
+  float t = 0.0f;
+  for (int b = 0; b < blocks; ++b) t += part[b * N + j];
+  dbias[j] = t;
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// Tile and split of a product.
+struct Plan {
+  int tile;              // 256, 128 or 64
+  int32_t splits, split_tiles;
+  int64_t part_bytes;
+};
+
+Plan plan_product(int64_t I, int64_t J, int64_t C) {
+  Plan pl;
+  auto tiles = [&](int64_t b) { return ((I + b - 1) / b) * ((J + b - 1) / b); };
+  pl.tile = tiles(256) >= kCus / 2 && J >= 192 && I >= 192 ? 256 : (J > 64 && I > 64 && tiles(128) >= kCus / 4 ? 128 : 64);
+  const int64_t t = tiles(pl.tile), all = (C + kC - 1) / kC;
+  int64_t s = t >= kCus || t == 0 ? 1 : (2 * kCus) / t;
+  if (s > all / 8) s = all / 8;     // at least 8 tiles of 64 per split
+  if (s > 64) s = 64;
+  if (s < 1) s = 1;
+  // an empty contraction still has one split, which writes zeros
+  pl.split_tiles = (int32_t)(all ? (all + s - 1) / s : 1);
+  pl.splits = (int32_t)(all ? (all + pl.split_tiles - 1) / pl.split_tiles : 1);
+  pl.part_bytes = pl.splits > 1 ? up(4 * I * J * pl.splits, 256) : 0;
+  return pl;
+}
+
+template <bool kARows, bool kBRows>
+int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int64_t C, const Epi& epi, float* part,
+                   hipStream_t st) {
+  const Plan pl = plan_product(I, J, C);
+  Product p;
+  p.a = a;
+  p.b = b;
+  p.I = I;
+  p.J = J;
+  p.C = C;
+  p.tiles_i = (int32_t)((I + pl.tile - 1) / pl.tile);
+  p.tiles_j = (int32_t)((J + pl.tile - 1) / pl.tile);
+  p.splits = pl.splits;
+  p.split_tiles = pl.split_tiles;
+  p.part = part;
+  p.epi = epi;
+  const int64_t total = (int64_t)p.tiles_i * p.tiles_j * p.splits;
+  if (total >= (1ll << 30)) return MX_EUNSUPPORTED;
+  const unsigned grid = (unsigned)(((total + kXcds - 1) / kXcds) * kXcds);
+  if (pl.tile == 256) hipLaunchKernelGGL((k_product<256, 256, 2, 4, 2, kARows, kBRows>), dim3(grid), dim3(512), 0, st, p);
+  else if (pl.tile == 128) hipLaunchKernelGGL((k_product<128, 128, 2, 2, 2, kARows, kBRows>), dim3(grid), dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((k_product<64, 64, 2, 2, 4, kARows, kBRows>), dim3(grid), dim3(256), 0, st, p);
+  if (p.splits > 1) {
+    const int64_t n = I * ((J + 7) / 8);
+    hipLaunchKernelGGL(k_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, p.splits, I, J, epi);
+  }
+  return launch_status();
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// Sizes the 32-bit offsets of the tiles allow (256 rows of an operand below 2^31 bytes).
+bool too_large(int64_t rows, int64_t n, int64_t k) {
+  return k >= (1 << 21) || n >= (1 << 21) || rows >= (1ll << 31);
+}
+
+// Sections of the backward's workspace.
+struct BwdSpace {
+  int64_t pitch, dz, sums, part;   // dz row pitch; byte sizes
+  int32_t ct, blocks;              // column groups per block, row blocks of k_dz
+  int64_t rows_per;
+};
+
+BwdSpace bwd_space(int64_t M, int64_t N, int64_t K) {
+  BwdSpace s;
+  s.pitch = up(N, 8);
+  s.dz = up(2 * M * s.pitch, 256);
+  s.ct = 1;
+  while (s.ct < 64 && 8 * s.ct < N) s.ct *= 2;
+  // row blocks: about eight workgroups per CU, at least four rows per thread row
+  const int64_t gx = (N + 8 * s.ct - 1) / (8 * s.ct);
+  int64_t want = 8 * kCus / gx;
+  const int64_t most = (M + 4 * (256 / s.ct) - 1) / (4 * (256 / s.ct));
+  want = want < 1 ? 1 : (want > most ? most : want);
+  if (want > 256) want = 256;
+  s.rows_per = want ? up((M + want - 1) / want, 256 / s.ct) : 1;
+  s.blocks = (int32_t)((M + s.rows_per - 1) / s.rows_per);
+  s.sums = up(4 * (int64_t)s.blocks * N, 256);
+  const int64_t a = plan_product(M, K, N).part_bytes, b = plan_product(N, K, M).part_bytes;
+  s.part = a > b ? a : b;
+  return s;
+}
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" size_t mx_bf16_linear_workspace_size(int64_t rows, int64_t n, int64_t k) {
+  if (rows <= kSkinny || n <= 0 || k <= 0 || too_large(rows, n, k)) return 0;
+  return (size_t)plan_product(rows, n, k).part_bytes;
+}
+
+extern "C" int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual,
+                              int64_t rows, int64_t n, int64_t k, int32_t act, uint16_t* z, void* out,
+                              int32_t out_dtype, void* workspace, size_t workspace_bytes, mx_stream_t stream) {
+  if (rows < 0 || n <= 0 || k <= 0 || k % 32) return MX_EINVAL;
+  if (!x || !w || !out || act < MX_ACT_NONE || act > MX_ACT_SILU) return MX_EINVAL;
+  if (out_dtype != MX_OUT_BF16 && out_dtype != MX_OUT_F32) return MX_EINVAL;
+  if (misaligned(x) || misaligned(w) || misaligned(residual) || misaligned(z) || misaligned(out)) return MX_EINVAL;
+  if (((uintptr_t)bias & 3) || misaligned(workspace)) return MX_EINVAL;
+  if (too_large(rows, n, k)) return MX_EUNSUPPORTED;
+  if (rows == 0) return MX_OK;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  Epi epi;
+  epi.bias = bias;
+  epi.residual = residual;
+  epi.z = z;
+  epi.out = out;
+  epi.act = act;
+  epi.f32 = out_dtype == MX_OUT_F32;
+  epi.wide = n % 8 == 0;
+  if (rows <= kSkinny) {
+    const dim3 grid((unsigned)((n + 15) / 16)), block(64 * kSkWaves);
+    if (rows <= 16) hipLaunchKernelGGL(k_skinny<1>, grid, block, 0, st, x, w, rows, n, k, epi);
+    else if (rows <= 32) hipLaunchKernelGGL(k_skinny<2>, grid, block, 0, st, x, w, rows, n, k, epi);
+    else hipLaunchKernelGGL(k_skinny<4>, grid, block, 0, st, x, w, rows, n, k, epi);
+    return launch_status();
+  }
+  const int64_t need = plan_product(rows, n, k).part_bytes;
+  if (need && (!workspace || (int64_t)workspace_bytes < need)) return MX_EINVAL;
+  return launch_product<true, true>(Operand{x, k}, Operand{w, k}, rows, n, k, epi, static_cast<float*>(workspace), st);
+}
+
+extern "C" size_t mx_bf16_linear_bwd_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t act) {
+  if (rows <= 0 || n <= 0 || k <= 0 || too_large(rows, n, k) || act < MX_ACT_NONE || act > MX_ACT_SILU) return 0;
+  const BwdSpace s = bwd_space(rows, n, k);
+  return (size_t)(s.dz + s.sums + s.part);
+}
+
+extern "C" int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const uint16_t* z, const uint16_t* x,
+                                  const uint16_t* w, const uint16_t* dx_add, int64_t rows, int64_t n, int64_t k,
+                                  int32_t act, uint16_t* dx, uint16_t* dw, float* dbias, void* workspace,
+                                  size_t workspace_bytes, mx_stream_t stream) {
+  if (rows < 0 || n <= 0 || k <= 0 || k % 32 || act < MX_ACT_NONE || act > MX_ACT_SILU) return MX_EINVAL;
+  if (dout_dtype != MX_OUT_BF16 && dout_dtype != MX_OUT_F32) return MX_EINVAL;
+  if (!dout || (act != MX_ACT_NONE && !z) || (!dx && !dw && !dbias)) return MX_EINVAL;
+  if ((dx && !w) || (dw && !x) || (dx_add && !dx)) return MX_EINVAL;
+  if (misaligned(dout) || misaligned(z) || misaligned(x) || misaligned(w) || misaligned(dx_add) || misaligned(dx) ||
+      misaligned(dw) || ((uintptr_t)dbias & 3) || misaligned(workspace))
+    return MX_EINVAL;
+  if (too_large(rows, n, k)) return MX_EUNSUPPORTED;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const BwdSpace s = bwd_space(rows, n, k);
+  if (rows > 0 && (!workspace || (int64_t)workspace_bytes < s.dz + s.sums + s.part)) return MX_EINVAL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* sums = reinterpret_cast<float*>(ws + s.dz);
+  float* part = reinterpret_cast<float*>(ws + s.dz + s.sums);
+  // dout itself serves as dz where it is bf16, linear and has 16-byte rows
+  const bool same = act == MX_ACT_NONE && dout_dtype == MX_OUT_BF16 && n % 8 == 0;
+  const uint16_t* dzp = same ? static_cast<const uint16_t*>(dout) : reinterpret_cast<uint16_t*>(ws);
+  const int64_t pitch = same ? n : s.pitch;
+  if (rows > 0 && (!same || dbias)) {
+    const dim3 grid((unsigned)((n + 8 * s.ct - 1) / (8 * s.ct)), (unsigned)s.blocks);
+    uint16_t* dz = same ? nullptr : reinterpret_cast<uint16_t*>(ws);
+    float* sp = dbias ? sums : nullptr;
+    if (dout_dtype == MX_OUT_F32)
+      hipLaunchKernelGGL(k_dz<true>, grid, dim3(256), 0, st, dout, z, rows, n, pitch, act, s.ct, s.rows_per, dz, sp);
+    else
+      hipLaunchKernelGGL(k_dz<false>, grid, dim3(256), 0, st, dout, z, rows, n, pitch, act, s.ct, s.rows_per, dz, sp);
+  }
+  if (dbias)
+    hipLaunchKernelGGL(k_dbias, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, sums, rows > 0 ? s.blocks : 0, n,
+                       dbias);
+  Epi epi;
+  epi.bias = nullptr;
+  epi.residual = nullptr;
+  epi.z = nullptr;
+  epi.act = MX_ACT_NONE;
+  epi.f32 = false;
+  epi.wide = true;   // K % 32 == 0
+  if (dx && rows > 0) {
+    epi.out = dx;
+    epi.residual = dx_add;
+    const int rc = launch_product<true, false>(Operand{dzp, pitch}, Operand{w, k}, rows, k, n, epi, part, st);
+    if (rc != MX_OK) return rc;
+  }
+  if (dw) {
+    epi.out = dw;
+    epi.residual = nullptr;
+    const int rc = launch_product<false, false>(Operand{dzp, pitch}, Operand{x, k}, n, k, rows, epi, part, st);
+    if (rc != MX_OK) return rc;
+  }
+  return launch_status();
+}
