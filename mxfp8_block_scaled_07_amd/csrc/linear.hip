@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __rest
     load_w<false>(ws, wr, (uint32_t)r, (uint32_t)K, (uint32_t)(s * kStepK), r < rows);
 #pragma unroll
     for (int t = 0; t < NT; ++t) load_x(xs[t], xr, off[t], (uint32_t)K, (uint32_t)(s * kStepK));
-    mma_step<false, NT>(acc, ws, xs);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma_step<false>(acc[t], ws, xs[t]);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)

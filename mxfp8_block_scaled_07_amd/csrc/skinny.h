@@ -56,32 +56,35 @@ struct WRows {
   uint32_t panel;                // bytes between scale panels
 };
 
-// row: the lane's weight row; k0 a multiple of 128.  Blocks past K read as zero.
+// row: the lane's weight row; k0 a multiple of 128.  Blocks past K read as
+// zero (a whole step past K keeps the scalar offset inside the buffer).
 template <bool kMx>
 __device__ __forceinline__ void load_w(WStep<kMx>& w, const WRows<kMx>& m, uint32_t row, uint32_t K, uint32_t k0,
                                        bool row_ok) {
   const uint32_t h = (threadIdx.x & 63) >> 4;
-  const uint32_t k = k0 + 32 * h;
-  const bool ok = row_ok & (k < K);
+  const bool ok = row_ok & (k0 + 32 * h < K);
+  const uint32_t ks = k0 < K ? k0 : 0;
   if constexpr (kMx) {
     const uint32_t off = ok ? row * K + 32 * h : kNoRow;
-    w.q[0] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off, (int)k0, 0);
-    w.q[1] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off + 16, (int)k0, 0);
-    w.s = __builtin_amdgcn_raw_buffer_load_b32(m.s, (int)(ok ? 4 * row : kNoRow), (int)((k0 >> 7) * m.panel), 0);
+    w.q[0] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off, (int)ks, 0);
+    w.q[1] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off + 16, (int)ks, 0);
+    w.s = __builtin_amdgcn_raw_buffer_load_b32(m.s, (int)(ok ? 4 * row : kNoRow), (int)((ks >> 7) * m.panel), 0);
   } else {
     const uint32_t off = ok ? 2 * (row * K + 32 * h) : kNoRow;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w.q[i] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off + 16 * i, (int)(2 * k0), 0);
+      w.q[i] = __builtin_amdgcn_raw_buffer_load_b128(m.q, (int)off + 16 * i, (int)(2 * ks), 0);
   }
 }
 
 // off: byte offset of the lane's token row, or kNoRow for a lane without one.
 __device__ __forceinline__ void load_x(XStep& x, __amdgpu_buffer_rsrc_t m, uint32_t off, uint32_t K, uint32_t k0) {
   const uint32_t h = (threadIdx.x & 63) >> 4;
-  const uint32_t o = k0 + 32 * h < K ? off + 64 * h : kNoRow;
+  const bool ok = (k0 + 32 * h < K) & (off != kNoRow);
+  const uint32_t o = ok ? off + 64 * h : kNoRow;
+  const uint32_t ks = k0 < K ? k0 : 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x.q[i] = __builtin_amdgcn_raw_buffer_load_b128(m, (int)o + 16 * i, (int)(2 * k0), 0);
+  for (int i = 0; i < 4; ++i) x.q[i] = __builtin_amdgcn_raw_buffer_load_b128(m, (int)o + 16 * i, (int)(2 * ks), 0);
 }
 
 // The lane's 8 weights of instruction i as bf16.
@@ -107,16 +110,13 @@ __device__ __forceinline__ float step_scale(const WStep<kMx>& w) {
   return 1.0f;
 }
 
-template <bool kMx, int NT>
-__device__ __forceinline__ void mma_step(v4f_s (&acc)[NT], const WStep<kMx>& w, const XStep (&x)[NT]) {
+template <bool kMx>
+__device__ __forceinline__ void mma_step(v4f_s& acc, const WStep<kMx>& w, const XStep& x) {
   const float scale = step_scale<kMx>(w);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const v8bf_s a = weights8<kMx>(w, i, scale);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(v8bf_s, x[t].q[i]), acc[t], 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<kMx>(w, i, scale), __builtin_bit_cast(v8bf_s, x.q[i]), acc,
+                                                  0, 0, 0);
 }
 
 }  // namespace mx
