@@ -191,6 +191,15 @@ __device__ __forceinline__ void dma16(const v4u& r, uint32_t lds, uint32_t voff,
 
 constexpr int waitcnt_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
 
+// A barrier that waits for nothing by itself (a fence's wait would include
+// loads still in flight); nothing may be moved across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Swizzles of 16-byte chunks.  Rows: 128-byte LDS rows, chunk ^ (r >> 1) & 7,
 // so the 16-byte reads of 32 consecutive rows spread over all banks.  Columns:
 // an LDS row is one c with R columns; a transposing read takes 64 bytes of 4
@@ -344,46 +353,59 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
 
+  // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.
 #pragma unroll
-  for (int s = 0; s < kSlots - 1; ++s)
+  for (int s = 0; s < kSlots; ++s)
     if (t0 + s < t1) {
       la.issue(t0 + s, p.C, base + s * kSlot);
       lb.issue(t0 + s, p.C, base + s * kSlot + kABytes);
     }
+  if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
+  else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  lds_barrier();
+
+  // Fragments are read one 16-c part ahead of their products, across tiles:
+  // the barrier of a tile stands before its last part's products.
+  v8bf_s a[2][FM], b[2][FN];
+  auto read = [&](int q, const uint8_t* tile, int kk) {
+#pragma unroll
+    for (int n = 0; n < FN; ++n) b[q][n] = fb.read(tile + kABytes, wn * TN + 32 * n, kk);
+#pragma unroll
+    for (int m = 0; m < FM; ++m) a[q][m] = fa.read(tile, wm * TM + 32 * m, kk);
+  };
+  auto products = [&](int q) {
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[q][n], a[q][m], acc[m][n], 0, 0, 0);
+  };
   int slot = 0;
+  if (t0 < t1) read(0, lds, 0);
   for (int64_t t = t0; t < t1; ++t) {
-    // this wave's loads of tile t are done (the kSlots - 2 tiles after it may
-    // be in flight; near the end fewer are, so everything is waited for) ...
-    if (t + kSlots - 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 2)));
+    const uint8_t* tile = lds + slot * kSlot;
+    const int next = slot + 1 == kSlots ? 0 : slot + 1;
+    read(1, tile, 1);
+    products(0);
+    read(0, tile, 2);
+    products(1);
+    read(1, tile, 3);
+    products(0);
+    // this wave has read its share of the slot, and its loads of tile t + 1
+    // are done (the kSlots - 2 tiles after it may be in flight; near the end
+    // fewer are, so everything is waited for) ...
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+    if (t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 2)));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    asm volatile("" ::: "memory");
-    // ... and after the barrier every wave's, and every wave has read tile t - 1
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const int64_t nt = t + kSlots - 1;
-    if (nt < t1) {
-      const int ns = slot == 0 ? kSlots - 1 : slot - 1;   // the slot of tile t - 1
-      la.issue(nt, p.C, base + ns * kSlot);
-      lb.issue(nt, p.C, base + ns * kSlot + kABytes);
+    // ... and after the barrier every wave's: the slot takes tile t + kSlots
+    lds_barrier();
+    if (t + kSlots < t1) {
+      la.issue(t + kSlots, p.C, base + slot * kSlot);
+      lb.issue(t + kSlots, p.C, base + slot * kSlot + kABytes);
     }
-    const uint8_t* A = lds + slot * kSlot;
-    const uint8_t* B = A + kABytes;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      v8bf_s a[FM], b[FN];
-#pragma unroll
-      for (int n = 0; n < FN; ++n) b[n] = fb.read(B, wn * TN + 32 * n, kk);
-#pragma unroll
-      for (int m = 0; m < FM; ++m) a[m] = fa.read(A, wm * TM + 32 * m, kk);
-#pragma unroll
-      for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[n], a[m], acc[m][n], 0, 0, 0);
-    }
-    slot = slot + 1 == kSlots ? 0 : slot + 1;
-    // this wave's LDS reads are done before it reaches the next barrier
-    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));
-    asm volatile("" ::: "memory");
+    if (t + 1 < t1) read(0, lds + next * kSlot, 0);
+    products(1);
+    slot = next;
   }
   __syncthreads();
 
@@ -589,14 +611,27 @@ __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const
   }
 }
 
-// dbias: the blocks' sums in order.
+// dbias from the blocks' sums: 16 columns per workgroup, 16 threads to a
+// column, each a run of blocks in order, then the runs in order (one thread
+// per column takes 16 to 31 us for 256 blocks, their latencies in a row).
 __global__ void __launch_bounds__(256) k_dbias(const float* __restrict__ part, int32_t blocks, int64_t N,
                                                float* __restrict__ dbias) {
-  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= N) return;
+  __shared__ float sum[16][17];
+  const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int64_t j = 16 * (int64_t)blockIdx.x + c;
+  const int per = (blocks + 15) / 16;
+  const int b1 = (run + 1) * per < blocks ? (run + 1) * per : blocks;
   float t = 0.0f;
-  for (int b = 0; b < blocks; ++b) t += part[b * N + j];
-  dbias[j] = t;
+  if (j < N) {
+#pragma unroll 8
+    for (int b = run * per; b < b1; ++b) t += part[b * N + j];
+  }
+  sum[run][c] = t;
+  __syncthreads();
+  if (run == 0 && j < N) {
+    for (int r = 1; r < 16; ++r) t += sum[r][c];
+    dbias[j] = t;
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -767,7 +802,7 @@ extern "C" int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const ui
       hipLaunchKernelGGL(k_dz<false>, grid, dim3(256), 0, st, dout, z, rows, n, pitch, act, s.ct, s.rows_per, dz, sp);
   }
   if (dbias)
-    hipLaunchKernelGGL(k_dbias, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, sums, rows > 0 ? s.blocks : 0, n,
+    hipLaunchKernelGGL(k_dbias, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, st, sums, rows > 0 ? s.blocks : 0, n,
                        dbias);
   Epi epi;
   epi.bias = nullptr;
