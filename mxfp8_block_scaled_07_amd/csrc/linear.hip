@@ -31,7 +31,6 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 
 constexpr int kCus = 256;                    // MI355X
 constexpr int kXcds = 8;
-constexpr int kC = 64;                       // contraction elements of an LDS tile
 constexpr uint32_t kOob = 0x80000000u;       // an offset that reads as zero
 constexpr int kSkinny = 64;                  // most rows of the streaming form
 
@@ -98,62 +97,47 @@ struct Epi {
   bool wide;                 // J % 8 == 0: 16-byte accesses
 };
 
-// 8 consecutive columns of one row from their fp32 sums.
-__device__ __forceinline__ void finish8(const Epi& e, float (&v)[8], int64_t i, int64_t j, int64_t J) {
-  if (j >= J) return;
-  const int n = J - j < 8 ? (int)(J - j) : 8;
-  if (e.bias) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) v[k] += e.bias[j + k];
-  }
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+}
+
+// z of 8 consecutive columns of one row (bias added) to the results; res: the
+// residual's 8 values where accesses are wide.
+__device__ __forceinline__ void finish8(const Epi& e, int act, float (&v)[8], const uint4& res, int64_t i, int64_t j,
+                                        int64_t J) {
   const int64_t at = i * J + j;
-  if (e.z) {
-    if (e.wide) {
-      *reinterpret_cast<uint4*>(e.z + at) =
-          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-    } else {
-      for (int k = 0; k < n; ++k) e.z[at + k] = (uint16_t)bf16x2_rne(v[k], v[k]);
-    }
-  }
-  if (e.act != MX_ACT_NONE) {
+  if (e.wide) {
+    if (e.z) *reinterpret_cast<uint4*>(e.z + at) = pack8(v);
+    if (act != MX_ACT_NONE) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], e.act);
-  }
-  if (e.residual) {
-    if (e.wide) {
-      const uint4 r = *reinterpret_cast<const uint4*>(e.residual + at);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], act);
+    }
+    if (e.residual) {
+      const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[2 * k] += bf_lo(w[k]);
         v[2 * k + 1] += bf_hi(w[k]);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) v[k] += bf1(e.residual[at + k]);
     }
-  }
-  if (e.f32) {
-    float* o = static_cast<float*>(e.out) + at;
-    if (e.wide) {
+    if (e.f32) {
+      float* o = static_cast<float*>(e.out) + at;
       *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) o[k] = v[k];
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at) = pack8(v);
     }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(e.out) + at;
-    if (e.wide) {
-      *reinterpret_cast<uint4*>(o) =
-          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-    } else {
+    return;
+  }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) o[k] = (uint16_t)bf16x2_rne(v[k], v[k]);
+  for (int k = 0; k < 8; ++k) {
+    if (j + k < J) {
+      float x = v[k];
+      if (e.z) e.z[at + k] = (uint16_t)bf16x2_rne(x, x);
+      x = act_value(x, act);
+      if (e.residual) x += bf1(e.residual[at + k]);
+      if (e.f32) static_cast<float*>(e.out)[at + k] = x;
+      else static_cast<uint16_t*>(e.out)[at + k] = (uint16_t)bf16x2_rne(x, x);
     }
   }
 }
@@ -167,11 +151,23 @@ struct Operand {
 struct Product {
   Operand a, b;
   int64_t I, J, C;       // rows and columns of the result, contraction length
-  int32_t tiles_i, tiles_j, splits;
-  int32_t split_tiles;   // LDS tiles (64 c) per split
-  float* part;           // splits > 1: fp32 partial sums [splits, I, J]
+  int32_t tiles_i, tiles_j;
+  int32_t full;          // tiles computed whole; the others are split over the contraction
+  int32_t splits;
+  int32_t split_c;       // contraction elements per split (a multiple of 64)
+  float* part;           // fp32 sums of the split tiles [splits, tiles - full, BM x BN in register order]
   Epi epi;
 };
+
+// The q-th tile: bands of 8 row tiles, so that tiles that run together share
+// operands in an XCD's L2.
+__device__ __forceinline__ void tile_at(const Product& p, int32_t q, int bm, int bn, int64_t& i0, int64_t& j0) {
+  constexpr int kBand = 8;
+  const int32_t band = q / (kBand * p.tiles_j), in = q % (kBand * p.tiles_j);
+  const int32_t rows = p.tiles_i - band * kBand < kBand ? p.tiles_i - band * kBand : kBand;
+  i0 = (int64_t)(band * kBand + in % rows) * bm;
+  j0 = (int64_t)(in / rows) * bn;
+}
 
 __device__ __forceinline__ v4u rsrc(const void* base, int64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -204,15 +200,16 @@ __device__ __forceinline__ void lds_barrier() {
 // so the 16-byte reads of 32 consecutive rows spread over all banks.  Columns:
 // an LDS row is one c with R columns; a transposing read takes 64 bytes of 4
 // consecutive c at once, which the swizzle moves to different 64-byte banks.
-__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
+template <int kC>
+__device__ __forceinline__ int row_swizzle(int r) { return kC == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
 template <int R>
 __device__ __forceinline__ int col_swizzle(int c) { return R >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2; }
 
 // The LDS-direct loads of one operand tile: kLoads per wave and 64-c tile.
-template <bool kRows, int R, int kNw>
+template <bool kRows, int R, int kNw, int kC>
 struct TileLoads {
-  static constexpr int kLoads = R / 8 / kNw;
-  static_assert(R % (8 * kNw) == 0, "whole loads per wave");
+  static constexpr int kLoads = R * kC * 2 / 1024 / kNw;
+  static_assert(R * kC * 2 % (1024 * kNw) == 0, "whole loads per wave");
   uint32_t voff[kLoads];
   int32_t kc;   // rows: the lane's first c in a tile
   const uint8_t* base;
@@ -230,8 +227,9 @@ struct TileLoads {
       kc = 0;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = 8 * (w + kNw * i) + (lane >> 3);
-        const int ch = (lane & 7) ^ row_swizzle(r);
+        constexpr int kPer = kC / 8;         // chunks per LDS row
+        const int r = 64 / kPer * (w + kNw * i) + lane / kPer;
+        const int ch = (lane % kPer) ^ row_swizzle<kC>(r);
         kc = 8 * ch;   // the same for every i (kNw is even)
         voff[i] = (uint32_t)r * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch;
       }
@@ -252,32 +250,40 @@ struct TileLoads {
     }
   }
 
-  // tile: index of the 64-c tile
-  __device__ void issue(int64_t tile, int64_t C, uint32_t lds) const {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // The loads of a tile: prepare() once per tile, then load(i).
+  struct Tile {
+    v4u r;
+    uint32_t soff;
+    bool ok;
+  };
+  __device__ Tile prepare(int64_t tile, int64_t C) const {
+    Tile t;
     if constexpr (kRows) {
-      const v4u r = rsrc(base, bytes);
-      const uint32_t soff = (uint32_t)(tile * kC * 2);
-      const bool ok = tile * kC + kc < C;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) dma16(r, lds + 1024u * (uint32_t)(w + kNw * i), ok ? voff[i] : kOob, soff);
+      t.r = rsrc(base, bytes);
+      t.soff = (uint32_t)(tile * kC * 2);
+      t.ok = tile * kC + kc < C;
     } else {
-      const v4u r = rsrc(base + tile * step, bytes - tile * step);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) dma16(r, lds + 1024u * (uint32_t)(w + kNw * i), voff[i], 0);
+      t.r = rsrc(base + tile * step, bytes - tile * step);
+      t.soff = 0;
+      t.ok = true;
     }
+    return t;
+  }
+  __device__ void load(const Tile& t, int i, uint32_t lds) const {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    dma16(t.r, lds + 1024u * (uint32_t)(w + kNw * i), kRows && !t.ok ? kOob : voff[i], t.soff);
   }
 };
 
 // Lane offsets of a 32 (i) x 16 (c) fragment; kk = 0..3 in a 64-c tile.
-template <bool kRows, int R>
+template <bool kRows, int R, int kC>
 struct FragAt {
   int row, sw, lo, hi;
   __device__ void init() {
     const int lane = threadIdx.x & 63;
     if constexpr (kRows) {
-      row = (lane & 31) * 128;
-      sw = row_swizzle(lane & 31);
+      row = (lane & 31) * (2 * kC);
+      sw = row_swizzle<kC>(lane & 31);
       lo = lane >> 5;
     } else {
       const int l = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
@@ -291,7 +297,7 @@ struct FragAt {
   // i0: the fragment's first row inside the tile, a multiple of 32
   __device__ v8bf_s read(const uint8_t* tile, int i0, int kk) const {
     if constexpr (kRows) {
-      return *reinterpret_cast<const v8bf_s*>(tile + i0 * 128 + row + 16 * ((2 * kk + lo) ^ sw));
+      return *reinterpret_cast<const v8bf_s*>(tile + i0 * (2 * kC) + row + 16 * ((2 * kk + lo) ^ sw));
     } else {
       const uint8_t* p = tile + kk * 16 * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
       // c .. c + 3 and c + 4 .. c + 7: the swizzle depends on c & 3 only
@@ -302,46 +308,108 @@ struct FragAt {
   }
 };
 
-// BM x BN result tile, kWm x kWn waves, kSlots LDS tiles in flight.
-template <int BM, int BN, int kWm, int kWn, int kSlots, bool kARows, bool kBRows>
+// Epilogue of a wave's TM x TN sums through its LDS slice: the accumulators
+// hold 4 consecutive columns of one row per lane (32 rows of W fp32 columns
+// are staged at a time), rows of 8 columns per lane go out.  The residual of the next 32 rows is fetched while these are
+// finished: read where it is added, its latency costs more than the products
+// of a 256 x 256 tile's last quarter.
+template <int TN>
+constexpr int kStageCols = TN < 64 ? TN : 64;
+template <int TN>
+constexpr int kStageBytes = 32 * (kStageCols<TN> * 4 + 16);
+
+template <int TM, int TN, int kAct>
+__device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
+                                         int64_t j0, int64_t I, int64_t J) {
+  constexpr int FM = TM / 32, FN = TN / 32, W = kStageCols<TN>, kPitch = W * 4 + 16;
+  constexpr int kLpr = W / 8, kRpp = 64 / kLpr, kIt = 32 / kRpp;   // lanes per row, rows per pass, passes
+  const int lane = threadIdx.x & 63;
+  const int wr = lane & 31, h = lane >> 5;
+  const int rr = lane / kLpr, c8 = lane % kLpr;
+#pragma unroll
+  for (int n0 = 0; n0 < FN; n0 += W / 32) {
+    const int64_t j = j0 + 32 * n0 + 8 * c8;
+    float bias[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bias[k] = e.bias && j + k < J ? e.bias[j + k] : 0.0f;
+    uint4 res[2][kIt];
+    auto fetch = [&](int m) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int64_t i = i0 + 32 * m + kRpp * it + rr;
+        res[m & 1][it] = make_uint4(0, 0, 0, 0);
+        if (e.residual && e.wide && i < I && j < J)
+          res[m & 1][it] = *reinterpret_cast<const uint4*>(e.residual + i * J + j);
+      }
+    };
+    fetch(0);
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      if (m + 1 < FM) fetch(m + 1);
+#pragma unroll
+      for (int n = 0; n < W / 32; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(slice + wr * kPitch + (32 * n + 8 * g + 4 * h) * 4) =
+              make_float4(acc[m][n0 + n][4 * g], acc[m][n0 + n][4 * g + 1], acc[m][n0 + n][4 * g + 2],
+                          acc[m][n0 + n][4 * g + 3]);
+      // exchanged between the wave's lanes, whose LDS accesses run in order
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int row = kRpp * it + rr;
+        const float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8);
+        const float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8 + 16);
+        const int64_t i = i0 + 32 * m + row;
+        if (i < I && j < J) {
+          float v[8] = {x.x + bias[0], x.y + bias[1], x.z + bias[2], x.w + bias[3],
+                        y.x + bias[4], y.y + bias[5], y.z + bias[6], y.w + bias[7]};
+          finish8(e, kAct, v, res[m & 1][it], i, j, J);
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+}
+
+// BM x BN result tile, kWm x kWn waves, kSlots LDS tiles of kC contraction
+// elements in flight.
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct>
 __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   constexpr int kNw = kWm * kWn;
   constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
   constexpr int kABytes = BM * kC * 2, kSlot = (BM + BN) * kC * 2;
-  // the epilogue's slice of a wave: 32 rows of W fp32 columns
-  constexpr int W = TN < 64 ? TN : 64, kPitch = W * 4 + 16;
-  constexpr int kLds = kSlots * kSlot > kNw * 32 * kPitch ? kSlots * kSlot : kNw * 32 * kPitch;
+  constexpr int kLds = kSlots * kSlot > kNw * kStageBytes<TN> ? kSlots * kSlot : kNw * kStageBytes<TN>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / kWn, wn = wave % kWn;
 
-  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous range of tiles,
-  // walked in bands of 8 row tiles, so that neighbours share operands in its L2.
-  const int64_t total = (int64_t)p.tiles_i * p.tiles_j * p.splits;
-  const int64_t per = (total + kXcds - 1) / kXcds;
-  const int64_t L = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (blockIdx.x / kXcds >= per || L >= total) return;
-  const int32_t tiles = p.tiles_i * p.tiles_j;
-  const int32_t split = (int32_t)(L / tiles), q = (int32_t)(L % tiles);
-  constexpr int kBand = 8;
-  const int32_t band = q / (kBand * p.tiles_j), in = q % (kBand * p.tiles_j);
-  const int32_t rows_in = p.tiles_i - band * kBand < kBand ? p.tiles_i - band * kBand : kBand;
-  const int64_t i0 = (int64_t)(band * kBand + in % rows_in) * BM;
-  const int64_t j0 = (int64_t)(in / rows_in) * BN;
-
+  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous range of the
+  // whole tiles, then one of the split tiles' parts.
+  const int32_t tiles = p.tiles_i * p.tiles_j, tail = tiles - p.full;
+  const int32_t full8 = (p.full + kXcds - 1) / kXcds * kXcds;
+  const bool whole = (int32_t)blockIdx.x < full8;
+  const int32_t bid = whole ? blockIdx.x : blockIdx.x - full8;
+  const int32_t total = whole ? p.full : tail * p.splits;
+  const int32_t per = (total + kXcds - 1) / kXcds;
+  const int32_t L = (bid % kXcds) * per + bid / kXcds;
+  if (bid / kXcds >= per || L >= total) return;
+  const int32_t split = whole ? 0 : L / tail;
+  int64_t i0, j0;
+  tile_at(p, whole ? L : p.full + L % tail, BM, BN, i0, j0);
   const int64_t all = (p.C + kC - 1) / kC;
-  const int64_t t0 = (int64_t)split * p.split_tiles;
-  const int64_t t1 = t0 + p.split_tiles < all ? t0 + p.split_tiles : all;
+  const int64_t t0 = whole ? 0 : (int64_t)split * (p.split_c / kC);
+  const int64_t t1 = whole || t0 + p.split_c / kC > all ? all : t0 + p.split_c / kC;
 
-  TileLoads<kARows, BM, kNw> la;
-  TileLoads<kBRows, BN, kNw> lb;
+  TileLoads<kARows, BM, kNw, kC> la;
+  TileLoads<kBRows, BN, kNw, kC> lb;
   la.init(p.a, i0, p.I, p.C);
   lb.init(p.b, j0, p.J, p.C);
-  constexpr int kLoads = TileLoads<kARows, BM, kNw>::kLoads + TileLoads<kBRows, BN, kNw>::kLoads;
+  constexpr int kLoads = TileLoads<kARows, BM, kNw, kC>::kLoads + TileLoads<kBRows, BN, kNw, kC>::kLoads;
   const uint32_t base = (uint32_t)(uintptr_t)(const lds_void*)lds;
-  FragAt<kARows, BM> fa;
-  FragAt<kBRows, BN> fb;
+  FragAt<kARows, BM, kC> fa;
+  FragAt<kBRows, BN, kC> fb;
   fa.init();
   fb.init();
 
@@ -354,43 +422,68 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
       for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
 
   // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.
+  constexpr int kLa = decltype(la)::kLoads;
+  typename decltype(la)::Tile ta;
+  typename decltype(lb)::Tile tb;
+  uint32_t dst = 0;
+  auto load = [&](int i) {   // load i of the tile in hand
+    if (i < kLa) la.load(ta, i, dst);
+    else lb.load(tb, i - kLa, dst + kABytes);
+  };
+  auto hand = [&](int64_t t, int s) {
+    ta = la.prepare(t, p.C);
+    tb = lb.prepare(t, p.C);
+    dst = base + (uint32_t)s * kSlot;
+  };
 #pragma unroll
   for (int s = 0; s < kSlots; ++s)
     if (t0 + s < t1) {
-      la.issue(t0 + s, p.C, base + s * kSlot);
-      lb.issue(t0 + s, p.C, base + s * kSlot + kABytes);
+      hand(t0 + s, s);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i);
     }
   if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
   else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   lds_barrier();
 
-  // Fragments are read one 16-c part ahead of their products, across tiles:
-  // the barrier of a tile stands before its last part's products.
+  // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
+  // are read during the part before it, and the loads into the slot that the
+  // last tile left are spread over a tile's parts, all placed between the
+  // products: a burst of either stalls the products behind it.
+  constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
+  // with two slots a tile has one tile's time to arrive: its loads all go into the first part
+  constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
   v8bf_s a[2][FM], b[2][FN];
-  auto read = [&](int q, const uint8_t* tile, int kk) {
+  // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
+  auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
 #pragma unroll
-    for (int n = 0; n < FN; ++n) b[q][n] = fb.read(tile + kABytes, wn * TN + 32 * n, kk);
+    for (int i = 0; i < kMfma; ++i) {
+      const int m = i / FN, n = i % FN;
+      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[q][n], a[q][m], acc[m][n], 0, 0, 0);
 #pragma unroll
-    for (int m = 0; m < FM; ++m) a[q][m] = fa.read(tile, wm * TM + 32 * m, kk);
+      for (int f = i * kFrags / kMfma; f < (i + 1) * kFrags / kMfma; ++f) {
+        if (f < FN) b[1 - q][f] = fb.read(tile + kABytes, wn * TN + 32 * f, kk);
+        else a[1 - q][f - FN] = fa.read(tile, wm * TM + 32 * (f - FN), kk);
+      }
+      if (fill) {
+#pragma unroll
+        for (int l = i * kPerPart / kMfma; l < (i + 1) * kPerPart / kMfma; ++l)
+          if (first + l < kLoads) load(first + l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  auto products = [&](int q) {
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
+  for (int n = 0; n < FN; ++n) b[0][n] = fb.read(lds + kABytes, wn * TN + 32 * n, 0);
 #pragma unroll
-      for (int n = 0; n < FN; ++n)
-        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[q][n], a[q][m], acc[m][n], 0, 0, 0);
-  };
+  for (int m = 0; m < FM; ++m) a[0][m] = fa.read(lds, wm * TM + 32 * m, 0);
   int slot = 0;
-  if (t0 < t1) read(0, lds, 0);
+  bool fill = false;   // whether the tile in hand is loaded
   for (int64_t t = t0; t < t1; ++t) {
     const uint8_t* tile = lds + slot * kSlot;
     const int next = slot + 1 == kSlots ? 0 : slot + 1;
-    read(1, tile, 1);
-    products(0);
-    read(0, tile, 2);
-    products(1);
-    read(1, tile, 3);
-    products(0);
+#pragma unroll
+    for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, kk, fill, kk * kPerPart);
     // this wave has read its share of the slot, and its loads of tile t + 1
     // are done (the kSlots - 2 tiles after it may be in flight; near the end
     // fewer are, so everything is waited for) ...
@@ -399,84 +492,63 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     // ... and after the barrier every wave's: the slot takes tile t + kSlots
     lds_barrier();
-    if (t + kSlots < t1) {
-      la.issue(t + kSlots, p.C, base + slot * kSlot);
-      lb.issue(t + kSlots, p.C, base + slot * kSlot + kABytes);
-    }
-    if (t + 1 < t1) read(0, lds + next * kSlot, 0);
-    products(1);
+    fill = t + kSlots < t1;
+    hand(t + kSlots, slot);
+    // (after the last tile this reads an old slot, which is not used)
+    part(1, lds + next * kSlot, 0, fill, 0);
     slot = next;
   }
   __syncthreads();
 
-  // Epilogue through LDS (a wave's own slice): the accumulators hold 4
-  // consecutive columns of one row per lane; rows of 8 columns per lane go out.
-  uint8_t* slice = lds + wave * 32 * kPitch;
-  const int wr = lane & 31, h = lane >> 5;
-  constexpr int kLpr = W / 8, kRpp = 64 / kLpr;   // lanes per row, rows per pass
-  const int rr = lane / kLpr, c8 = lane % kLpr;
+  if (!whole) {
+    float4* o = reinterpret_cast<float4*>(p.part) + (int64_t)L * (BM * BN / 4) + wave * (TM * TN / 4) + lane;
 #pragma unroll
-  for (int m = 0; m < FM; ++m) {
+    for (int m = 0; m < FM; ++m)
 #pragma unroll
-    for (int n0 = 0; n0 < FN; n0 += W / 32) {
-#pragma unroll
-      for (int n = 0; n < W / 32; ++n)
+      for (int n = 0; n < FN; ++n)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<float4*>(slice + wr * kPitch + (32 * n + 8 * g + 4 * h) * 4) =
-              make_float4(acc[m][n0 + n][4 * g], acc[m][n0 + n][4 * g + 1], acc[m][n0 + n][4 * g + 2],
-                          acc[m][n0 + n][4 * g + 3]);
-      // exchanged between the wave's lanes, whose LDS accesses run in order
-      asm volatile("" ::: "memory");
-#pragma unroll 1
-      for (int it = 0; it < 32 / kRpp; ++it) {
-        const int row = kRpp * it + rr;
-        const float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8);
-        const float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8 + 16);
-        const int64_t i = i0 + wm * TM + 32 * m + row, j = j0 + wn * TN + 32 * n0 + 8 * c8;
-        if (i < p.I && j < p.J) {
-          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          if (p.splits > 1) {
-            float* o = p.part + ((int64_t)split * p.I + i) * p.J + j;
-            if (p.epi.wide) {
-              *reinterpret_cast<float4*>(o) = x;
-              *reinterpret_cast<float4*>(o + 4) = y;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (j + k < p.J) o[k] = v[k];
-            }
-          } else {
-            finish8(p.epi, v, i, j, p.J);
-          }
-        }
-      }
-      asm volatile("" ::: "memory");
-    }
+          o[((m * FN + n) * 4 + g) * 64] =
+              make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
+    return;
   }
+  epilogue<TM, TN, kAct>(p.epi, acc, lds + wave * kStageBytes<TN>, i0 + wm * TM, j0 + wn * TN, p.I, p.J);
 }
 
-// The partial sums of a split contraction, in order, then the epilogue.
-__global__ void __launch_bounds__(256) k_join(const float* __restrict__ part, int32_t splits, int64_t I, int64_t J,
-                                              Epi epi) {
-  const int64_t groups = (J + 7) / 8;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= I * groups) return;
-  const int64_t i = at / groups, j = 8 * (at - i * groups);
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) {
-    const float* p = part + ((int64_t)s * I + i) * J + j;
-    if (epi.wide) {
-      const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-    } else {
+// The split tiles: one wave per wave's share of a tile adds its partial sums
+// in the splits' order, then the epilogue.
+template <int BM, int BN, int kWm, int kWn, int kAct>
+__global__ void __launch_bounds__(64) k_join(Product p) {
+  constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t slice[kStageBytes<TN>];
+  const int32_t tail = p.tiles_i * p.tiles_j - p.full;
+  const int32_t t = blockIdx.x / (kWm * kWn), wave = blockIdx.x % (kWm * kWn);
+  int64_t i0, j0;
+  tile_at(p, p.full + t, BM, BN, i0, j0);
+  v16f acc[FM][FN];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (j + k < J) v[k] += p[k];
-    }
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float4* o = reinterpret_cast<const float4*>(p.part) + ((int64_t)s * tail + t) * (BM * BN / 4) +
+                      wave * (TM * TN / 4) + threadIdx.x;
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 v = o[((m * FN + n) * 4 + g) * 64];
+          acc[m][n][4 * g] += v.x;
+          acc[m][n][4 * g + 1] += v.y;
+          acc[m][n][4 * g + 2] += v.z;
+          acc[m][n][4 * g + 3] += v.w;
+        }
   }
-  finish8(epi, v, i, j, J);
+  epilogue<TM, TN, kAct>(p.epi, acc, slice, i0 + wave / kWn * TM, j0 + wave % kWn * TN, p.I, p.J);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -530,7 +602,16 @@ __global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __rest
 #pragma unroll
       for (int g = 0; g < kSkWaves; ++g) v[k] += red[g][m >> 4][c & 3][16 * (c >> 2) + (m & 15)];
     }
-    finish8(epi, v, m, n0 + c0, N);
+    const int64_t j = n0 + c0;
+    if (j >= N) continue;
+    if (epi.bias) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j + k < N) v[k] += epi.bias[j + k];
+    }
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (epi.residual && epi.wide) res = *reinterpret_cast<const uint4*>(epi.residual + m * N + j);
+    finish8(epi, epi.act, v, res, m, j, N);
   }
 }
 
@@ -637,30 +718,50 @@ __global__ void __launch_bounds__(256) k_dbias(const float* __restrict__ part, i
 // ---------------------------------------------------------------- host side
 constexpr int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Tile and split of a product.
+// Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
+// tiles of the last, partly filled round are split over the contraction so
+// that it is filled.
 struct Plan {
   int tile;              // 256, 128 or 64
-  int32_t splits, split_tiles;
+  int32_t full, splits, split_c;
   int64_t part_bytes;
 };
 
 Plan plan_product(int64_t I, int64_t J, int64_t C) {
-  Plan pl;
-  auto tiles = [&](int64_t b) { return ((I + b - 1) / b) * ((J + b - 1) / b); };
-  pl.tile = tiles(256) >= kCus / 2 && J >= 192 && I >= 192 ? 256 : (J > 64 && I > 64 && tiles(128) >= kCus / 4 ? 128 : 64);
-  const int64_t t = tiles(pl.tile), all = (C + kC - 1) / kC;
-  int64_t s = t >= kCus || t == 0 ? 1 : (2 * kCus) / t;
-  if (s > all / 8) s = all / 8;     // at least 8 tiles of 64 per split
-  if (s > 64) s = 64;
-  if (s < 1) s = 1;
-  // an empty contraction still has one split, which writes zeros
-  pl.split_tiles = (int32_t)(all ? (all + s - 1) / s : 1);
-  pl.splits = (int32_t)(all ? (all + pl.split_tiles - 1) / pl.split_tiles : 1);
-  pl.part_bytes = pl.splits > 1 ? up(4 * I * J * pl.splits, 256) : 0;
-  return pl;
+#ifndef FORCE_TILE
+#define FORCE_TILE 0
+#endif
+  // workgroups per CU, and microseconds per 64 c of a round (all slots busy)
+  struct Shape { int tile, per_cu; double us; };
+  constexpr Shape shapes[3] = {{256, 1, 1.45}, {128, 2, 1.0}, {64, 2, 0.5}};
+  const int64_t all = (C + 63) / 64;
+  Plan best{};
+  double least = 1e30;
+  for (const Shape& sh : shapes) {
+    if (FORCE_TILE && sh.tile != FORCE_TILE) continue;
+    const int64_t ti = (I + sh.tile - 1) / sh.tile, tj = (J + sh.tile - 1) / sh.tile, t = ti * tj;
+    const int64_t slots = sh.per_cu * kCus, rounds = t / slots, rem = t - rounds * slots;
+    int64_t s = rem ? slots / rem : 1;
+    if (s > all / 8) s = all / 8;     // at least 512 c per split
+    if (s < 1) s = 1;
+    const int64_t per = all ? (all + s - 1) / s : 1;
+    s = all ? (all + per - 1) / per : 1;
+    double us = sh.us * ((double)rounds * all + (rem ? (double)per : 0.0)) + 3.0 * (rounds + (rem != 0));
+    const double part = 4.0 * s * rem * sh.tile * sh.tile;
+    if (s > 1) us += 4.0 + 2.0 * part / 4e6;   // the join's launch, its bytes at 4 TB/s
+    if (us < least) {
+      least = us;
+      best.tile = sh.tile;
+      best.full = (int32_t)(s > 1 ? rounds * slots : t);
+      best.splits = (int32_t)s;
+      best.split_c = (int32_t)(64 * per);
+      best.part_bytes = s > 1 ? (int64_t)part : 0;
+    }
+  }
+  return best;
 }
 
-template <bool kARows, bool kBRows>
+template <bool kARows, bool kBRows, int kAct>
 int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int64_t C, const Epi& epi, float* part,
                    hipStream_t st) {
   const Plan pl = plan_product(I, J, C);
@@ -670,21 +771,27 @@ int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int
   p.I = I;
   p.J = J;
   p.C = C;
-  p.tiles_i = (int32_t)((I + pl.tile - 1) / pl.tile);
-  p.tiles_j = (int32_t)((J + pl.tile - 1) / pl.tile);
+  const int64_t ti = (I + pl.tile - 1) / pl.tile, tj = (J + pl.tile - 1) / pl.tile;
+  if (ti * tj >= (1ll << 28)) return MX_EUNSUPPORTED;
+  p.tiles_i = (int32_t)ti;
+  p.tiles_j = (int32_t)tj;
+  p.full = pl.full;
   p.splits = pl.splits;
-  p.split_tiles = pl.split_tiles;
+  p.split_c = pl.split_c;
   p.part = part;
   p.epi = epi;
-  const int64_t total = (int64_t)p.tiles_i * p.tiles_j * p.splits;
-  if (total >= (1ll << 30)) return MX_EUNSUPPORTED;
-  const unsigned grid = (unsigned)(((total + kXcds - 1) / kXcds) * kXcds);
-  if (pl.tile == 256) hipLaunchKernelGGL((k_product<256, 256, 2, 4, 2, kARows, kBRows>), dim3(grid), dim3(512), 0, st, p);
-  else if (pl.tile == 128) hipLaunchKernelGGL((k_product<128, 128, 2, 2, 2, kARows, kBRows>), dim3(grid), dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((k_product<64, 64, 2, 2, 4, kARows, kBRows>), dim3(grid), dim3(256), 0, st, p);
-  if (p.splits > 1) {
-    const int64_t n = I * ((J + 7) / 8);
-    hipLaunchKernelGGL(k_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, p.splits, I, J, epi);
+  auto up8 = [](int64_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
+  const int64_t tail = ti * tj - pl.full;
+  const dim3 grid((unsigned)(up8(pl.full) + up8(tail * pl.splits)));
+  if (pl.tile == 256) {
+    hipLaunchKernelGGL((k_product<256, 256, 2, 4, 64, 2, kARows, kBRows, kAct>), grid, dim3(512), 0, st, p);
+    if (tail) hipLaunchKernelGGL((k_join<256, 256, 2, 4, kAct>), dim3((unsigned)(8 * tail)), dim3(64), 0, st, p);
+  } else if (pl.tile == 128) {
+    hipLaunchKernelGGL((k_product<128, 128, 2, 2, 64, 2, kARows, kBRows, kAct>), grid, dim3(256), 0, st, p);
+    if (tail) hipLaunchKernelGGL((k_join<128, 128, 2, 2, kAct>), dim3((unsigned)(4 * tail)), dim3(64), 0, st, p);
+  } else {
+    hipLaunchKernelGGL((k_product<64, 64, 2, 2, 64, 4, kARows, kBRows, kAct>), grid, dim3(256), 0, st, p);
+    if (tail) hipLaunchKernelGGL((k_join<64, 64, 2, 2, kAct>), dim3((unsigned)(4 * tail)), dim3(64), 0, st, p);
   }
   return launch_status();
 }
@@ -761,7 +868,15 @@ extern "C" int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float*
   }
   const int64_t need = plan_product(rows, n, k).part_bytes;
   if (need && (!workspace || (int64_t)workspace_bytes < need)) return MX_EINVAL;
-  return launch_product<true, true>(Operand{x, k}, Operand{w, k}, rows, n, k, epi, static_cast<float*>(workspace), st);
+  const Operand a{x, k}, b{w, k};
+  float* part = static_cast<float*>(workspace);
+  switch (act) {   // (the epilogue of a large tile is compiled per activation)
+    case MX_ACT_RELU: return launch_product<true, true, MX_ACT_RELU>(a, b, rows, n, k, epi, part, st);
+    case MX_ACT_GELU: return launch_product<true, true, MX_ACT_GELU>(a, b, rows, n, k, epi, part, st);
+    case MX_ACT_GELU_TANH: return launch_product<true, true, MX_ACT_GELU_TANH>(a, b, rows, n, k, epi, part, st);
+    case MX_ACT_SILU: return launch_product<true, true, MX_ACT_SILU>(a, b, rows, n, k, epi, part, st);
+    default: return launch_product<true, true, MX_ACT_NONE>(a, b, rows, n, k, epi, part, st);
+  }
 }
 
 extern "C" size_t mx_bf16_linear_bwd_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t act) {
@@ -814,13 +929,13 @@ extern "C" int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const ui
   if (dx && rows > 0) {
     epi.out = dx;
     epi.residual = dx_add;
-    const int rc = launch_product<true, false>(Operand{dzp, pitch}, Operand{w, k}, rows, k, n, epi, part, st);
+    const int rc = launch_product<true, false, MX_ACT_NONE>(Operand{dzp, pitch}, Operand{w, k}, rows, k, n, epi, part, st);
     if (rc != MX_OK) return rc;
   }
   if (dw) {
     epi.out = dw;
     epi.residual = nullptr;
-    const int rc = launch_product<false, false>(Operand{dzp, pitch}, Operand{x, k}, n, k, rows, epi, part, st);
+    const int rc = launch_product<false, false, MX_ACT_NONE>(Operand{dzp, pitch}, Operand{x, k}, n, k, rows, epi, part, st);
     if (rc != MX_OK) return rc;
   }
   return launch_status();
