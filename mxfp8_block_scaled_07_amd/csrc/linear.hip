@@ -35,10 +35,16 @@ constexpr uint32_t kOob = 0x80000000u;       // an offset that reads as zero
 constexpr int kSkinny = 64;                  // most rows of the streaming form
 
 // ---------------------------------------------------------------- activations
+// e^x for x <= 0 by the hardware's 2^x: its relative error grows with |x| (the
+// rounding of x log2 e), its absolute error |x| e^x 2^-24 stays below a unit of
+// the sums it goes into.
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
 // sigmoid(x) and sigmoid(-x) from e^-|x| in (0, 1]: neither is a difference.
+// 1 + e lies in (1, 2], where the hardware reciprocal is within a unit.
 __device__ __forceinline__ float sigmoid2(float x, float& minus) {
-  const float e = expf(-fabsf(x));
-  const float r = 1.0f / (1.0f + e), q = e * r;
+  const float e = exp_neg(-fabsf(x));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), q = e * r;
   minus = x >= 0.0f ? q : r;
   return x >= 0.0f ? r : q;
 }
@@ -66,7 +72,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case MX_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
     case MX_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * exp_neg(-0.5f * z * z);
     case MX_ACT_GELU_TANH: {
       if (fabsf(z) > 20.0f) return z > 0.0f ? 1.0f : 0.0f;   // to fp32 (and z^3 could overflow)
       float m;
@@ -312,15 +318,16 @@ struct FragAt {
 // hold 4 consecutive columns of one row per lane (32 rows of W fp32 columns
 // are staged at a time), rows of 8 columns per lane go out.  The residual of the next 32 rows is fetched while these are
 // finished: read where it is added, its latency costs more than the products
-// of a 256 x 256 tile's last quarter.
+// of a 256 x 256 tile's last quarter.  sums(): brings the accumulators, after
+// the first fetches.
 template <int TN>
 constexpr int kStageCols = TN < 64 ? TN : 64;
 template <int TN>
 constexpr int kStageBytes = 32 * (kStageCols<TN> * 4 + 16);
 
-template <int TM, int TN, int kAct>
+template <int TM, int TN, int kAct, typename Sums>
 __device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
-                                         int64_t j0, int64_t I, int64_t J) {
+                                         int64_t j0, int64_t I, int64_t J, Sums sums) {
   constexpr int FM = TM / 32, FN = TN / 32, W = kStageCols<TN>, kPitch = W * 4 + 16;
   constexpr int kLpr = W / 8, kRpp = 64 / kLpr, kIt = 32 / kRpp;   // lanes per row, rows per pass, passes
   const int lane = threadIdx.x & 63;
@@ -343,6 +350,7 @@ __device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN /
       }
     };
     fetch(0);
+    if (n0 == 0) sums();
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
       if (m + 1 < FM) fetch(m + 1);
@@ -452,7 +460,8 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   // products: a burst of either stalls the products behind it.
   constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
   // with two slots a tile has one tile's time to arrive: its loads all go into the first part
-  constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
+  // (one slot serves a contraction of one tile, which loads nothing here)
+  constexpr int kPerPart = kSlots <= 2 ? kLoads : (kLoads + kParts - 1) / kParts;
   v8bf_s a[2][FM], b[2][FN];
   // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
   auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
     // are done (the kSlots - 2 tiles after it may be in flight; near the end
     // fewer are, so everything is waited for) ...
     __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-    if (t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 2)));
+    if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     // ... and after the barrier every wave's: the slot takes tile t + kSlots
     lds_barrier();
@@ -512,43 +521,43 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
               make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
     return;
   }
-  epilogue<TM, TN, kAct>(p.epi, acc, lds + wave * kStageBytes<TN>, i0 + wm * TM, j0 + wn * TN, p.I, p.J);
+  epilogue<TM, TN, kAct>(p.epi, acc, lds + wave * kStageBytes<TN>, i0 + wm * TM, j0 + wn * TN, p.I, p.J, [] {});
 }
 
-// The split tiles: one wave per wave's share of a tile adds its partial sums
-// in the splits' order, then the epilogue.
+// The split tiles: one wave per 32 rows of a wave's share of a tile adds the
+// partial sums in the splits' order, then the epilogue.
 template <int BM, int BN, int kWm, int kWn, int kAct>
 __global__ void __launch_bounds__(64) k_join(Product p) {
   constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
   __shared__ __attribute__((aligned(16))) uint8_t slice[kStageBytes<TN>];
   const int32_t tail = p.tiles_i * p.tiles_j - p.full;
-  const int32_t t = blockIdx.x / (kWm * kWn), wave = blockIdx.x % (kWm * kWn);
+  const int32_t t = blockIdx.x / (kWm * kWn * FM), in = blockIdx.x % (kWm * kWn * FM);
+  const int32_t wave = in / FM, m = in % FM;
   int64_t i0, j0;
   tile_at(p, p.full + t, BM, BN, i0, j0);
-  v16f acc[FM][FN];
+  v16f acc[1][FN];
 #pragma unroll
-  for (int m = 0; m < FM; ++m)
+  for (int n = 0; n < FN; ++n)
 #pragma unroll
-    for (int n = 0; n < FN; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float4* o = reinterpret_cast<const float4*>(p.part) + ((int64_t)s * tail + t) * (BM * BN / 4) +
-                      wave * (TM * TN / 4) + threadIdx.x;
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
+    for (int r = 0; r < 16; ++r) acc[0][n][r] = 0.f;
+  const float4* o = reinterpret_cast<const float4*>(p.part) + (int64_t)t * (BM * BN / 4) + wave * (TM * TN / 4) +
+                    m * (FN * 256) + threadIdx.x;
+  auto sums = [&] {
+#pragma unroll 2
+    for (int s = 0; s < p.splits; ++s, o += (int64_t)tail * (BM * BN / 4)) {
 #pragma unroll
       for (int n = 0; n < FN; ++n)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float4 v = o[((m * FN + n) * 4 + g) * 64];
-          acc[m][n][4 * g] += v.x;
-          acc[m][n][4 * g + 1] += v.y;
-          acc[m][n][4 * g + 2] += v.z;
-          acc[m][n][4 * g + 3] += v.w;
+          const float4 v = o[(n * 4 + g) * 64];
+          acc[0][n][4 * g] += v.x;
+          acc[0][n][4 * g + 1] += v.y;
+          acc[0][n][4 * g + 2] += v.z;
+          acc[0][n][4 * g + 3] += v.w;
         }
-  }
-  epilogue<TM, TN, kAct>(p.epi, acc, slice, i0 + wave / kWn * TM, j0 + wave % kWn * TN, p.I, p.J);
+    }
+  };
+  epilogue<32, TN, kAct>(p.epi, acc, slice, i0 + wave / kWn * TM + 32 * m, j0 + wave % kWn * TN, p.I, p.J, sums);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -632,6 +641,7 @@ __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (j < N) {
     const int n = N - j < 8 ? (int)(N - j) : 8;
+#pragma unroll 2
     for (int64_t r = r0 + rl; r < r1; r += rt) {
       float v[8];
       const int64_t at = r * N + j;
@@ -718,28 +728,37 @@ __global__ void __launch_bounds__(256) k_dbias(const float* __restrict__ part, i
 // ---------------------------------------------------------------- host side
 constexpr int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
+// Tile shapes.
+enum Shape { k256x256, k128x128, k128x128One, k128x64, k64x64, kShapes };
+constexpr struct {
+  int bm, bn, per_cu;   // workgroups per CU (LDS)
+  double us;            // microseconds per 64 c of a round with all slots busy and operands in L2
+  double stream;        // bytes per microsecond at which it streams operands that are read once
+} kShape[kShapes] = {
+    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
+    {128, 128, 2, 1.13, 4.9e6},
+    {128, 128, 4, 2.2, 4.9e6},    // one LDS tile: contractions up to 64 (8191 x 7168 x 64: 56 us, against 61)
+    {128, 64, 1, 0.70, 5.6e6},    // 32768 x 64 x 7168: 86 us, against 94 with 64 x 64
+    {64, 64, 2, 0.50, 4.9e6}};
+
 // Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
 // tiles of the last, partly filled round are split over the contraction so
 // that it is filled.
 struct Plan {
-  int tile;              // 256, 128 or 64
+  int shape;
   int32_t full, splits, split_c;
   int64_t part_bytes;
 };
 
 Plan plan_product(int64_t I, int64_t J, int64_t C) {
-#ifndef FORCE_TILE
-#define FORCE_TILE 0
-#endif
-  // workgroups per CU, and microseconds per 64 c of a round (all slots busy)
-  struct Shape { int tile, per_cu; double us; };
-  constexpr Shape shapes[3] = {{256, 1, 1.45}, {128, 2, 1.0}, {64, 2, 0.5}};
   const int64_t all = (C + 63) / 64;
   Plan best{};
   double least = 1e30;
-  for (const Shape& sh : shapes) {
-    if (FORCE_TILE && sh.tile != FORCE_TILE) continue;
-    const int64_t ti = (I + sh.tile - 1) / sh.tile, tj = (J + sh.tile - 1) / sh.tile, t = ti * tj;
+  for (int id = 0; id < kShapes; ++id) {
+    // one LDS tile: the output is the cost, and four workgroups per CU overlap it best
+    if (C <= 64 ? id == k256x256 || id == k128x128 : id == k128x128One) continue;
+    const auto& sh = kShape[id];
+    const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn, t = ti * tj;
     const int64_t slots = sh.per_cu * kCus, rounds = t / slots, rem = t - rounds * slots;
     int64_t s = rem ? slots / rem : 1;
     if (s > all / 8) s = all / 8;     // at least 512 c per split
@@ -747,11 +766,12 @@ Plan plan_product(int64_t I, int64_t J, int64_t C) {
     const int64_t per = all ? (all + s - 1) / s : 1;
     s = all ? (all + per - 1) / per : 1;
     double us = sh.us * ((double)rounds * all + (rem ? (double)per : 0.0)) + 3.0 * (rounds + (rem != 0));
-    const double part = 4.0 * s * rem * sh.tile * sh.tile;
+    if (us < 2.0 * C * (I + J) / sh.stream) us = 2.0 * C * (I + J) / sh.stream;
+    const double part = 4.0 * s * rem * sh.bm * sh.bn;
     if (s > 1) us += 4.0 + 2.0 * part / 4e6;   // the join's launch, its bytes at 4 TB/s
     if (us < least) {
       least = us;
-      best.tile = sh.tile;
+      best.shape = id;
       best.full = (int32_t)(s > 1 ? rounds * slots : t);
       best.splits = (int32_t)s;
       best.split_c = (int32_t)(64 * per);
@@ -761,17 +781,28 @@ Plan plan_product(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct>
+void launch_shape(const Product& p, hipStream_t st) {
+  auto up8 = [](int32_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
+  const int32_t tail = p.tiles_i * p.tiles_j - p.full;
+  const dim3 grid((unsigned)(up8(p.full) + up8(tail * p.splits)));
+  hipLaunchKernelGGL((k_product<BM, BN, kWm, kWn, kC, kSlots, kARows, kBRows, kAct>), grid, dim3(64 * kWm * kWn), 0, st, p);
+  if (tail)
+    hipLaunchKernelGGL((k_join<BM, BN, kWm, kWn, kAct>), dim3((unsigned)(BM / 32 * kWn * tail)), dim3(64), 0, st, p);
+}
+
 template <bool kARows, bool kBRows, int kAct>
 int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int64_t C, const Epi& epi, float* part,
                    hipStream_t st) {
   const Plan pl = plan_product(I, J, C);
+  const auto& sh = kShape[pl.shape];
   Product p;
   p.a = a;
   p.b = b;
   p.I = I;
   p.J = J;
   p.C = C;
-  const int64_t ti = (I + pl.tile - 1) / pl.tile, tj = (J + pl.tile - 1) / pl.tile;
+  const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn;
   if (ti * tj >= (1ll << 28)) return MX_EUNSUPPORTED;
   p.tiles_i = (int32_t)ti;
   p.tiles_j = (int32_t)tj;
@@ -780,18 +811,12 @@ int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int
   p.split_c = pl.split_c;
   p.part = part;
   p.epi = epi;
-  auto up8 = [](int64_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
-  const int64_t tail = ti * tj - pl.full;
-  const dim3 grid((unsigned)(up8(pl.full) + up8(tail * pl.splits)));
-  if (pl.tile == 256) {
-    hipLaunchKernelGGL((k_product<256, 256, 2, 4, 64, 2, kARows, kBRows, kAct>), grid, dim3(512), 0, st, p);
-    if (tail) hipLaunchKernelGGL((k_join<256, 256, 2, 4, kAct>), dim3((unsigned)(8 * tail)), dim3(64), 0, st, p);
-  } else if (pl.tile == 128) {
-    hipLaunchKernelGGL((k_product<128, 128, 2, 2, 64, 2, kARows, kBRows, kAct>), grid, dim3(256), 0, st, p);
-    if (tail) hipLaunchKernelGGL((k_join<128, 128, 2, 2, kAct>), dim3((unsigned)(4 * tail)), dim3(64), 0, st, p);
-  } else {
-    hipLaunchKernelGGL((k_product<64, 64, 2, 2, 64, 4, kARows, kBRows, kAct>), grid, dim3(256), 0, st, p);
-    if (tail) hipLaunchKernelGGL((k_join<64, 64, 2, 2, kAct>), dim3((unsigned)(4 * tail)), dim3(64), 0, st, p);
+  switch (pl.shape) {
+    case k256x256: launch_shape<256, 256, 2, 4, 64, 2, kARows, kBRows, kAct>(p, st); break;
+    case k128x128: launch_shape<128, 128, 2, 2, 64, 2, kARows, kBRows, kAct>(p, st); break;
+    case k128x128One: launch_shape<128, 128, 2, 2, 64, 1, kARows, kBRows, kAct>(p, st); break;
+    case k128x64: launch_shape<128, 64, 2, 2, 64, 5, kARows, kBRows, kAct>(p, st); break;
+    default: launch_shape<64, 64, 2, 2, 64, 4, kARows, kBRows, kAct>(p, st); break;
   }
   return launch_status();
 }
