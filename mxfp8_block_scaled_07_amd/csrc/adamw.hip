@@ -9,8 +9,10 @@
 //
 // One launch takes up to kBatch tensors: their pointers travel in the kernel
 // arguments, so the call needs no table in device memory and can be captured.
-// A block takes one chunk of one tensor, a thread 4 consecutive elements (16
-// bytes of fp32) per pass.
+// A block takes 1024 elements of one tensor, a thread 4 consecutive ones (16
+// bytes of fp32); more per block is slower (fp32 states 144, 145, 149 us for 1,
+// 2, 4 times as many on 30M elements; 8-bit states 1.80, 1.91, 1.94 ms on 671M,
+// 6.0 TB/s at best).
 //
 // 8-bit states are MX blocks of 32 consecutive elements (E4M3 codes, one E8M0
 // scale).  m is kept as it is and v as its root: E4M3 spans 2^-9 .. 448 inside
@@ -32,14 +34,13 @@ namespace mx {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kPass = 4 * kAdamThreads;   // elements of a block per pass
+constexpr int kChunk = 4 * kAdamThreads;  // elements of a block
 constexpr int kBatch = 48;                // tensors per launch (the arguments stay below 4 KB)
 
 struct Batch {
   mx_adamw_tensor_t t[kBatch];
   int32_t first[kBatch + 1];   // chunks before each tensor
   int32_t count, base;         // tensors here; the index of t[0] in the call
-  int32_t passes;              // a chunk's passes
 };
 static_assert(sizeof(Batch) <= 3500, "kernel arguments");
 
@@ -101,33 +102,59 @@ __device__ __forceinline__ uint32_t stochastic_bf16(float x, uint32_t u) {
   return finite(x) ? (b + u) >> 16 : (b >> 16) | ((b & 0xFFFFu) ? 0x40u : 0u);
 }
 
+// Four elements from i on; n of them where not kFull.  Each byte is used once:
+// non-temporal accesses leave the caches alone (97 tensors of 30M elements,
+// fp32: 144 us, against 191 with default ones).
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+
 template <bool kF32>
-__device__ __forceinline__ void load4(const void* p, int64_t i, int n, float (&x)[4]) {
-  if (n == 4) {
-    if constexpr (kF32) {
-      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+struct Raw4 {
+  f4 f;
+};
+template <>
+struct Raw4<false> {
+  u2 f;
+};
+
+template <bool kF32, bool kFull>
+__device__ __forceinline__ Raw4<kF32> load4(const void* p, int64_t i, int n) {
+  Raw4<kF32> r;
+  if constexpr (kF32) {
+    const float* s = static_cast<const float*>(p) + i;
+    if (kFull) {
+      r.f = __builtin_nontemporal_load(reinterpret_cast<const f4*>(s));
     } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    }
-    return;
-  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[k] = 0.0f;
-    if (k < n) {
-      if constexpr (kF32) x[k] = static_cast<const float*>(p)[i + k];
-      else x[k] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i + k] << 16);
+      for (int k = 0; k < 4; ++k) r.f[k] = k < n ? s[k] : 0.0f;
+    }
+  } else {
+    const uint16_t* s = static_cast<const uint16_t*>(p) + i;
+    if (kFull) {
+      r.f = __builtin_nontemporal_load(reinterpret_cast<const u2*>(s));
+    } else {
+      r.f = u2{0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < n) r.f[k >> 1] |= (uint32_t)s[k] << (16 * (k & 1));
     }
   }
+  return r;
 }
 
+__device__ __forceinline__ void widen(const Raw4<true>& r, float (&x)[4]) {
+  x[0] = r.f[0]; x[1] = r.f[1]; x[2] = r.f[2]; x[3] = r.f[3];
+}
+__device__ __forceinline__ void widen(const Raw4<false>& r, float (&x)[4]) {
+  x[0] = __uint_as_float(r.f[0] << 16); x[1] = __uint_as_float(r.f[0] & 0xFFFF0000u);
+  x[2] = __uint_as_float(r.f[1] << 16); x[3] = __uint_as_float(r.f[1] & 0xFFFF0000u);
+}
+
+template <bool kFull>
 __device__ __forceinline__ void store4_f32(void* p, int64_t i, int n, const float (&x)[4]) {
   float* d = static_cast<float*>(p) + i;
-  if (n == 4) {
-    *reinterpret_cast<float4*>(d) = make_float4(x[0], x[1], x[2], x[3]);
+  if (kFull) {
+    __builtin_nontemporal_store(f4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f4*>(d));
     return;
   }
 #pragma unroll
@@ -135,10 +162,11 @@ __device__ __forceinline__ void store4_f32(void* p, int64_t i, int n, const floa
     if (k < n) d[k] = x[k];
 }
 
+template <bool kFull>
 __device__ __forceinline__ void store4_u16(void* p, int64_t i, int n, uint32_t lo, uint32_t hi) {
   uint16_t* d = static_cast<uint16_t*>(p) + i;
-  if (n == 4) {
-    *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+  if (kFull) {
+    __builtin_nontemporal_store(u2{lo, hi}, reinterpret_cast<u2*>(d));
     return;
   }
 #pragma unroll
@@ -146,9 +174,10 @@ __device__ __forceinline__ void store4_u16(void* p, int64_t i, int n, uint32_t l
     if (k < n) d[k] = (uint16_t)((k < 2 ? lo : hi) >> (16 * (k & 1)));
 }
 
+template <bool kFull>
 __device__ __forceinline__ uint32_t load4_u8(const void* p, int64_t i, int n) {
   const uint8_t* s = static_cast<const uint8_t*>(p) + i;
-  if (n == 4) return *reinterpret_cast<const uint32_t*>(s);
+  if (kFull) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(s));
   uint32_t v = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -156,10 +185,11 @@ __device__ __forceinline__ uint32_t load4_u8(const void* p, int64_t i, int n) {
   return v;
 }
 
+template <bool kFull>
 __device__ __forceinline__ void store4_u8(void* p, int64_t i, int n, uint32_t v) {
   uint8_t* d = static_cast<uint8_t*>(p) + i;
-  if (n == 4) {
-    *reinterpret_cast<uint32_t*>(d) = v;
+  if (kFull) {
+    __builtin_nontemporal_store(v, reinterpret_cast<uint32_t*>(d));
     return;
   }
 #pragma unroll
@@ -194,95 +224,141 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t 
   return codes;
 }
 
+struct Step {
+  float b1, b2, c1, c2, size, root2, decay, eps, gs;
+  uint32_t key;
+};
+
+// What a thread reads of four elements.
 template <bool kP32, bool kG32, bool kS8>
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(Batch b, Hyper hp) {
-  // the block's tensor: the last with first[i] <= blockIdx.x
-  int lo = 0, hi = b.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (b.first[mid] <= (int)blockIdx.x) lo = mid; else hi = mid;
+struct In {
+  Raw4<kP32> p;
+  Raw4<kG32> g;
+  Raw4<true> m, v;         // fp32 states
+  uint32_t mc, vc, ms, vs; // or codes and scales
+};
+
+template <bool kP32, bool kG32, bool kS8, bool kFull>
+__device__ __forceinline__ void read(In<kP32, kG32, kS8>& in, const mx_adamw_tensor_t& t, int64_t i, int n) {
+  in.p = load4<kP32, kFull>(t.param, i, n);
+  in.g = load4<kG32, kFull>(t.grad, i, n);
+  if constexpr (kS8) {
+    in.mc = load4_u8<kFull>(t.m, i, n);
+    in.vc = load4_u8<kFull>(t.v, i, n);
+    in.ms = kFull || n ? t.m_scale[i >> 5] : 0u;
+    in.vs = kFull || n ? t.v_scale[i >> 5] : 0u;
+  } else {
+    in.m = load4<true, kFull>(t.m, i, n);
+    in.v = load4<true, kFull>(t.v, i, n);
   }
-  const mx_adamw_tensor_t& t = b.t[lo];
-  const int64_t begin = (int64_t)((int)blockIdx.x - b.first[lo]) * b.passes * kPass;
+}
 
-  const int32_t st = *hp.step;
-  const uint32_t step = st < 1 ? 1u : (uint32_t)st;
-  const float lr = *hp.lr;
-  const float gs = hp.grad_scale ? *hp.grad_scale : 1.0f;
-  const float b1 = (float)hp.b1, b2 = (float)hp.b2;
-  const float c1 = (float)(1.0 - hp.b1), c2 = (float)(1.0 - hp.b2);
-  const float size = lr / (float)one_minus_pow(hp.b1, step);
-  const float root2 = (float)(1.0 / sqrt(one_minus_pow(hp.b2, step)));
-  const float decay = 1.0f - lr * hp.wd;
-  uint32_t key = mix(hp.seed_lo ^ kGold);
-  key = mix(key ^ hp.seed_hi);
-  key = mix(key ^ step);
-  key = mix(key ^ (uint32_t)(b.base + lo));
-
-  for (int pass = 0; pass < b.passes; ++pass) {
-    const int64_t i = begin + (int64_t)pass * kPass + 4 * threadIdx.x;
-    if (i - 4 * (int64_t)threadIdx.x >= t.n) break;
-    // lanes past the end stay, so that whole blocks of 32 reduce together
-    const int n = i >= t.n ? 0 : (t.n - i < 4 ? (int)(t.n - i) : 4);
-    float p[4], g[4], m[4], v[4];
-    load4<kP32>(t.param, i, n, p);
-    load4<kG32>(t.grad, i, n, g);
-    if constexpr (kS8) {
-      const int64_t blk = i >> 5;
-      const uint32_t mc = load4_u8(t.m, i, n), vc = load4_u8(t.v, i, n);
-      decode4(mc, n ? t.m_scale[blk] : 0u, m);
-      decode4(vc, n ? t.v_scale[blk] : 0u, v);
+template <bool kP32, bool kG32, bool kS8, bool kFull>
+__device__ __forceinline__ void update(const In<kP32, kG32, kS8>& in, const mx_adamw_tensor_t& t, int64_t i, int n,
+                                       const Step& s) {
+  float p[4], g[4], m[4], v[4], root[4];
+  widen(in.p, p);
+  widen(in.g, g);
+  if constexpr (kS8) {
+    decode4(in.mc, in.ms, m);
+    decode4(in.vc, in.vs, v);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] *= v[k];
-    } else {
-      load4<true>(t.m, i, n, m);
-      load4<true>(t.v, i, n, v);
-    }
-    float root[4];
+    for (int k = 0; k < 4; ++k) v[k] *= v[k];
+  } else {
+    widen(in.m, m);
+    widen(in.v, v);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float gk = g[k] * s.gs;
+    m[k] = fmaf(s.b1, m[k], s.c1 * gk);
+    v[k] = fmaf(s.b2, v[k], s.c2 * (gk * gk));
+    // hardware root and reciprocal, each within a unit (exact ones cost the 8-bit
+    // step 8% of its time)
+    root[k] = __builtin_amdgcn_sqrtf(v[k]);
+    p[k] = fmaf(-s.size, m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.root2, s.eps)), p[k] * s.decay);
+  }
+  uint32_t h[4];
+  if constexpr (kS8 || !kP32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = mix((s.key + (uint32_t)(i + k) * kGold) ^ (uint32_t)(i >> 32));
+  }
+  if constexpr (kS8) {
+    uint32_t um[4], uv[4], bm, bv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float gk = g[k] * gs;
-      m[k] = fmaf(b1, m[k], c1 * gk);
-      v[k] = fmaf(b2, v[k], c2 * (gk * gk));
-      root[k] = sqrtf(v[k]);
-      p[k] = fmaf(-size, m[k] / fmaf(root[k], root2, hp.eps), p[k] * decay);
+      um[k] = h[k] >> 16;
+      uv[k] = h[k] & 0xFFFFu;
+      if (!kFull && k >= n) m[k] = root[k] = 0.0f;   // not in the block
     }
-    uint32_t h[4];
-    if constexpr (kS8 || !kP32) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = mix((key + (uint32_t)(i + k) * kGold) ^ (uint32_t)((i + k) >> 32));
+    const uint32_t cm = encode4<false>(m, um, bm), cv = encode4<true>(root, uv, bv);
+    store4_u8<kFull>(t.m, i, n, cm);
+    store4_u8<kFull>(t.v, i, n, cv);
+    if ((threadIdx.x & 7) == 0 && (kFull || n)) {
+      t.m_scale[i >> 5] = (uint8_t)bm;
+      t.v_scale[i >> 5] = (uint8_t)bv;
     }
-    if constexpr (kS8) {
-      uint32_t um[4], uv[4], bm, bv;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        um[k] = h[k] >> 16;
-        uv[k] = h[k] & 0xFFFFu;
-        if (k >= n) m[k] = root[k] = 0.0f;   // not in the block
-      }
-      const uint32_t cm = encode4<false>(m, um, bm), cv = encode4<true>(root, uv, bv);
-      store4_u8(t.m, i, n, cm);
-      store4_u8(t.v, i, n, cv);
-      if ((threadIdx.x & 7) == 0 && n) {
-        t.m_scale[i >> 5] = (uint8_t)bm;
-        t.v_scale[i >> 5] = (uint8_t)bv;
-      }
-    } else {
-      store4_f32(t.m, i, n, m);
-      store4_f32(t.v, i, n, v);
-    }
-    if constexpr (kP32) {
-      store4_f32(t.param, i, n, p);
-      if (t.copy) store4_u16(t.copy, i, n, bf16x2_rne(p[0], p[1]), bf16x2_rne(p[2], p[3]));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = stochastic_bf16(p[k], mix(h[k] ^ kGold) >> 16);
-      const uint32_t a = w[0] | (w[1] << 16), c = w[2] | (w[3] << 16);
-      store4_u16(t.param, i, n, a, c);
-      if (t.copy) store4_u16(t.copy, i, n, a, c);
-    }
+  } else {
+    store4_f32<kFull>(t.m, i, n, m);
+    store4_f32<kFull>(t.v, i, n, v);
   }
+  if constexpr (kP32) {
+    store4_f32<kFull>(t.param, i, n, p);
+    if (t.copy) store4_u16<kFull>(t.copy, i, n, bf16x2_rne(p[0], p[1]), bf16x2_rne(p[2], p[3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = stochastic_bf16(p[k], mix(h[k] ^ kGold) >> 16);
+    const uint32_t a = w[0] | (w[1] << 16), c = w[2] | (w[3] << 16);
+    store4_u16<kFull>(t.param, i, n, a, c);
+    if (t.copy) store4_u16<kFull>(t.copy, i, n, a, c);
+  }
+}
+
+template <bool kP32, bool kG32, bool kS8>
+__global__ void __launch_bounds__(kAdamThreads) k_adamw(Batch b, Hyper hp) {
+  // the block's tensor: the last with first[i] <= blockIdx.x (one load, by lane)
+  const int lane = threadIdx.x & 63;
+  const bool at = lane < b.count && b.first[lane < kBatch ? lane : 0] <= (int)blockIdx.x;
+  const int which = __builtin_amdgcn_readfirstlane(63 - __clzll((long long)__ballot(at)));
+  const mx_adamw_tensor_t t = b.t[which];
+  const int64_t begin = (int64_t)((int)blockIdx.x - b.first[which]) * kChunk;
+  const int64_t i = begin + 4 * threadIdx.x;
+  // a whole chunk, or the tensor's last one: there lanes past the end stay, so
+  // that whole blocks of 32 reduce together
+  const bool full = begin + kChunk <= t.n;
+  const int n = full ? 4 : (i >= t.n ? 0 : (t.n - i < 4 ? (int)(t.n - i) : 4));
+  In<kP32, kG32, kS8> in;
+  if (full) read<kP32, kG32, kS8, true>(in, t, i, n);
+  else read<kP32, kG32, kS8, false>(in, t, i, n);
+
+  // the step's constants, by one wave (about a hundred fp64 operations)
+  __shared__ Step shared;
+  if (threadIdx.x < 64) {
+    const int32_t st = *hp.step;
+    const uint32_t step = st < 1 ? 1u : (uint32_t)st;
+    const float lr = *hp.lr;
+    Step c;
+    c.gs = hp.grad_scale ? *hp.grad_scale : 1.0f;
+    c.b1 = (float)hp.b1;
+    c.b2 = (float)hp.b2;
+    c.c1 = (float)(1.0 - hp.b1);
+    c.c2 = (float)(1.0 - hp.b2);
+    c.size = lr / (float)one_minus_pow(hp.b1, step);
+    c.root2 = (float)(1.0 / sqrt(one_minus_pow(hp.b2, step)));
+    c.decay = 1.0f - lr * hp.wd;
+    c.eps = hp.eps;
+    uint32_t key = mix(hp.seed_lo ^ kGold);
+    key = mix(key ^ hp.seed_hi);
+    key = mix(key ^ step);
+    c.key = mix(key ^ (uint32_t)(b.base + which));
+    if (threadIdx.x == 0) shared = c;
+  }
+  __syncthreads();
+  const Step s = shared;
+
+  if (full) update<kP32, kG32, kS8, true>(in, t, i, n, s);
+  else update<kP32, kG32, kS8, false>(in, t, i, n, s);
 }
 
 template <bool kP32, bool kG32>
@@ -317,15 +393,10 @@ extern "C" int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t
     // 16-byte accesses
     if (((uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.m | (uintptr_t)t.v | (uintptr_t)t.copy) & 15)
       return MX_EINVAL;
-    if (t.n >= (1ll << 40) || total >= (1ll << 40)) return MX_EUNSUPPORTED;
+    if (t.n >= (1ll << 40) || total >= (1ll << 40)) return MX_EUNSUPPORTED;   // blocks below 2^31
     total += t.n;
   }
   if (total == 0) return MX_OK;
-  // passes per block: one while that still gives every CU its eight blocks,
-  // up to eight so that large steps do not pay a block's start per 1024 elements
-  int64_t passes = total / (256ll * 8 * kPass);
-  passes = passes < 1 ? 1 : (passes > 8 ? 8 : passes);
-  while (total / (passes * kPass) >= (1ll << 30)) passes *= 2;
   Hyper hp;
   hp.lr = lr;
   hp.grad_scale = grad_scale;
@@ -341,12 +412,11 @@ extern "C" int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t
     Batch b;
     b.count = count - base < kBatch ? count - base : kBatch;
     b.base = base;
-    b.passes = (int32_t)passes;
     int64_t chunks = 0;
     for (int32_t i = 0; i < b.count; ++i) {
       b.t[i] = tensors[base + i];
       b.first[i] = (int32_t)chunks;
-      chunks += (b.t[i].n + passes * kPass - 1) / (passes * kPass);
+      chunks += (b.t[i].n + kChunk - 1) / kChunk;
     }
     b.first[b.count] = (int32_t)chunks;
     if (chunks == 0) continue;
