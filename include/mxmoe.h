@@ -289,8 +289,8 @@ int mx_router_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, int64
 
 /*
  * The whole SwiGLU MoE layer for a few tokens (decoding): what the layer of
- * mx_route_topk .. mx_combine computes, in two launches, for at most 64
- * tokens.  Weights are those of the layer's forward GEMMs; activations stay
+ * mx_route_topk .. mx_combine computes, in two or three launches, for at most
+ * 64 tokens.  Weights are those of the layer's forward GEMMs; activations stay
  * in bf16 (they are not quantized: with this few tokens the stream of weights
  * is the cost), so the result is nearer to the real-valued layer than the
  * MXFP8 path's.
@@ -311,7 +311,7 @@ int mx_router_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, int64
  * The result does not depend on the schedule (bit-identical between calls),
  * and a token's row not on the other tokens beyond the order of its fp32 sums.
  * Requires H % 32 == 0, F % 32 == 0, 1 <= topk <= num_experts; x, w1, w2 and
- * the workspace 16-byte aligned.  MX_EUNSUPPORTED (and a workspace size of 0)
+ * the workspace 16-byte, out and residual 4-byte aligned.  MX_EUNSUPPORTED (and a workspace size of 0)
  * above 64 tokens, 1024 experts or top-64, and for one expert's matrix or the
  * scales of 2^31 bytes or more.
  */

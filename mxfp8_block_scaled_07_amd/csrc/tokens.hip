@@ -1,5 +1,5 @@
 // The whole SwiGLU MoE layer for a few tokens (gfx950), from the router's
-// logits to the combined rows, in two kernels:
+// logits to the combined rows:
 //
 //   [G; U] = W1_e x_t,  A = w_tj silu(G) U,  out_t = residual_t + sum_j W2_e A
 //   with e = ids_tj the k largest logits of token t (equal logits to the lower
@@ -10,46 +10,79 @@
 // many tokens pads each expert to 32 rows and makes eighteen launches; here
 //   k_tokens_up    every workgroup routes all tokens by itself (a few hundred
 //                  instructions per token, cheaper than a launch of its own),
-//                  then takes items of 16 gate and 16 up rows of one active
-//                  expert, its eight waves splitting H, and writes A;
-//   k_tokens_down  a workgroup owns 16 rows of the output and reads them from
-//                  every active expert's W2, its waves splitting experts and F.
-// A is kept in bf16 (one rounding of w silu(G) U); everything else between
-// the two roundings of bf16 inputs and outputs is fp32.  The weight goes into
-// A so that the sum over a token's experts is one fp32 sum over its products.
-// All sums have a fixed order: the result does not depend on scheduling.
+//                  then takes a run of items: 16 gate and 16 up rows of one
+//                  active expert, its eight waves splitting H; writes A
+//   k_tokens_down  groups of 128 output rows, 16 per wave, over the active
+//                  experts' F; the groups' work is cut evenly over the card
+//   k_tokens_join  adds the pieces of a group in order (where it was cut)
+//
+// The weights stream through LDS: non-temporal LDS-direct loads of whole
+// 128-byte lines into a ring of each wave's own, so that waiting needs no
+// barrier and no registers.  A read-only stream of whole lines runs at 7.1 TB/s
+// here non-temporally and at 6.3 TB/s otherwise, one of half lines (as matrix
+// fragments loaded straight into registers) at 5.0 and 6.3.  What then costs is
+// every other vector load beside the stream: reading the tokens again for each
+// step took 10% of the up kernel and 28% of the down kernel (33 tokens).  So
+// the up kernel keeps its waves' share of the tokens in registers while it
+// stays with an expert, and the down kernel's waves share theirs through LDS.
+//
+// A wave's products: 16 weight rows as the first operand and 16 token rows as
+// the second of V_MFMA_F32_16X16X32_BF16.  Of a 128-byte line of weight row r,
+// lane (r = l & 15, h = l >> 4) takes the bytes 32 h .. 32 h + 31 and the same
+// elements of token row r (the order of k inside a dot product is free as long
+// as both operands share it).  For fp8 these are one MX block: its scale is one
+// byte of the panel dword, and the codes become bf16 in registers (an E4M3 code
+// times a power of two is exact in bf16), so weights are used unrounded and
+// tokens stay in bf16.  A is kept in bf16 (one rounding of w silu(G) U);
+// everything else between the bf16 inputs and outputs is fp32.  The weight goes
+// into A so that the sum over a token's experts is one fp32 sum.  All sums have
+// a fixed order: the result does not depend on scheduling.
 
-#include "skinny.h"
+#include "mx_device.h"
+
+// The LDS-direct loads below set M0 in inline asm.
+#pragma clang diagnostic ignored "-Winline-asm"
 
 namespace mx {
 namespace {
 
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
 constexpr int kMaxTokens = 64;     // one bit of a 64-bit mask each
 constexpr int kTokExperts = 1024;  // as mx_route_topk
 constexpr int kTokTopk = 64;
+constexpr int kMaxRows = kMaxTokens * kTokTopk;
+constexpr int kEntries = kTokExperts + kMaxRows / 16;
 constexpr int kWaves = 8;
-constexpr int kTokThreads = 64 * kWaves;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kCus = 256;          // MI355X
+constexpr uint32_t kOob = 0x80000000u;   // an offset that reads as zero
 
-// Workspace: the routing table, then A [rows, F] in bf16.
-//   int32 U; act[U] (expert), first[U + 1] (rows before it); uint8 token[rows]
+// Entries: an active expert's rows (token, expert pairs) in groups of at most
+// the up kernel's token tiles.  The workspace holds the table for the down
+// kernel, the pieces of the output, then A [rows, F] in bf16.
 struct Table {
-  int32_t U, rows;
-  int32_t pad[2];
-  int32_t act[kTokExperts];
-  int32_t first[kTokExperts + 1];
-  int32_t pad2[3];
-  uint8_t token[kMaxTokens * kTokTopk];
+  int32_t entries, rows;
+  int32_t tiles;                    // 16-row tiles of all entries
+  int32_t pad;
+  int32_t expert[kEntries];
+  int32_t first[kEntries + 1];      // rows before the entry
+  int32_t tile[kEntries + 1];       // tiles before the entry
+  uint8_t token[kMaxRows];
 };
 constexpr int64_t kTableBytes = (sizeof(Table) + 255) & ~(int64_t)255;
 
 struct Routing {
   unsigned long long mask[kTokExperts];   // bit t: token t goes to the expert
-  int32_t act[kTokExperts];
-  int32_t first[kTokExperts + 1];
-  int32_t U;
+  int32_t expert[kEntries];
+  int32_t first[kEntries + 1];
+  int32_t entries;
   float zmax[kMaxTokens], zsum[kMaxTokens];
-  uint8_t token[kMaxTokens * kTokTopk];
-  float weight[kMaxTokens * kTokTopk];
+  uint8_t token[kMaxRows];
+  float weight[kMaxRows];
 };
 
 __device__ __forceinline__ float wave_max_f(float v) {
@@ -140,11 +173,11 @@ __device__ __forceinline__ void route_token(Routing& rt, const float* __restrict
   }
 }
 
-// The whole routing, by one workgroup.
-__device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, int E, int k) {
+// The whole routing, by one workgroup; entries of at most `group` rows.
+__device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, int E, int k, int group) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  for (int e = tid; e < E; e += kTokThreads) rt.mask[e] = 0;
+  for (int e = tid; e < E; e += kThreads) rt.mask[e] = 0;
   __syncthreads();
   for (int t = wave; t < T; t += kWaves) {
     const float* row = logits + (int64_t)t * E;
@@ -154,38 +187,40 @@ __device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, 
   }
   __syncthreads();
   if (wave == 0) {
-    int U = 0, rows = 0;
+    int V = 0, rows = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
-      const int n = e < E ? __popcll(rt.mask[e]) : 0;
-      const unsigned long long b = __ballot(n > 0);
-      int s = n;
+      const int n = e < E ? (int)__popcll(rt.mask[e]) : 0;
+      const int g = (n + group - 1) / group;
+      int s = n, v = g;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(s, d, 64);
-        if (lane >= d) s += o;
+        const int o = __shfl_up(s, d, 64), q = __shfl_up(v, d, 64);
+        if (lane >= d) {
+          s += o;
+          v += q;
+        }
       }
-      if (n > 0) {
-        const int u = U + __popcll(b & ((1ull << lane) - 1));
-        rt.act[u] = e;
-        rt.first[u] = rows + s - n;
+      for (int i = 0; i < g; ++i) {
+        rt.expert[V + v - g + i] = e;
+        rt.first[V + v - g + i] = rows + s - n + i * group;
       }
-      U += __popcll(b);
+      V += __shfl(v, 63, 64);
       rows += __shfl(s, 63, 64);
     }
     if (lane == 0) {
-      rt.first[U] = rows;
-      rt.U = U;
+      rt.first[V] = rows;
+      rt.entries = V;
     }
   }
   __syncthreads();
-  // a thread per (active expert, token)
-  for (int i = tid; i < 64 * rt.U; i += kTokThreads) {
+  // a thread per (entry, token); the entries of one expert share its mask
+  for (int i = tid; i < 64 * rt.entries; i += kThreads) {
     const int u = i >> 6, t = i & 63;
-    const int e = rt.act[u];
+    const int e = rt.expert[u];
     const unsigned long long m = rt.mask[e];
-    if (m >> t & 1u) {
-      const int r = rt.first[u] + __popcll(m & ((1ull << t) - 1));
+    if ((m >> t & 1u) && (u == 0 || rt.expert[u - 1] != e)) {
+      const int r = rt.first[u] + (int)__popcll(m & ((1ull << t) - 1));
       rt.token[r] = (uint8_t)t;
       rt.weight[r] = expf(logits[(int64_t)t * E + e] - rt.zmax[t]) / rt.zsum[t];
     }
@@ -201,127 +236,263 @@ struct TokensProblem {
   const uint16_t* residual;
   uint16_t* out;
   Table* table;
+  float* part;      // pieces of the output, or null: one workgroup per group of rows writes it
   uint16_t* a;
 };
 
-template <bool kMx>
-__device__ __forceinline__ WRows<kMx> expert_rows(const uint8_t* w, const uint8_t* s, int64_t e, int64_t E,
-                                                  int64_t rows, int64_t cols) {
-  WRows<kMx> m;
-  m.q = buf(w + e * rows * cols * (kMx ? 1 : 2), rows * cols * (kMx ? 1 : 2));
-  // scales of the expert's rows start 4 e rows into every panel
-  m.s = kMx ? buf(s + 4 * e * rows, ((cols + 127) / 128 * E - e) * rows * 4) : m.q;
-  m.panel = (uint32_t)(4 * E * rows);
-  return m;
+// ---------------------------------------------------------------- the stream
+__device__ __forceinline__ v4u rsrc(const void* base, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return v4u{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, (uint32_t)bytes, 0x00020000u};
 }
 
-// One step of the up kernel in flight: gate and up weights, and the tokens of
-// the item's first 16 rows.
-template <bool kMx>
-struct UpStep {
-  WStep<kMx> g, u;
-  XStep x;
-};
-
-// An item (active expert u, 16 columns f0 of F) as a wave walks it.
-template <bool kMx>
-struct UpItem {
-  WRows<kMx> w;
-  int32_t item, i, f0, lo, hi;   // i: the wave's step in the item
-  uint32_t off;                  // the lane's token row of the first tile
-};
-
-template <bool kMx>
-__device__ __forceinline__ void open_item(UpItem<kMx>& c, const TokensProblem& p, const Routing& rt, int item, int fb) {
-  const int u = item / fb;
-  const int e = __builtin_amdgcn_readfirstlane(rt.act[u]);
-  c.item = item;
-  c.i = 0;
-  c.f0 = 16 * (item - u * fb);
-  c.lo = __builtin_amdgcn_readfirstlane(rt.first[u]);
-  c.hi = __builtin_amdgcn_readfirstlane(rt.first[u + 1]);
-  c.w = expert_rows<kMx>(p.w1, p.w1_s, e, p.E, 2 * (int64_t)p.F, p.H);
-  const int row = c.lo + (threadIdx.x & 15);
-  c.off = row < c.hi ? 2u * (uint32_t)rt.token[row] * (uint32_t)p.H : kNoRow;
+// LDS-direct loads of 16 (4) bytes per lane to LDS byte lds + 16 (4) lane.
+// Inline asm, so that the compiler puts no wait of its own before LDS reads:
+// every wait on these loads is an explicit vmcnt.
+__device__ __forceinline__ void dma16(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "m0", "memory");
+}
+__device__ __forceinline__ void dma16_nt(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "m0", "memory");
+}
+__device__ __forceinline__ void dma4(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "m0", "memory");
 }
 
-// kTiles: most tiles of 16 tokens an expert can have.  The loads run kDepth - 1
-// steps ahead of the products, across items, so that the stream of weights does
-// not pause for the reduction at an item's end.
-template <bool kMx, int kTiles, int kDepth, int kOcc>
-__global__ void __launch_bounds__(kTokThreads, kOcc) k_tokens_up(TokensProblem p) {
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(const lds_void*)p; }
+
+constexpr int waitcnt_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+constexpr int kWaitLgkm0 = 0xF | (0x3 << 14) | (0x7 << 4);
+
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
+
+// A workgroup barrier for LDS alone: the loads in flight go on.
+__device__ __forceinline__ void lds_barrier() {
+  fence();
+  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+  __builtin_amdgcn_s_barrier();
+  fence();
+}
+
+// Elements of a 128-byte weight line.
+template <bool kMx> constexpr int kLineK = kMx ? 128 : 64;
+// 16-byte pieces of token elements that go with a lane's 32 weight bytes.
+template <bool kMx> constexpr int kXp = kMx ? 4 : 2;
+
+// A block of 16 weight rows x 128 bytes in LDS, its 16-byte chunks swizzled by
+// row so that a fragment's reads fall on all banks.  Load q (0, 1) of it covers
+// rows 8 q .. 8 q + 7: lane l holds row 8 q + l / 8.
+__device__ __forceinline__ int chunk_swizzle(int r) { return (r >> 1) & 7; }
+
+struct Fragment {
+  uint4 lo, hi;   // the lane's 32 bytes
+  uint32_t s;     // the panel dword of its row
+};
+
+__device__ __forceinline__ Fragment read_fragment(const uint8_t* block, const uint8_t* scales) {
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4, sw = chunk_swizzle(r);
+  Fragment f;
+  f.lo = *reinterpret_cast<const uint4*>(block + r * 128 + 16 * ((2 * h) ^ sw));
+  f.hi = *reinterpret_cast<const uint4*>(block + r * 128 + 16 * ((2 * h + 1) ^ sw));
+  f.s = *reinterpret_cast<const uint32_t*>(scales + 4 * r);
+  return f;
+}
+
+// The lane's weights of instruction i as bf16.
+template <bool kMx>
+__device__ __forceinline__ v8bf weights8(const Fragment& f, int i, float scale) {
+  if constexpr (kMx) {
+    const uint4& c = i < 2 ? f.lo : f.hi;
+    const uint2 a = cvt4_bf16((i & 1) ? c.z : c.x, scale), b = cvt4_bf16((i & 1) ? c.w : c.y, scale);
+    return __builtin_bit_cast(v8bf, make_uint4(a.x, a.y, b.x, b.y));
+  } else {
+    return __builtin_bit_cast(v8bf, i == 0 ? f.lo : f.hi);
+  }
+}
+
+template <bool kMx>
+__device__ __forceinline__ float fragment_scale(const Fragment& f) {
+  return kMx ? e8m0_to_f32((f.s >> (8 * ((threadIdx.x & 63) >> 4))) & 0xFFu) : 1.0f;
+}
+
+// Scales of an expert's rows start 4 e rows into every panel.
+__device__ __forceinline__ v4u scale_rsrc(const uint8_t* s, int64_t e, int64_t E, int64_t rows, int64_t cols) {
+  return rsrc(s + 4 * e * rows, ((cols + 127) / 128 * E - e) * rows * 4);
+}
+
+// ---------------------------------------------------------------- up
+constexpr int kUpDepth = 3;                        // steps of a wave in flight
+constexpr int kUpSlot = 2 * 2048 + 256;            // gate and up blocks, their scale dwords
+
+// kSteps: steps of a wave whose tokens stay in registers, for kTiles tiles of
+// 16 tokens (128 registers in all).  kSteps * 8 lines cover H, or the tokens
+// are read again for each item.
+template <bool kMx, int kSteps, int kTiles>
+__global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
   __shared__ Routing rt;
-  __shared__ float red[kWaves][2][4][64];
+  __shared__ __attribute__((aligned(16))) float red[kWaves][2][4][64];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kWaves][kUpDepth][kUpSlot];
+  constexpr int kOps = kMx ? 5 : 4, eb = kMx ? 1 : 2, kK = kLineK<kMx>, kP = kXp<kMx>;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int r = lane & 15;
-  route_all(rt, p.logits, p.T, p.E, p.k);
-  const int U = __builtin_amdgcn_readfirstlane(rt.U);
+  const int r = lane & 15, h = lane >> 4;
+  route_all(rt, p.logits, p.T, p.E, p.k, 16 * kTiles);
+  const int V = __builtin_amdgcn_readfirstlane(rt.entries);
   if (blockIdx.x == 0) {
-    if (tid == 0) {
-      p.table->U = U;
-      p.table->rows = rt.first[U];
-    }
-    for (int u = tid; u < U; u += kTokThreads) p.table->act[u] = rt.act[u];
-    for (int u = tid; u <= U; u += kTokThreads) p.table->first[u] = rt.first[u];
-    for (int i = tid; i < rt.first[U]; i += kTokThreads) p.table->token[i] = rt.token[i];
-  }
-  const int fb = p.F / 16, items = U * fb;
-  if ((int)blockIdx.x >= items) return;
-  const uint32_t H = (uint32_t)p.H;
-  // a wave takes steps wave, wave + 8, ...; every wave as many (those past H read zeros)
-  const int per = ((p.H + kStepK - 1) / kStepK + kWaves - 1) / kWaves;
-  const __amdgpu_buffer_rsrc_t xr = buf(p.x, (int64_t)p.T * p.H * 2);
-  UpItem<kMx> ld, cur;
-  open_item(ld, p, rt, blockIdx.x, fb);
-  cur = ld;
-  bool more = true;
-  UpStep<kMx> st[kDepth];
-  auto load = [&](UpStep<kMx>& s) {
-    if (!more) return;
-    const uint32_t k0 = (uint32_t)(wave + kWaves * ld.i) * kStepK;
-    load_w<kMx>(s.g, ld.w, (uint32_t)(ld.f0 + r), H, k0, true);
-    load_w<kMx>(s.u, ld.w, (uint32_t)(p.F + ld.f0 + r), H, k0, true);
-    load_x(s.x, xr, ld.off, H, k0);
-    if (++ld.i == per) {
-      more = ld.item + (int)gridDim.x < items;
-      if (more) open_item(ld, p, rt, ld.item + gridDim.x, fb);
-    }
-  };
-  v4f_s g[kTiles], up[kTiles];
+    for (int u = tid; u < V; u += kThreads) p.table->expert[u] = rt.expert[u];
+    for (int u = tid; u <= V; u += kThreads) p.table->first[u] = rt.first[u];
+    for (int i = tid; i < rt.first[V]; i += kThreads) p.table->token[i] = rt.token[i];
+    if (wave == 0) {   // tiles before each entry
+      int before = 0;
+      for (int u0 = 0; u0 < V; u0 += 64) {
+        const int u = u0 + lane;
+        const int n = u < V ? (rt.first[u + 1] - rt.first[u] + 15) / 16 : 0;
+        int s = n;
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) g[t] = up[t] = v4f_s{0.f, 0.f, 0.f, 0.f};
-  // one step's products; false after the workgroup's last item
-  auto step = [&](UpStep<kMx>& s) -> bool {
-    mma_step<kMx>(g[0], s.g, s.x);
-    mma_step<kMx>(up[0], s.u, s.x);
-#pragma unroll
-    for (int t = 1; t < kTiles; ++t) {
-      if (cur.lo + 16 * t < cur.hi) {   // an expert with more than 16 tokens
-        const int row = cur.lo + 16 * t + r;
-        XStep x;
-        load_x(x, xr, row < cur.hi ? 2u * (uint32_t)rt.token[row] * H : kNoRow, H,
-               (uint32_t)(wave + kWaves * cur.i) * kStepK);
-        mma_step<kMx>(g[t], s.g, x);
-        mma_step<kMx>(up[t], s.u, x);
+        for (int d = 1; d < 64; d <<= 1) {
+          const int o = __shfl_up(s, d, 64);
+          if (lane >= d) s += o;
+        }
+        if (u < V) p.table->tile[u] = before + s - n;
+        before += __shfl(s, 63, 64);
+      }
+      if (lane == 0) {
+        p.table->tile[V] = before;
+        p.table->tiles = before;
+        p.table->entries = V;
+        p.table->rows = rt.first[V];
       }
     }
-    load(s);
-    if (++cur.i < per) return true;
+  }
+  const int fb = p.F / 16, items = V * fb;
+  const int begin = (int)((int64_t)items * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+  if (begin >= end) return;
+  const int lines = (p.H * eb + 127) / 128;
+  const int per = (lines + kWaves - 1) / kWaves;   // a wave takes lines wave, wave + 8, ...
+  const int64_t rows = 2 * (int64_t)p.F, row_bytes = (int64_t)p.H * eb;
+
+  // the loads' cursor
+  int li = begin, ls = 0, lf = 0, seq = 0;
+  v4u lq, lsc;
+  auto open = [&](int item) {
+    const int u = item / fb;
+    const int64_t e = __builtin_amdgcn_readfirstlane(rt.expert[u]);
+    lf = 16 * (item - u * fb);
+    lq = rsrc(p.w1 + e * rows * row_bytes, rows * row_bytes);
+    if constexpr (kMx) lsc = scale_rsrc(p.w1_s, e, p.E, rows, p.H);
+  };
+  open(begin);
+  const int lr = lane >> 3, ch = (lane & 7);
+  auto load = [&]() {
+    const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kUpDepth) * kUpSlot;
+    const int line = wave + kWaves * ls;
+    const bool in = li < end && line < lines;
+    const uint32_t soff = in ? 128u * (uint32_t)line : 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 8 * (q & 1) + lr;
+      const int c = 16 * (ch ^ chunk_swizzle(row));
+      const bool ok = in & ((int64_t)soff + c < row_bytes);
+      const uint32_t off = (uint32_t)((q >> 1) * p.F + lf + row) * (uint32_t)row_bytes + (uint32_t)c;
+      dma16_nt(lq, dst + 1024u * q, ok ? off : kOob, soff);
+    }
+    if constexpr (kMx) {
+      const uint32_t off = 4u * (uint32_t)((lane >> 4) * p.F + lf + r);
+      dma4(lsc, dst + 4096u, (in && lane < 32) ? off : kOob, in ? (uint32_t)line * (uint32_t)(4 * p.E * rows) : 0u);
+    }
+    ++seq;
+    if (++ls == per) {
+      ls = 0;
+      if (++li < end) open(li);
+    }
+  };
+
+  // the tokens of `line` .. of the entry's tiles
+  v8bf x[kTiles][kSteps][kP];
+  auto tokens = [&](int lo, int hi, int s0) {
+    const __amdgpu_buffer_rsrc_t xr =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.x), (short)0, (int)(2 * p.T * p.H), 0x00020000);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      if (cur.lo + 16 * t < cur.hi) {
+      const int row = lo + 16 * t + r;
+      const uint32_t base = row < hi ? 2u * (uint32_t)rt.token[row] * (uint32_t)p.H : kOob;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int k = (wave + kWaves * (s0 + s)) * kK + kK / 4 * h;
+        const uint32_t off = (row < hi && k < p.H) ? base + 2u * (uint32_t)k : kOob;
+#pragma unroll
+        for (int j = 0; j < kP; ++j)
+          x[t][s][j] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)off + 16 * j, 0, 0));
+      }
+    }
+    // waited for here, once: a wait at each use would also drain the stream
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  };
+
+#pragma unroll
+  for (int d = 0; d < kUpDepth; ++d) load();
+  int entry = -1, used = 0;
+  for (int item = begin; item < end; ++item) {
+    const int u = item / fb, f0 = 16 * (item - u * fb);
+    const int lo = __builtin_amdgcn_readfirstlane(rt.first[u]), hi = __builtin_amdgcn_readfirstlane(rt.first[u + 1]);
+    v4f g[kTiles], up[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) g[t] = up[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < per; s0 += kSteps) {
+      if (u != entry || per > kSteps) tokens(lo, hi, s0);
+      entry = u;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (s0 + s < per) {
+          // the oldest step's loads are done, the others may be in flight
+          fence();
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm(kOps * (kUpDepth - 1)));
+          fence();
+          const uint8_t* slot = ring[wave][used % kUpDepth];
+          const Fragment fg = read_fragment(slot, slot + 4096), fu = read_fragment(slot + 2048, slot + 4096 + 64);
+          fence();
+          __builtin_amdgcn_s_waitcnt(kWaitLgkm0);   // read: the slot is free
+          fence();
+          load();
+          ++used;
+          const float sg = fragment_scale<kMx>(fg), su = fragment_scale<kMx>(fu);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) {
+            const v8bf wg = weights8<kMx>(fg, j, sg), wu = weights8<kMx>(fu, j, su);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              if (t == 0 || lo + 16 * t < hi) {
+                g[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wg, x[t][s][j], g[t], 0, 0, 0);
+                up[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wu, x[t][s][j], up[t], 0, 0, 0);
+              }
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      if (lo + 16 * t < hi) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           red[wave][0][i][lane] = g[t][i];
           red[wave][1][i][lane] = up[t][i];
         }
-        g[t] = up[t] = v4f_s{0.f, 0.f, 0.f, 0.f};
-        __syncthreads();
+        lds_barrier();
         // thread (token c, row f of 16): the waves' partial sums in order
         const int c = tid >> 4, f = tid & 15;
-        const int row = cur.lo + 16 * t + c;
-        if (tid < 256 && row < cur.hi) {
+        const int row = lo + 16 * t + c;
+        if (tid < 256 && row < hi) {
           float sg = 0.0f, su = 0.0f;
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) {
@@ -329,152 +500,282 @@ __global__ void __launch_bounds__(kTokThreads, kOcc) k_tokens_up(TokensProblem p
             su += red[w][1][f & 3][16 * (f >> 2) + c];
           }
           const float a = rt.weight[row] * (sg / (1.0f + expf(-sg)) * su);
-          p.a[(int64_t)row * p.F + cur.f0 + f] = (uint16_t)bf16x2_rne(a, a);
+          p.a[(int64_t)row * p.F + f0 + f] = (uint16_t)bf16x2_rne(a, a);
         }
-        __syncthreads();
+        lds_barrier();
       }
     }
-    if (cur.item + (int)gridDim.x >= items) return false;
-    open_item(cur, p, rt, cur.item + gridDim.x, fb);
-    return true;
-  };
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(st[d]);
-  bool on = true;
-  while (on) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) on = on && step(st[d]);
   }
+  // loads past the last item may still be writing LDS
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
 }
 
-// One step of the down kernel in flight.
-template <bool kMx>
-struct DownStep {
-  WStep<kMx> w;
-  XStep x;
-};
+// ---------------------------------------------------------------- down
+constexpr int kGroupRows = 16 * kWaves;            // output rows of a workgroup
+constexpr int kDownDepth = 2;                      // chunks of a wave in flight
+constexpr int kDownSlot = 2 * 2048 + 256;          // two lines of 16 rows, their scale dwords
+constexpr int kXSlots = 3;
+
+// Units of work: (group of rows, entry, chunk of two lines, tile), the tile
+// innermost so that an entry's later tiles find the chunk in the cache.
+// Workgroup b of B takes [total b / B, total (b + 1) / B).
+__device__ __forceinline__ int64_t share(int64_t total, int64_t b, int64_t B) { return total * b / B; }
+
+// The workgroup whose share holds unit x (total > 0).
+__device__ __forceinline__ int64_t owner(int64_t total, int64_t x, int64_t B) {
+  int64_t b = x * B / total;
+  while (share(total, b + 1, B) <= x) ++b;
+  while (share(total, b, B) > x) --b;
+  return b;
+}
 
 template <bool kMx>
-struct DownUnit {
-  WRows<kMx> w;
-  int32_t c, s, s1, lo, hi;   // the unit; its step and end
-  uint32_t off;
-};
-
-// Steps of a unit, the share of one expert's F that a wave takes at a time.
-constexpr int kUnitSteps = 4;
-
-// kNw waves: eight where the output's 16-row blocks give every CU two
-// workgroups, sixteen where they are fewer.
-template <bool kMx, int kNw, int kDepth, int kOcc>
-__global__ void __launch_bounds__(64 * kNw, kOcc) k_tokens_down(TokensProblem p) {
-  __shared__ int32_t act[kTokExperts], first[kTokExperts + 1];
-  __shared__ uint8_t token[kMaxTokens * kTokTopk];
-  __shared__ float sum[kNw][kMaxTokens][16];
-  constexpr int kThreads = 64 * kNw;
+__global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
+  constexpr int kOps = kMx ? 6 : 5, eb = kMx ? 1 : 2, kK = kLineK<kMx>, kP = kXp<kMx>;
+  constexpr int kXRow = 2 * kK * 2;                // bytes of a token row of a chunk
+  __shared__ int32_t expert[kEntries], first[kEntries + 1], tile[kEntries + 1];
+  __shared__ uint8_t token[kMaxRows];
+  __shared__ __attribute__((aligned(16))) float sum[kWaves][kMaxTokens][16];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kWaves][kDownDepth][kDownSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t xs[kXSlots][16 * kXRow];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, h = lane >> 4;
-  const int U = __builtin_amdgcn_readfirstlane(p.table->U);
+  const int V = __builtin_amdgcn_readfirstlane(p.table->entries);
   const int rows = __builtin_amdgcn_readfirstlane(p.table->rows);
-  for (int u = tid; u < U; u += kThreads) act[u] = p.table->act[u];
-  for (int u = tid; u <= U; u += kThreads) first[u] = p.table->first[u];
+  const int tiles = __builtin_amdgcn_readfirstlane(p.table->tiles);
+  for (int u = tid; u < V; u += kThreads) expert[u] = p.table->expert[u];
+  for (int u = tid; u <= V; u += kThreads) {
+    first[u] = p.table->first[u];
+    tile[u] = p.table->tile[u];
+  }
   for (int i = tid; i < rows; i += kThreads) token[i] = p.table->token[i];
   for (int i = lane; i < 16 * p.T; i += 64) (&sum[wave][0][0])[i] = 0.0f;
   __syncthreads();
-  const uint32_t n0 = 16 * blockIdx.x, F = (uint32_t)p.F;
-  const int steps = (p.F + kStepK - 1) / kStepK;
-  const int per = (steps + kUnitSteps - 1) / kUnitSteps;
-  const int units = U * per;
-  const __amdgpu_buffer_rsrc_t ar = buf(p.a, (int64_t)rows * p.F * 2);
-  auto open = [&](DownUnit<kMx>& q, int c) {
-    const int u = c / per;
-    q.c = c;
-    q.s = (c - u * per) * kUnitSteps;
-    q.s1 = q.s + kUnitSteps < steps ? q.s + kUnitSteps : steps;
-    const int e = __builtin_amdgcn_readfirstlane(act[u]);
-    q.lo = __builtin_amdgcn_readfirstlane(first[u]);
-    q.hi = __builtin_amdgcn_readfirstlane(first[u + 1]);
-    q.w = expert_rows<kMx>(p.w2, p.w2_s, e, p.E, p.H, p.F);
-    q.off = q.lo + r < q.hi ? 2u * (uint32_t)(q.lo + r) * F : kNoRow;
-  };
-  if (wave < units) {
-    DownUnit<kMx> ld, cur;
-    open(ld, wave);
-    cur = ld;
-    bool more = true;
-    DownStep<kMx> st[kDepth];
-    auto load = [&](DownStep<kMx>& s) {
-      if (!more) return;
-      load_w<kMx>(s.w, ld.w, n0 + r, F, (uint32_t)(ld.s * kStepK), true);
-      load_x(s.x, ar, ld.off, F, (uint32_t)(ld.s * kStepK));
-      if (++ld.s == ld.s1) {
-        more = ld.c + kNw < units;
-        if (more) open(ld, ld.c + kNw);
+  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  const int64_t row_bytes = (int64_t)p.F * eb;
+  const int chunks = (int)((row_bytes + 255) / 256);
+  const int64_t each = (int64_t)tiles * chunks;    // units of a group
+  const int64_t total = groups * each;
+  const int64_t u0 = share(total, blockIdx.x, gridDim.x), u1 = share(total, blockIdx.x + 1, gridDim.x);
+
+  // a group's sums to their place: lane's 4 rows of 16 for each token
+  auto put = [&](int64_t g) {
+    const int64_t n0 = g * kGroupRows + 16 * wave;
+    if (n0 < p.H) {
+      float* part = nullptr;
+      if (p.part) part = p.part + (blockIdx.x - owner(total, g * each, gridDim.x)) * p.T * (int64_t)p.H;
+      for (int i = lane; i < 16 * p.T; i += 64) {
+        const int t = i >> 4;
+        const int64_t at = (int64_t)t * p.H + n0 + (i & 15);
+        float v = (&sum[wave][0][0])[i];
+        (&sum[wave][0][0])[i] = 0.0f;
+        if (part) {
+          part[at] = v;
+        } else {
+          if (p.residual) v += __uint_as_float((uint32_t)p.residual[at] << 16);
+          p.out[at] = (uint16_t)bf16x2_rne(v, v);
+        }
       }
-    };
-    // the lane's sums of one tile's token
-    auto flush = [&](const v4f_s& y, int row) {
-      if (row < cur.hi) {
-        float* d = sum[wave][token[row]] + 4 * h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] += y[i];
-      }
-    };
-    v4f_s y = {0.f, 0.f, 0.f, 0.f};
-    // one step's products; false after the wave's last unit
-    auto step = [&](DownStep<kMx>& s) -> bool {
-      mma_step<kMx>(y, s.w, s.x);
-      for (int row0 = cur.lo + 16; row0 < cur.hi; row0 += 16) {   // an expert with more than 16 tokens
-        XStep x;
-        load_x(x, ar, row0 + r < cur.hi ? 2u * (uint32_t)(row0 + r) * F : kNoRow, F, (uint32_t)(cur.s * kStepK));
-        v4f_s z = {0.f, 0.f, 0.f, 0.f};
-        mma_step<kMx>(z, s.w, x);
-        flush(z, row0 + r);
-      }
-      load(s);
-      if (++cur.s < cur.s1) return true;
-      flush(y, cur.lo + r);
-      y = v4f_s{0.f, 0.f, 0.f, 0.f};
-      if (cur.c + kNw >= units) return false;
-      open(cur, cur.c + kNw);
-      return true;
-    };
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(st[d]);
-    bool on = true;
-    while (on) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) on = on && step(st[d]);
     }
+  };
+  if (u0 >= u1) {
+    // (without pieces a workgroup owns its group even if no expert is active)
+    if (!p.part && blockIdx.x < groups) put(blockIdx.x);
+    return;
   }
-  __syncthreads();
-  for (int i = tid; i < 16 * p.T; i += kThreads) {
-    const int t = i >> 4, n = i & 15;
-    float v = p.residual ? __uint_as_float((uint32_t)p.residual[(int64_t)t * p.H + n0 + n] << 16) : 0.0f;
+
+  struct Unit {
+    int64_t g;
+    int32_t u, c, t, nt;   // entry, chunk, tile of nt
+  };
+  auto at = [&](int64_t x) {
+    Unit q;
+    q.g = x / each;
+    const int64_t y = x - q.g * each;
+    int a = 0, b = V;      // tile[a] * chunks <= y < tile[b] * chunks
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if ((int64_t)__builtin_amdgcn_readfirstlane(tile[m]) * chunks <= y) a = m; else b = m;
+    }
+    const int before = __builtin_amdgcn_readfirstlane(tile[a]);
+    q.u = a;
+    q.nt = __builtin_amdgcn_readfirstlane(tile[a + 1]) - before;
+    const int in = (int)(y - (int64_t)before * chunks);
+    q.c = in / q.nt;
+    q.t = in - q.c * q.nt;
+    return q;
+  };
+  auto next = [&](Unit& q) {
+    if (++q.t < q.nt) return;
+    q.t = 0;
+    if (++q.c < chunks) return;
+    q.c = 0;
+    if (++q.u == V) {
+      q.u = 0;
+      ++q.g;
+    }
+    q.nt = __builtin_amdgcn_readfirstlane(tile[q.u + 1]) - __builtin_amdgcn_readfirstlane(tile[q.u]);
+  };
+
+  Unit ld = at(u0), cur = ld;
+  int64_t issued = u0;
+  const v4u ar = rsrc(p.a, (int64_t)rows * p.F * 2);
+  const int lr = lane >> 3, ch = lane & 7;
+  auto load = [&]() {
+    const bool on = issued < u1;
+    const int seq = (int)(issued - u0);
+    const int64_t e = __builtin_amdgcn_readfirstlane(expert[ld.u]);
+    const int64_t n0 = ld.g * kGroupRows + 16 * wave;
+    const bool in = on && n0 < p.H;
+    const v4u wq = rsrc(p.w2 + e * p.H * row_bytes, p.H * row_bytes);
+    const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kDownDepth) * kDownSlot;
 #pragma unroll
-    for (int w = 0; w < kNw; ++w) v += sum[w][t][n];
-    p.out[(int64_t)t * p.H + n0 + n] = (uint16_t)bf16x2_rne(v, v);
+    for (int q = 0; q < 4; ++q) {
+      const int row = 8 * (q & 1) + lr;
+      const int c = 16 * (ch ^ chunk_swizzle(row));
+      const int64_t k = 256 * (int64_t)ld.c + 128 * (q >> 1) + c;
+      const bool ok = in & (k < row_bytes);
+      const uint32_t off = (uint32_t)(n0 + row) * (uint32_t)row_bytes + (uint32_t)k;
+      dma16_nt(wq, dst + 1024u * q, ok ? off : kOob, 0);
+    }
+    if constexpr (kMx) {   // lanes 0..15: the first line's scale dwords, 16..31 the second's
+      const v4u sr = scale_rsrc(p.w2_s, e, p.E, p.H, p.F);
+      const int64_t panel = 2 * (int64_t)ld.c + (lane >> 4);
+      const bool ok = in & (lane < 32) & (128 * panel < p.F);
+      const uint32_t off = (uint32_t)(panel * 4 * p.E * p.H) + 4u * (uint32_t)(n0 + r);
+      dma4(sr, dst + 4096u, ok ? off : kOob, 0);
+    }
+    // this wave's two token rows of the chunk
+    const uint32_t xd = lds_addr(xs[0]) + (uint32_t)(seq % kXSlots) * (16 * kXRow) + (uint32_t)wave * (2 * kXRow);
+    constexpr int kChunks = kXRow / 16;            // 16-byte chunks of a token row
+    if (lane < 2 * kChunks) {
+      const int rl = 2 * wave + lane / kChunks;
+      const int c = (lane % kChunks) ^ (rl & 15);
+      const int row = __builtin_amdgcn_readfirstlane(first[ld.u]) + 16 * ld.t + rl;
+      const int k = ld.c * 2 * kK + 8 * c;
+      const bool ok = on & (row < __builtin_amdgcn_readfirstlane(first[ld.u + 1])) & (k < p.F);
+      dma16(ar, xd, ok ? 2u * ((uint32_t)row * (uint32_t)p.F + (uint32_t)k) : kOob, 0);
+    }
+    ++issued;
+    if (issued < u1) next(ld);
+  };
+
+#pragma unroll
+  for (int d = 0; d < kDownDepth; ++d) load();
+  for (int64_t x = u0; x < u1; ++x) {
+    const int seq = (int)(x - u0);
+    // this unit's loads are done, the next one's may be in flight; after the
+    // barrier every wave's token rows are there, and every wave has read the
+    // token slot that the loads below overwrite (two units ago)
+    fence();
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kOps * (kDownDepth - 1)));
+    lds_barrier();
+    const uint8_t* slot = ring[wave][seq % kDownDepth];
+    const uint8_t* xt = xs[seq % kXSlots] + r * kXRow;
+    Fragment f[2];
+    v8bf xv[2][kP];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[i] = read_fragment(slot + 2048 * i, slot + 4096 + 64 * i);
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+        xv[i][j] = *reinterpret_cast<const v8bf*>(xt + 16 * ((4 * kP * i + kP * h + j) ^ r));
+    }
+    fence();
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);        // read: the ring's slot is free
+    fence();
+    load();
+    v4f y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = fragment_scale<kMx>(f[i]);
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<kMx>(f[i], j, s), xv[i][j], y, 0, 0, 0);
+    }
+    const int row = __builtin_amdgcn_readfirstlane(first[cur.u]) + 16 * cur.t + r;
+    if (row < __builtin_amdgcn_readfirstlane(first[cur.u + 1])) {   // the lane owns 4 sums of its token
+      float4* d = reinterpret_cast<float4*>(sum[wave][token[row]] + 4 * h);
+      float4 v = *d;
+      v.x += y[0];
+      v.y += y[1];
+      v.z += y[2];
+      v.w += y[3];
+      *d = v;
+    }
+    const int64_t g = cur.g;
+    next(cur);
+    if (cur.g != g || x + 1 == u1) put(g);
   }
+  // loads past the last unit may still be writing LDS
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
 }
 
-constexpr int kCus = 256;   // MI355X
+// The pieces of a group in the workgroups' order, the residual, the rounding.
+__global__ void __launch_bounds__(256) k_tokens_join(TokensProblem p, int32_t line_bytes, int32_t blocks) {
+  const int64_t i = 2 * ((int64_t)blockIdx.x * 256 + threadIdx.x);   // two columns of a token
+  if (i >= (int64_t)p.T * p.H) return;
+  const int64_t n = i % p.H;
+  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  const int64_t each = (int64_t)p.table->tiles * ((line_bytes + 255) / 256);
+  const int64_t total = groups * each;
+  float a = 0.0f, b = 0.0f;
+  if (p.residual) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p.residual + i);
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+  }
+  if (total > 0) {
+    const int64_t g = n / kGroupRows;
+    const int64_t b0 = owner(total, g * each, blocks), b1 = owner(total, (g + 1) * each - 1, blocks);
+    for (int64_t s = 0; s <= b1 - b0; ++s) {
+      const float2 v = *reinterpret_cast<const float2*>(p.part + s * p.T * p.H + i);
+      a += v.x;
+      b += v.y;
+    }
+  }
+  *reinterpret_cast<uint32_t*>(p.out + i) = bf16x2_rne(a, b);
+}
+
+// Pieces of one group at most, times its columns over the card: where the
+// groups are at most kCus, (kCus / groups + 2) * 128 groups.
+constexpr int64_t kPartCols = 128 * 3 * (int64_t)kCus;
+
+// Whether the groups' work is cut over the card: not where they fill it, nor
+// where there is less than two units for every CU.
+bool cut(const TokensProblem& p, bool mxw) {
+  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  const int64_t pairs = (int64_t)p.T * p.k;
+  const int64_t units = (p.E < pairs ? p.E : pairs) * (((int64_t)p.F * (mxw ? 1 : 2) + 255) / 256) * groups;
+  return groups < kCus && units > 2 * kCus;
+}
 
 template <bool kMx>
-int launch_tokens(const TokensProblem& p, hipStream_t st) {
-  const int64_t most = (int64_t)(p.E < p.T * p.k ? p.E : p.T * p.k) * (p.F / 16);
-  // one up workgroup per CU with four (three) steps in flight per wave: 77 us for
-  // one token of the 64-expert layer, against 84 with two workgroups and two steps
-  const dim3 up((unsigned)(most < kCus ? most : kCus)), down(p.H / 16);
-  if (p.T <= 16) hipLaunchKernelGGL((k_tokens_up<kMx, 1, 4, 2>), up, dim3(kTokThreads), 0, st, p);
-  else hipLaunchKernelGGL((k_tokens_up<kMx, kMaxTokens / 16, 3, 2>), up, dim3(kTokThreads), 0, st, p);
-  if (down.x > kCus) hipLaunchKernelGGL((k_tokens_down<kMx, 8, 3, 4>), down, dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((k_tokens_down<kMx, 16, 3, 4>), down, dim3(1024), 0, st, p);
+int launch_tokens(TokensProblem p, hipStream_t st) {
+  const int64_t pairs = (int64_t)p.T * p.k;
+  const int64_t most = ((p.E < pairs ? p.E : pairs) + pairs / 16) * (p.F / 16);
+  const dim3 up((unsigned)(most < kCus ? most : kCus));
+  // steps of 8 waves x 128 bytes; registers hold 8 (fp8) or 16 (bf16) of one tile
+  constexpr int kLong = kMx ? 8 : 16;
+  if (p.T <= 16 || p.H > 4096) hipLaunchKernelGGL((k_tokens_up<kMx, kLong, 1>), up, dim3(kThreads), 0, st, p);
+  else if (p.H > 2048) hipLaunchKernelGGL((k_tokens_up<kMx, kLong / 2, 2>), up, dim3(kThreads), 0, st, p);
+  else hipLaunchKernelGGL((k_tokens_up<kMx, kLong / 4, 4>), up, dim3(kThreads), 0, st, p);
+  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  if (cut(p, kMx)) {
+    hipLaunchKernelGGL(k_tokens_down<kMx>, dim3(kCus), dim3(kThreads), 0, st, p);
+    const int64_t n = (int64_t)p.T * p.H / 2;
+    hipLaunchKernelGGL(k_tokens_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p,
+                       (int32_t)(p.F * (kMx ? 1 : 2)), (int32_t)kCus);
+  } else {
+    p.part = nullptr;
+    hipLaunchKernelGGL(k_tokens_down<kMx>, dim3((unsigned)groups), dim3(kThreads), 0, st, p);
+  }
   return launch_status();
 }
 
 int64_t tokens_bytes(int64_t tokens, int64_t topk, int64_t F) {
-  return kTableBytes + ((tokens * topk * F * 2 + 255) & ~(int64_t)255);
+  return kTableBytes + 4 * tokens * kPartCols + ((tokens * topk * F * 2 + 255) & ~(int64_t)255);
 }
 
 int tokens_call(bool mxw, const uint16_t* x, const float* logits, int64_t tokens, int32_t topk, int32_t E, int64_t H,
@@ -484,7 +785,7 @@ int tokens_call(bool mxw, const uint16_t* x, const float* logits, int64_t tokens
   if (!x || !logits || !w1 || !w2 || !out || !ws || (mxw && (!w1_s || !w2_s))) return MX_EINVAL;
   if (((uintptr_t)x | (uintptr_t)w1 | (uintptr_t)w2 | (uintptr_t)ws) & 15) return MX_EINVAL;
   if (((uintptr_t)logits | (uintptr_t)w1_s | (uintptr_t)w2_s) & 3) return MX_EINVAL;
-  if (((uintptr_t)out | (uintptr_t)residual) & 1) return MX_EINVAL;
+  if (((uintptr_t)out | (uintptr_t)residual) & 3) return MX_EINVAL;
   if (tokens > kMaxTokens || E > kTokExperts || topk > kTokTopk) return MX_EUNSUPPORTED;
   // one expert's matrix and the scales are addressed with 31-bit byte offsets
   const int64_t eb = mxw ? 1 : 2;
@@ -509,7 +810,8 @@ int tokens_call(bool mxw, const uint16_t* x, const float* logits, int64_t tokens
   p.residual = residual;
   p.out = out;
   p.table = static_cast<Table*>(ws);
-  p.a = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kTableBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kTableBytes);
+  p.a = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kTableBytes + 4 * tokens * kPartCols);
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   return mxw ? launch_tokens<true>(p, st) : launch_tokens<false>(p, st);
 }
