@@ -85,16 +85,33 @@ struct Routing {
   float weight[kMaxRows];
 };
 
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+// Reductions over the wave by DPP: rows of 16 lanes, then their last lanes
+// into the rows after them; lane 63 holds the result.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old), (int)__float_as_uint(v), kCtrl,
+                                                               kRows, 0xF, false));
 }
-
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max_f(float v) {
+  v = fmaxf(v, dpp<0x111, 0xF>(v, v));        // row_shr 1, 2, 4, 8 (a lane without a source keeps its own)
+  v = fmaxf(v, dpp<0x112, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x114, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x118, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x142, 0xA>(v, v));        // row_bcast 15 into rows 1 and 3
+  v = fmaxf(v, dpp<0x143, 0xC>(v, v));        // row_bcast 31 into rows 2 and 3
+  return last_lane(v);
+}
 __device__ __forceinline__ float wave_add_f(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  v += dpp<0x111, 0xF>(0.0f, v);
+  v += dpp<0x112, 0xF>(0.0f, v);
+  v += dpp<0x114, 0xF>(0.0f, v);
+  v += dpp<0x118, 0xF>(0.0f, v);
+  v += dpp<0x142, 0xA>(0.0f, v);
+  v += dpp<0x143, 0xC>(0.0f, v);
+  return last_lane(v);
 }
 
 // Order-preserving integer key of a float (-0 as +0).
@@ -173,8 +190,8 @@ __device__ __forceinline__ void route_token(Routing& rt, const float* __restrict
   }
 }
 
-// The whole routing, by one workgroup; entries of at most `group` rows.
-__device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, int E, int k, int group) {
+// The routing, by one workgroup: entries of at most `group` rows ...
+__device__ __forceinline__ void route_entries(Routing& rt, const float* __restrict__ logits, int T, int E, int k, int group) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   for (int e = tid; e < E; e += kThreads) rt.mask[e] = 0;
@@ -214,7 +231,12 @@ __device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, 
     }
   }
   __syncthreads();
-  // a thread per (entry, token); the entries of one expert share its mask
+}
+
+// ... and then their rows' tokens and weights: a thread per (entry, token);
+// the entries of one expert share its mask.  (The caller's barrier follows.)
+__device__ __forceinline__ void route_rows(Routing& rt, const float* __restrict__ logits, int E) {
+  const int tid = threadIdx.x;
   for (int i = tid; i < 64 * rt.entries; i += kThreads) {
     const int u = i >> 6, t = i & 63;
     const int e = rt.expert[u];
@@ -225,7 +247,6 @@ __device__ void route_all(Routing& rt, const float* __restrict__ logits, int T, 
       rt.weight[r] = expf(logits[(int64_t)t * E + e] - rt.zmax[t]) / rt.zsum[t];
     }
   }
-  __syncthreads();
 }
 
 struct TokensProblem {
@@ -333,6 +354,36 @@ __device__ __forceinline__ v4u scale_rsrc(const uint8_t* s, int64_t e, int64_t E
 constexpr int kUpDepth = 3;                        // steps of a wave in flight
 constexpr int kUpSlot = 2 * 2048 + 256;            // gate and up blocks, their scale dwords
 
+// The table for the down kernel, by one workgroup.
+__device__ void write_table(const Routing& rt, Table* table) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int V = rt.entries, rows = rt.first[V];
+  for (int u = tid; u < V; u += kThreads) table->expert[u] = rt.expert[u];
+  for (int u = tid; u <= V; u += kThreads) table->first[u] = rt.first[u];
+  for (int i = tid; i < rows; i += kThreads) table->token[i] = rt.token[i];
+  if (tid < 64) {   // tiles before each entry
+    int before = 0;
+    for (int u0 = 0; u0 < V; u0 += 64) {
+      const int u = u0 + lane;
+      const int n = u < V ? (rt.first[u + 1] - rt.first[u] + 15) / 16 : 0;
+      int s = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(s, d, 64);
+        if (lane >= d) s += o;
+      }
+      if (u < V) table->tile[u] = before + s - n;
+      before += __shfl(s, 63, 64);
+    }
+    if (lane == 0) {
+      table->tile[V] = before;
+      table->tiles = before;
+      table->entries = V;
+      table->rows = rows;
+    }
+  }
+}
+
 // kSteps: steps of a wave whose tokens stay in registers, for kTiles tiles of
 // 16 tokens (128 registers in all).  kSteps * 8 lines cover H, or the tokens
 // are read again for each item.
@@ -345,38 +396,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, h = lane >> 4;
-  route_all(rt, p.logits, p.T, p.E, p.k, 16 * kTiles);
+  route_entries(rt, p.logits, p.T, p.E, p.k, 16 * kTiles);
   const int V = __builtin_amdgcn_readfirstlane(rt.entries);
-  if (blockIdx.x == 0) {
-    for (int u = tid; u < V; u += kThreads) p.table->expert[u] = rt.expert[u];
-    for (int u = tid; u <= V; u += kThreads) p.table->first[u] = rt.first[u];
-    for (int i = tid; i < rt.first[V]; i += kThreads) p.table->token[i] = rt.token[i];
-    if (wave == 0) {   // tiles before each entry
-      int before = 0;
-      for (int u0 = 0; u0 < V; u0 += 64) {
-        const int u = u0 + lane;
-        const int n = u < V ? (rt.first[u + 1] - rt.first[u] + 15) / 16 : 0;
-        int s = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int o = __shfl_up(s, d, 64);
-          if (lane >= d) s += o;
-        }
-        if (u < V) p.table->tile[u] = before + s - n;
-        before += __shfl(s, 63, 64);
-      }
-      if (lane == 0) {
-        p.table->tile[V] = before;
-        p.table->tiles = before;
-        p.table->entries = V;
-        p.table->rows = rt.first[V];
-      }
-    }
-  }
   const int fb = p.F / 16, items = V * fb;
   const int begin = (int)((int64_t)items * blockIdx.x / gridDim.x);
   const int end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
-  if (begin >= end) return;
+  if (begin >= end && blockIdx.x) return;
   const int lines = (p.H * eb + 127) / 128;
   const int per = (lines + kWaves - 1) / kWaves;   // a wave takes lines wave, wave + 8, ...
   const int64_t rows = 2 * (int64_t)p.F, row_bytes = (int64_t)p.H * eb;
@@ -391,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
     lq = rsrc(p.w1 + e * rows * row_bytes, rows * row_bytes);
     if constexpr (kMx) lsc = scale_rsrc(p.w1_s, e, p.E, rows, p.H);
   };
-  open(begin);
+  if (begin < end) open(begin);
   const int lr = lane >> 3, ch = (lane & 7);
   auto load = [&]() {
     const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kUpDepth) * kUpSlot;
@@ -439,8 +464,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   };
 
-#pragma unroll
+#pragma unroll 1
   for (int d = 0; d < kUpDepth; ++d) load();
+  // the stream runs; what only the items' ends need comes now
+  route_rows(rt, p.logits, p.E);
+  lds_barrier();
+  if (blockIdx.x == 0) write_table(rt, p.table);
   int entry = -1, used = 0;
   for (int item = begin; item < end; ++item) {
     const int u = item / fb, f0 = 16 * (item - u * fb);
@@ -517,15 +546,17 @@ constexpr int kDownSlot = 2 * 2048 + 256;          // two lines of 16 rows, thei
 constexpr int kXSlots = 3;
 
 // Units of work: (group of rows, entry, chunk of two lines, tile), the tile
-// innermost so that an entry's later tiles find the chunk in the cache.
-// Workgroup b of B takes [total b / B, total (b + 1) / B).
-__device__ __forceinline__ int64_t share(int64_t total, int64_t b, int64_t B) { return total * b / B; }
+// innermost so that an entry's later tiles find the chunk in the cache.  A
+// group has `each` units.  Where the work is cut over the card, workgroup b of
+// kCus takes the units [total b / kCus, total (b + 1) / kCus) of all groups'.
+__device__ __forceinline__ int64_t share(int64_t total, int32_t b) { return total * b / kCus; }
 
-// The workgroup whose share holds unit x (total > 0).
-__device__ __forceinline__ int64_t owner(int64_t total, int64_t x, int64_t B) {
-  int64_t b = x * B / total;
-  while (share(total, b + 1, B) <= x) ++b;
-  while (share(total, b, B) > x) --b;
+// The workgroup whose share holds unit g each + y (0 <= y < each, each > 0).
+__device__ __forceinline__ int32_t owner(int32_t groups, int64_t each, int32_t g, int64_t y) {
+  const int64_t total = groups * each, x = g * each + y;
+  int32_t b = (int32_t)((y ? kCus * (g + 1) - 1 : kCus * g) / groups);   // near it: g each / total = g / groups
+  while (share(total, b + 1) <= x) ++b;
+  while (share(total, b) > x) --b;
   return b;
 }
 
@@ -534,37 +565,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
   constexpr int kOps = kMx ? 6 : 5, eb = kMx ? 1 : 2, kK = kLineK<kMx>, kP = kXp<kMx>;
   constexpr int kXRow = 2 * kK * 2;                // bytes of a token row of a chunk
   __shared__ int32_t expert[kEntries], first[kEntries + 1], tile[kEntries + 1];
-  __shared__ uint8_t token[kMaxRows];
+  __shared__ __attribute__((aligned(4))) uint8_t token[kMaxRows];
   __shared__ __attribute__((aligned(16))) float sum[kWaves][kMaxTokens][16];
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kWaves][kDownDepth][kDownSlot];
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kXSlots][16 * kXRow];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, h = lane >> 4;
+  // the table up to the most entries and rows there can be: no load waits for
+  // another (what lies past the entries is not used)
+  const int pairs = p.T * p.k, most = (p.E < pairs ? p.E : pairs) + pairs / 16;
   const int V = __builtin_amdgcn_readfirstlane(p.table->entries);
   const int rows = __builtin_amdgcn_readfirstlane(p.table->rows);
   const int tiles = __builtin_amdgcn_readfirstlane(p.table->tiles);
-  for (int u = tid; u < V; u += kThreads) expert[u] = p.table->expert[u];
-  for (int u = tid; u <= V; u += kThreads) {
+  for (int u = tid; u <= most; u += kThreads) {
+    if (u < kEntries) expert[u] = p.table->expert[u];
     first[u] = p.table->first[u];
     tile[u] = p.table->tile[u];
   }
-  for (int i = tid; i < rows; i += kThreads) token[i] = p.table->token[i];
+  for (int i = 4 * tid; i < pairs; i += 4 * kThreads)
+    *reinterpret_cast<uint32_t*>(token + i) = *reinterpret_cast<const uint32_t*>(p.table->token + i);
   for (int i = lane; i < 16 * p.T; i += 64) (&sum[wave][0][0])[i] = 0.0f;
   __syncthreads();
-  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  const int32_t groups = (p.H + kGroupRows - 1) / kGroupRows;
   const int64_t row_bytes = (int64_t)p.F * eb;
   const int chunks = (int)((row_bytes + 255) / 256);
   const int64_t each = (int64_t)tiles * chunks;    // units of a group
   const int64_t total = groups * each;
-  const int64_t u0 = share(total, blockIdx.x, gridDim.x), u1 = share(total, blockIdx.x + 1, gridDim.x);
+  const int64_t u0 = p.part ? share(total, blockIdx.x) : blockIdx.x * each;
+  const int64_t u1 = p.part ? share(total, blockIdx.x + 1) : u0 + each;
 
   // a group's sums to their place: lane's 4 rows of 16 for each token
   auto put = [&](int64_t g) {
     const int64_t n0 = g * kGroupRows + 16 * wave;
     if (n0 < p.H) {
       float* part = nullptr;
-      if (p.part) part = p.part + (blockIdx.x - owner(total, g * each, gridDim.x)) * p.T * (int64_t)p.H;
+      if (p.part) part = p.part + ((int32_t)blockIdx.x - owner(groups, each, (int32_t)g, 0)) * p.T * (int64_t)p.H;
       for (int i = lane; i < 16 * p.T; i += 64) {
         const int t = i >> 4;
         const int64_t at = (int64_t)t * p.H + n0 + (i & 15);
@@ -581,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
   };
   if (u0 >= u1) {
     // (without pieces a workgroup owns its group even if no expert is active)
-    if (!p.part && blockIdx.x < groups) put(blockIdx.x);
+    if (!p.part) put(blockIdx.x);
     return;
   }
 
@@ -713,24 +749,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
 }
 
 // The pieces of a group in the workgroups' order, the residual, the rounding.
-__global__ void __launch_bounds__(256) k_tokens_join(TokensProblem p, int32_t line_bytes, int32_t blocks) {
-  const int64_t i = 2 * ((int64_t)blockIdx.x * 256 + threadIdx.x);   // two columns of a token
-  if (i >= (int64_t)p.T * p.H) return;
-  const int64_t n = i % p.H;
-  const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
-  const int64_t each = (int64_t)p.table->tiles * ((line_bytes + 255) / 256);
-  const int64_t total = groups * each;
+__global__ void __launch_bounds__(256) k_tokens_join(TokensProblem p, int32_t chunks) {
+  const int32_t i = 2 * (blockIdx.x * 256 + threadIdx.x);   // two columns of a token (T H < 2^30)
+  const int32_t all = p.T * p.H;
+  if (i >= all) return;
+  const int32_t groups = (p.H + kGroupRows - 1) / kGroupRows;
+  const int64_t each = (int64_t)p.table->tiles * chunks;
   float a = 0.0f, b = 0.0f;
   if (p.residual) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p.residual + i);
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
   }
-  if (total > 0) {
-    const int64_t g = n / kGroupRows;
-    const int64_t b0 = owner(total, g * each, blocks), b1 = owner(total, (g + 1) * each - 1, blocks);
-    for (int64_t s = 0; s <= b1 - b0; ++s) {
-      const float2 v = *reinterpret_cast<const float2*>(p.part + s * p.T * p.H + i);
+  if (each > 0) {
+    const int32_t g = i % p.H / kGroupRows;
+    const int32_t n = owner(groups, each, g, each - 1) - owner(groups, each, g, 0) + 1;
+#pragma unroll 4
+    for (int32_t s = 0; s < n; ++s) {
+      const float2 v = *reinterpret_cast<const float2*>(p.part + (int64_t)s * all + i);
       a += v.x;
       b += v.y;
     }
@@ -758,7 +794,7 @@ int launch_tokens(TokensProblem p, hipStream_t st) {
   const dim3 up((unsigned)(most < kCus ? most : kCus));
   // steps of 8 waves x 128 bytes; registers hold 8 (fp8) or 16 (bf16) of one tile
   constexpr int kLong = kMx ? 8 : 16;
-  if (p.T <= 16 || p.H > 4096) hipLaunchKernelGGL((k_tokens_up<kMx, kLong, 1>), up, dim3(kThreads), 0, st, p);
+  if (p.H > 4096) hipLaunchKernelGGL((k_tokens_up<kMx, kLong, 1>), up, dim3(kThreads), 0, st, p);
   else if (p.H > 2048) hipLaunchKernelGGL((k_tokens_up<kMx, kLong / 2, 2>), up, dim3(kThreads), 0, st, p);
   else hipLaunchKernelGGL((k_tokens_up<kMx, kLong / 4, 4>), up, dim3(kThreads), 0, st, p);
   const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
@@ -766,7 +802,7 @@ int launch_tokens(TokensProblem p, hipStream_t st) {
     hipLaunchKernelGGL(k_tokens_down<kMx>, dim3(kCus), dim3(kThreads), 0, st, p);
     const int64_t n = (int64_t)p.T * p.H / 2;
     hipLaunchKernelGGL(k_tokens_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p,
-                       (int32_t)(p.F * (kMx ? 1 : 2)), (int32_t)kCus);
+                       (int32_t)(((int64_t)p.F * (kMx ? 1 : 2) + 255) / 256));
   } else {
     p.part = nullptr;
     hipLaunchKernelGGL(k_tokens_down<kMx>, dim3((unsigned)groups), dim3(kThreads), 0, st, p);
