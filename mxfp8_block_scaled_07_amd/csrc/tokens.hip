@@ -124,55 +124,50 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// One wave chooses token t's experts: the k-th largest key is built bit by
-// bit from the top (the count of keys at or above a candidate is a ballot and
-// a popcount; the search ends when a count is exactly k), ties at it go to
-// the lowest ids.  Then the softmax statistics of the chosen.  kGroups: groups
-// of 64 experts, one key of each per lane.
+// One wave chooses a token's experts: the k-th largest key is built bit by bit
+// from the top (the count of keys at or above a candidate is a ballot and a
+// popcount; the search ends when a count is exactly k), ties at it go to the
+// lowest ids.  Then the softmax statistics of the chosen.  kGroups: groups of
+// 64 experts, one key of each per lane; key 0 where there is no expert (also
+// the key of one NaN, which is then never chosen).
 template <int kGroups>
-__device__ __forceinline__ void route_token(Routing& rt, const float* __restrict__ row, int t, int E, int k) {
+__device__ __forceinline__ void route_token(Routing& rt, const uint32_t (&key)[kGroups], int t, int k) {
   const int lane = threadIdx.x & 63;
-  uint32_t key[kGroups];
-  uint32_t valid = 0, chosen = 0;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = order_key(e < E ? row[e] : 0.0f);
-    valid |= (e < E ? 1u : 0u) << i;
-  }
   uint32_t thr = 0;
   bool exact = false;
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t cand = thr | (1u << bit);
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) n += __popcll(__ballot((valid >> i & 1u) && key[i] >= cand));
+    for (int i = 0; i < kGroups; ++i) n += (int)__popcll(__ballot(key[i] >= cand));
     if (n >= k) thr = cand;
     if (n == k) {
       exact = true;
       break;
     }
   }
+  uint32_t chosen = 0;
   int gt = 0;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const bool in = (valid >> i & 1u) && (exact ? key[i] >= thr : key[i] > thr);
-    if (in) chosen |= 1u << i;
-    gt += __popcll(__ballot(in));
+    const bool in = key[i] >= thr + (exact ? 0u : 1u) && thr + (exact ? 0u : 1u) != 0u;
+    chosen |= (in ? 1u : 0u) << i;
+    gt += (int)__popcll(__ballot(in));
   }
   int left = k - gt;   // keys equal to the threshold still to take, lowest ids first
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const unsigned long long b = __ballot((valid >> i & 1u) && key[i] == thr);
-    if ((b >> lane & 1u) && (int)__popcll(b & ((1ull << lane) - 1)) < left) chosen |= 1u << i;
-    left -= __popcll(b);
+    const unsigned long long b = __ballot(!exact & (key[i] == thr) & (key[i] != 0u));
+    const bool in = (b >> lane & 1u) && (int)__popcll(b & ((1ull << lane) - 1)) < left;
+    chosen |= (in ? 1u : 0u) << i;
+    left -= (int)__popcll(b);
   }
   float zm = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
     const float v = key_value(key[i]);
     if (v == -INFINITY) chosen &= ~(1u << i);   // masked: weight 0
-    if (chosen >> i & 1u) zm = fmaxf(zm, v);
+    zm = (chosen >> i & 1u) ? fmaxf(zm, v) : zm;
   }
   zm = wave_max_f(zm);
   float sum = 0.0f;
@@ -190,18 +185,36 @@ __device__ __forceinline__ void route_token(Routing& rt, const float* __restrict
   }
 }
 
+template <int kGroups>
+__device__ __forceinline__ void route_wave(Routing& rt, const float* __restrict__ logits, int T, int E, int k) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  uint32_t next[kGroups];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int e = lane + 64 * i;
+      next[i] = e < E ? __float_as_uint(logits[(int64_t)t * E + e]) : 0u;
+    }
+  };
+  if (wave < T) fetch(wave);
+  for (int t = wave; t < T; t += kWaves) {
+    uint32_t key[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) key[i] = lane + 64 * i < E ? order_key(__uint_as_float(next[i])) : 0u;
+    if (t + kWaves < T) fetch(t + kWaves);   // in flight while this token is routed
+    route_token<kGroups>(rt, key, t, k);
+  }
+}
+
 // The routing, by one workgroup: entries of at most `group` rows ...
 __device__ __forceinline__ void route_entries(Routing& rt, const float* __restrict__ logits, int T, int E, int k, int group) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   for (int e = tid; e < E; e += kThreads) rt.mask[e] = 0;
   __syncthreads();
-  for (int t = wave; t < T; t += kWaves) {
-    const float* row = logits + (int64_t)t * E;
-    if (E <= 64) route_token<1>(rt, row, t, E, k);
-    else if (E <= 256) route_token<4>(rt, row, t, E, k);
-    else route_token<kTokExperts / 64>(rt, row, t, E, k);
-  }
+  if (E > 256) route_wave<kTokExperts / 64>(rt, logits, T, E, k);
+  else if (E > 64) route_wave<4>(rt, logits, T, E, k);
+  else route_wave<1>(rt, logits, T, E, k);
   __syncthreads();
   if (wave == 0) {
     int V = 0, rows = 0;
@@ -288,6 +301,8 @@ __device__ __forceinline__ void dma4(const v4u& r, uint32_t lds, uint32_t voff, 
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
                : "m0", "memory");
 }
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(const lds_void*)p; }
 
@@ -397,44 +412,61 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, h = lane >> 4;
   route_entries(rt, p.logits, p.T, p.E, p.k, 16 * kTiles);
+  route_rows(rt, p.logits, p.E);
+  lds_barrier();
   const int V = __builtin_amdgcn_readfirstlane(rt.entries);
+  // the last workgroup writes the table; it has items too where every CU has
+  const int takers = gridDim.x == kCus ? kCus : gridDim.x - 1;
+  const bool scribe = blockIdx.x == gridDim.x - 1;
+  if (scribe && takers < (int)gridDim.x) {
+    write_table(rt, p.table);
+    return;
+  }
   const int fb = p.F / 16, items = V * fb;
-  const int begin = (int)((int64_t)items * blockIdx.x / gridDim.x);
-  const int end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
-  if (begin >= end && blockIdx.x) return;
+  const int begin = (int)((int64_t)items * blockIdx.x / takers);
+  const int end = (int)((int64_t)items * (blockIdx.x + 1) / takers);
+  if (begin >= end) {
+    if (scribe) write_table(rt, p.table);
+    return;
+  }
   const int lines = (p.H * eb + 127) / 128;
   const int per = (lines + kWaves - 1) / kWaves;   // a wave takes lines wave, wave + 8, ...
   const int64_t rows = 2 * (int64_t)p.F, row_bytes = (int64_t)p.H * eb;
 
-  // the loads' cursor
-  int li = begin, ls = 0, lf = 0, seq = 0;
+  // the loads' cursor; a lane's offsets are the same for every item and line
+  int li = begin, ls = 0, seq = 0;
+  uint32_t lrow = 0, lrow_s = 0;   // the item's first row, in weight and scale bytes
   v4u lq, lsc;
   auto open = [&](int item) {
     const int u = item / fb;
     const int64_t e = __builtin_amdgcn_readfirstlane(rt.expert[u]);
-    lf = 16 * (item - u * fb);
+    const int f = 16 * (item - u * fb);
+    lrow = (uint32_t)f * (uint32_t)row_bytes;
+    lrow_s = 4u * (uint32_t)f;
     lq = rsrc(p.w1 + e * rows * row_bytes, rows * row_bytes);
     if constexpr (kMx) lsc = scale_rsrc(p.w1_s, e, p.E, rows, p.H);
   };
-  if (begin < end) open(begin);
-  const int lr = lane >> 3, ch = (lane & 7);
+  open(begin);
+  const uint32_t half = (uint32_t)p.F * (uint32_t)row_bytes, panel = 4u * (uint32_t)p.E * (uint32_t)rows;
+  uint32_t lane_off[2];
+  int32_t lane_c[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = 8 * q + (lane >> 3);
+    lane_c[q] = 16 * ((lane & 7) ^ chunk_swizzle(row));
+    lane_off[q] = (uint32_t)row * (uint32_t)row_bytes + (uint32_t)lane_c[q];
+  }
+  const uint32_t lane_s = lane < 32 ? 4u * (uint32_t)((lane >> 4) * p.F + r) : kOob;
   auto load = [&]() {
     const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kUpDepth) * kUpSlot;
     const int line = wave + kWaves * ls;
     const bool in = li < end && line < lines;
-    const uint32_t soff = in ? 128u * (uint32_t)line : 0u;
+    const uint32_t soff = in ? 128u * (uint32_t)line + lrow : 0u;
+    const int32_t left = in ? (int32_t)(row_bytes - 128 * (int64_t)line) : 0;   // bytes of the row from here on
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = 8 * (q & 1) + lr;
-      const int c = 16 * (ch ^ chunk_swizzle(row));
-      const bool ok = in & ((int64_t)soff + c < row_bytes);
-      const uint32_t off = (uint32_t)((q >> 1) * p.F + lf + row) * (uint32_t)row_bytes + (uint32_t)c;
-      dma16_nt(lq, dst + 1024u * q, ok ? off : kOob, soff);
-    }
-    if constexpr (kMx) {
-      const uint32_t off = 4u * (uint32_t)((lane >> 4) * p.F + lf + r);
-      dma4(lsc, dst + 4096u, (in && lane < 32) ? off : kOob, in ? (uint32_t)line * (uint32_t)(4 * p.E * rows) : 0u);
-    }
+    for (int q = 0; q < 4; ++q)
+      dma16_nt(lq, dst + 1024u * q, lane_c[q & 1] < left ? lane_off[q & 1] : kOob, soff + (in ? (q >> 1) * half : 0u));
+    if constexpr (kMx) dma4(lsc, dst + 4096u, in ? lane_s : kOob, in ? (uint32_t)line * panel + lrow_s : 0u);
     ++seq;
     if (++ls == per) {
       ls = 0;
@@ -460,17 +492,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
           x[t][s][j] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)off + 16 * j, 0, 0));
       }
     }
-    // waited for here, once: a wait at each use would also drain the stream
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   };
 
+  int entry = begin / fb, used = 0;
+  tokens(__builtin_amdgcn_readfirstlane(rt.first[entry]), __builtin_amdgcn_readfirstlane(rt.first[entry + 1]), 0);
 #pragma unroll 1
   for (int d = 0; d < kUpDepth; ++d) load();
-  // the stream runs; what only the items' ends need comes now
-  route_rows(rt, p.logits, p.E);
-  lds_barrier();
-  if (blockIdx.x == 0) write_table(rt, p.table);
-  int entry = -1, used = 0;
+  if (scribe) write_table(rt, p.table);
+  // the tokens are waited for here, ahead of the stream (by itself the compiler
+  // would wait at each use, and for the stream's loads too)
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(kOps * kUpDepth));
   for (int item = begin; item < end; ++item) {
     const int u = item / fb, f0 = 16 * (item - u * fb);
     const int lo = __builtin_amdgcn_readfirstlane(rt.first[u]), hi = __builtin_amdgcn_readfirstlane(rt.first[u + 1]);
@@ -478,8 +509,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) g[t] = up[t] = v4f{0.f, 0.f, 0.f, 0.f};
     for (int s0 = 0; s0 < per; s0 += kSteps) {
-      if (u != entry || per > kSteps) tokens(lo, hi, s0);
-      entry = u;
+      if (u != entry || (per > kSteps && (s0 || item > begin))) {
+        tokens(lo, hi, s0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        entry = u;
+      }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         if (s0 + s < per) {
@@ -655,52 +689,73 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
   };
 
   Unit ld = at(u0), cur = ld;
-  int64_t issued = u0;
+  const int count = (int)(u1 - u0);
+  int issued = 0;
   const v4u ar = rsrc(p.a, (int64_t)rows * p.F * 2);
-  const int lr = lane >> 3, ch = lane & 7;
-  auto load = [&]() {
-    const bool on = issued < u1;
-    const int seq = (int)(issued - u0);
-    const int64_t e = __builtin_amdgcn_readfirstlane(expert[ld.u]);
-    const int64_t n0 = ld.g * kGroupRows + 16 * wave;
-    const bool in = on && n0 < p.H;
-    const v4u wq = rsrc(p.w2 + e * p.H * row_bytes, p.H * row_bytes);
-    const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kDownDepth) * kDownSlot;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = 8 * (q & 1) + lr;
-      const int c = 16 * (ch ^ chunk_swizzle(row));
-      const int64_t k = 256 * (int64_t)ld.c + 128 * (q >> 1) + c;
-      const bool ok = in & (k < row_bytes);
-      const uint32_t off = (uint32_t)(n0 + row) * (uint32_t)row_bytes + (uint32_t)k;
-      dma16_nt(wq, dst + 1024u * q, ok ? off : kOob, 0);
+  v4u wq, sr;
+  uint32_t n_off = 0, n_off_s = 0;   // the wave's first row, in weight and scale bytes
+  bool rows_in = false;
+  int lo = 0, hi = 0, open_u = -1;
+  int64_t open_g = -1;
+  auto open = [&]() {
+    if (ld.u != open_u) {
+      const int64_t e = __builtin_amdgcn_readfirstlane(expert[ld.u]);
+      lo = __builtin_amdgcn_readfirstlane(first[ld.u]);
+      hi = __builtin_amdgcn_readfirstlane(first[ld.u + 1]);
+      wq = rsrc(p.w2 + e * p.H * row_bytes, p.H * row_bytes);
+      if constexpr (kMx) sr = scale_rsrc(p.w2_s, e, p.E, p.H, p.F);
+      open_u = ld.u;
     }
+    if (ld.g != open_g) {
+      const int64_t n0 = ld.g * kGroupRows + 16 * wave;
+      rows_in = n0 < p.H;
+      n_off = rows_in ? (uint32_t)n0 * (uint32_t)row_bytes : 0u;
+      n_off_s = rows_in ? 4u * (uint32_t)n0 : 0u;
+      open_g = ld.g;
+    }
+  };
+  uint32_t lane_off[2];
+  int32_t lane_c[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = 8 * q + (lane >> 3);
+    lane_c[q] = 16 * ((lane & 7) ^ chunk_swizzle(row));
+    lane_off[q] = (uint32_t)row * (uint32_t)row_bytes + (uint32_t)lane_c[q];
+  }
+  const uint32_t panel = 4u * (uint32_t)p.E * (uint32_t)p.H;
+  const uint32_t lane_s = (uint32_t)((lane >> 4) & 1) * panel + 4u * (uint32_t)r;
+  constexpr int kChunks = kXRow / 16;              // 16-byte chunks of a token row
+  const int xl = 2 * wave + lane / kChunks;        // the lane's token row of a tile, its chunk
+  const int xc = 8 * ((lane % kChunks) ^ (xl & 15));
+  auto load = [&]() {
+    const bool on = issued < count;
+    const bool in = on && rows_in;
+    const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(issued % kDownDepth) * kDownSlot;
+    const int32_t left = in ? (int32_t)(row_bytes - 256 * (int64_t)ld.c) : 0;   // bytes of the rows from here on
+    const uint32_t soff = uniform(in ? n_off + 256u * (uint32_t)ld.c : 0u);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)   // (a second line past the rows' end has no lane in range)
+      dma16_nt(wq, dst + 1024u * q, lane_c[q & 1] + 128 * (q >> 1) < left ? lane_off[q & 1] + 128u * (q >> 1) : kOob, soff);
     if constexpr (kMx) {   // lanes 0..15: the first line's scale dwords, 16..31 the second's
-      const v4u sr = scale_rsrc(p.w2_s, e, p.E, p.H, p.F);
-      const int64_t panel = 2 * (int64_t)ld.c + (lane >> 4);
-      const bool ok = in & (lane < 32) & (128 * panel < p.F);
-      const uint32_t off = (uint32_t)(panel * 4 * p.E * p.H) + 4u * (uint32_t)(n0 + r);
-      dma4(sr, dst + 4096u, ok ? off : kOob, 0);
+      const bool ok = lane < 32 && 128 * ((lane >> 4) & 1) < left;
+      dma4(sr, dst + 4096u, ok ? lane_s : kOob, uniform(in ? 2u * (uint32_t)ld.c * panel + n_off_s : 0u));
     }
     // this wave's two token rows of the chunk
-    const uint32_t xd = lds_addr(xs[0]) + (uint32_t)(seq % kXSlots) * (16 * kXRow) + (uint32_t)wave * (2 * kXRow);
-    constexpr int kChunks = kXRow / 16;            // 16-byte chunks of a token row
+    const uint32_t xd = lds_addr(xs[0]) + (uint32_t)(issued % kXSlots) * (16 * kXRow) + (uint32_t)wave * (2 * kXRow);
     if (lane < 2 * kChunks) {
-      const int rl = 2 * wave + lane / kChunks;
-      const int c = (lane % kChunks) ^ (rl & 15);
-      const int row = __builtin_amdgcn_readfirstlane(first[ld.u]) + 16 * ld.t + rl;
-      const int k = ld.c * 2 * kK + 8 * c;
-      const bool ok = on & (row < __builtin_amdgcn_readfirstlane(first[ld.u + 1])) & (k < p.F);
-      dma16(ar, xd, ok ? 2u * ((uint32_t)row * (uint32_t)p.F + (uint32_t)k) : kOob, 0);
+      const int row = lo + 16 * ld.t + xl, k = ld.c * 2 * kK + xc;
+      dma16(ar, xd, on && row < hi && k < p.F ? 2u * ((uint32_t)row * (uint32_t)p.F + (uint32_t)k) : kOob, 0);
     }
-    ++issued;
-    if (issued < u1) next(ld);
+    if (++issued < count) {
+      next(ld);
+      open();
+    }
   };
 
+  open();
 #pragma unroll
   for (int d = 0; d < kDownDepth; ++d) load();
-  for (int64_t x = u0; x < u1; ++x) {
-    const int seq = (int)(x - u0);
+  for (int seq = 0; seq < count; ++seq) {
     // this unit's loads are done, the next one's may be in flight; after the
     // barrier every wave's token rows are there, and every wave has read the
     // token slot that the loads below overwrite (two units ago)
@@ -742,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_down(TokensProblem p) {
     }
     const int64_t g = cur.g;
     next(cur);
-    if (cur.g != g || x + 1 == u1) put(g);
+    if (cur.g != g || seq + 1 == count) put(g);
   }
   // loads past the last unit may still be writing LDS
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
@@ -779,19 +834,20 @@ __global__ void __launch_bounds__(256) k_tokens_join(TokensProblem p, int32_t ch
 constexpr int64_t kPartCols = 128 * 3 * (int64_t)kCus;
 
 // Whether the groups' work is cut over the card: not where they fill it, nor
-// where there is less than two units for every CU.
+// where a group has at most six units (a unit takes its workgroup 0.8 us, the
+// join and the reading of more pieces 5 us).
 bool cut(const TokensProblem& p, bool mxw) {
   const int64_t groups = (p.H + kGroupRows - 1) / kGroupRows;
   const int64_t pairs = (int64_t)p.T * p.k;
-  const int64_t units = (p.E < pairs ? p.E : pairs) * (((int64_t)p.F * (mxw ? 1 : 2) + 255) / 256) * groups;
-  return groups < kCus && units > 2 * kCus;
+  const int64_t units = (p.E < pairs ? p.E : pairs) * (((int64_t)p.F * (mxw ? 1 : 2) + 255) / 256);
+  return groups < kCus && units > 6;
 }
 
 template <bool kMx>
 int launch_tokens(TokensProblem p, hipStream_t st) {
   const int64_t pairs = (int64_t)p.T * p.k;
   const int64_t most = ((p.E < pairs ? p.E : pairs) + pairs / 16) * (p.F / 16);
-  const dim3 up((unsigned)(most < kCus ? most : kCus));
+  const dim3 up((unsigned)(most + 1 < kCus ? most + 1 : kCus));   // items at most, and the table's writer
   // steps of 8 waves x 128 bytes; registers hold 8 (fp8) or 16 (bf16) of one tile
   constexpr int kLong = kMx ? 8 : 16;
   if (p.H > 4096) hipLaunchKernelGGL((k_tokens_up<kMx, kLong, 1>), up, dim3(kThreads), 0, st, p);
