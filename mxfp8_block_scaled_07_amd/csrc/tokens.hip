@@ -582,12 +582,18 @@ constexpr int kXSlots = 3;
 // Units of work: (group of rows, entry, chunk of two lines, tile), the tile
 // innermost so that an entry's later tiles find the chunk in the cache.  A
 // group has `each` units.  Where the work is cut over the card, workgroup b of
-// kCus takes the units [total b / kCus, total (b + 1) / kCus) of all groups'.
-__device__ __forceinline__ int64_t share(int64_t total, int32_t b) { return total * b / kCus; }
+// kCus takes the units [total b / kCus, total (b + 1) / kCus) of all groups',
+// or unit b where there are fewer units: the shares of a group's workgroups
+// follow each other and none of them is empty.
+__device__ __forceinline__ int64_t share(int64_t total, int32_t b) {
+  if (total < kCus) return b < total ? b : total;
+  return total * b / kCus;
+}
 
 // The workgroup whose share holds unit g each + y (0 <= y < each, each > 0).
 __device__ __forceinline__ int32_t owner(int32_t groups, int64_t each, int32_t g, int64_t y) {
   const int64_t total = groups * each, x = g * each + y;
+  if (total < kCus) return (int32_t)x;
   int32_t b = (int32_t)((y ? kCus * (g + 1) - 1 : kCus * g) / groups);   // near it: g each / total = g / groups
   while (share(total, b + 1) <= x) ++b;
   while (share(total, b) > x) --b;
