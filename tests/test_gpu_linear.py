@@ -50,7 +50,8 @@ class Case:
         M, N, K = self.M, self.N, self.K
         wsb = mxa.mx_bf16_linear_workspace_size(M, N, K)
         if not hasattr(self, "ws"):
-            self.ws = torch.full((wsb + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+            # all ones: NaN wherever the product would use what it has not written
+            self.ws = torch.full((wsb + 64,), 0xFF, dtype=torch.uint8, device=DEV)
             self.out = padded((M, N), torch.float32 if self.f32 else torch.bfloat16)
             self.z = padded((M, N), torch.bfloat16) if self.keep_z else None
         mxa.mx_bf16_linear(self.d["x"], self.d["w"], self.d["bias"], self.d["res"], M, N, K, ol.ACTS.index(self.act),
@@ -61,7 +62,7 @@ class Case:
         M, N, K, act = self.M, self.N, self.K, ol.ACTS.index(self.act)
         wsb = mxa.mx_bf16_linear_bwd_workspace_size(M, N, K, act)
         if not hasattr(self, "bws"):
-            self.bws = torch.full((wsb + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+            self.bws = torch.full((wsb + 64,), 0xFF, dtype=torch.uint8, device=DEV)
             self.dx, self.dw = padded((M, K), torch.bfloat16), padded((N, K), torch.bfloat16)
             self.db = torch.full((N + 1,), 77.0, device=DEV)
         mxa.mx_bf16_linear_bwd(self.d["dout"], F32 if self.f32 else BF, self.d["zin"] if act else None, self.d["x"],
@@ -71,7 +72,7 @@ class Case:
     def check_fwd(self):
         wsb = self.fwd()
         torch.cuda.synchronize()
-        assert (self.out[self.M] == 77).all() and (self.ws[wsb:] == 0xA5).all()
+        assert (self.out[self.M] == 77).all() and (self.ws[wsb:] == 0xFF).all()
         y, yb, z, zb = ol.forward(val(self.x), val(self.w), self.bias, None if self.res is None else val(self.res),
                                   self.act, self.f32)
         within(host(self.out[:self.M]), y, yb, "out")
@@ -83,7 +84,7 @@ class Case:
         wsb = self.bwd()
         torch.cuda.synchronize()
         assert (self.dx[self.M] == 77).all() and (self.dw[self.N] == 77).all() and self.db[self.N] == 77
-        assert (self.bws[wsb:] == 0xA5).all()
+        assert (self.bws[wsb:] == 0xFF).all()
         want = ol.backward(val(self.dout), val(self.zin), val(self.x), val(self.w),
                            None if self.add is None else val(self.add), self.act)
         within(host(self.dx[:self.M]), *want["dx"], "dx")
