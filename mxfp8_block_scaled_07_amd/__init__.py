@@ -393,6 +393,127 @@ def router_bwd(dout, y, dst_row, expert_ids, weights, num_experts, stream=None):
     return dw, dl
 
 
+# --- the layer for a few tokens, the dense product, AdamW ---------------------
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _tensor(name, t, shape, dtype, device=None):
+    """t is a contiguous tensor of this shape and type (bf16 may come as its int16 bits) on the device."""
+    import torch
+    kinds = (torch.bfloat16, torch.int16) if dtype == torch.bfloat16 else (dtype,)
+    _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    _need(t.dtype in kinds, f"{name} is {t.dtype}, not {dtype}")
+    _need(t.is_contiguous(), f"{name} is not contiguous")
+    _need(device is None or t.device == device, f"{name} is on {t.device}, not {device}")
+
+
+def _on(device):
+    """The tensors' device as the current one, whose current stream a call without a stream uses."""
+    import contextlib
+
+    import torch
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+
+
+def moe_tokens(x, logits, topk, w1, w2, residual=None, stream=None):
+    """The whole MoE layer for at most 64 tokens: x bf16 [T, H], logits fp32 [T, E]; w1, w2 bf16 [E, 2F, H] and
+    [E, H, F], or MX rowwise (codes, scales) pairs of them.  Returns bf16 [T, H]."""
+    import torch
+    T, H = x.shape
+    mxw = isinstance(w1, (tuple, list))
+    _need(mxw == isinstance(w2, (tuple, list)), "moe_tokens: w1 and w2 are both bf16 or both (codes, scales)")
+    E, F = logits.shape[1], (w2[0] if mxw else w2).shape[2]
+    dev, bf = x.device, torch.bfloat16
+    _tensor("x", x, (T, H), bf)
+    _tensor("logits", logits, (T, E), torch.float32, dev)
+    if mxw:
+        _tensor("w1 codes", w1[0], (E, 2 * F, H), torch.uint8, dev)
+        _tensor("w1 scales", w1[1], scale_shape(E * 2 * F, H), torch.uint8, dev)
+        _tensor("w2 codes", w2[0], (E, H, F), torch.uint8, dev)
+        _tensor("w2 scales", w2[1], scale_shape(E * H, F), torch.uint8, dev)
+    else:
+        _tensor("w1", w1, (E, 2 * F, H), bf, dev)
+        _tensor("w2", w2, (E, H, F), bf, dev)
+    if residual is not None:
+        _tensor("residual", residual, (T, H), bf, dev)
+    out = torch.empty((T, H), dtype=bf, device=dev)
+    if T:
+        wsb = mx_moe_tokens_workspace_size(T, topk, E, F)
+        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+        with _on(dev):
+            if mxw:
+                mx_moe_tokens(x, logits, T, topk, E, H, F, w1[0], w1[1], w2[0], w2[1], residual, out, ws, wsb, stream)
+            else:
+                mx_bf16_moe_tokens(x, logits, T, topk, E, H, F, w1, w2, residual, out, ws, wsb, stream)
+    return out
+
+
+def bf16_linear(x, w, bias=None, residual=None, act=MX_ACT_NONE, out_dtype=MX_OUT_BF16, want_z=False, stream=None):
+    """act(x w^T + bias) + residual: x bf16 [M, K], w bf16 [N, K], bias fp32 [N], residual bf16 [M, N].
+    Returns (out, z), z the bf16 pre-activation for the backward or None."""
+    import torch
+    M, K = x.shape
+    N, dev, bf = w.shape[0], x.device, torch.bfloat16
+    _tensor("x", x, (M, K), bf)
+    _tensor("w", w, (N, K), bf, dev)
+    if bias is not None:
+        _tensor("bias", bias, (N,), torch.float32, dev)
+    if residual is not None:
+        _tensor("residual", residual, (M, N), bf, dev)
+    out = torch.empty((M, N), dtype=bf if out_dtype == MX_OUT_BF16 else torch.float32, device=dev)
+    z = torch.empty((M, N), dtype=bf, device=dev) if want_z else None
+    if M:
+        wsb = mx_bf16_linear_workspace_size(M, N, K)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        with _on(dev):
+            mx_bf16_linear(x, w, bias, residual, M, N, K, act, z, out, out_dtype, ws, wsb, stream)
+    return out, z
+
+
+def bf16_linear_bwd(dout, x, w, z=None, act=MX_ACT_NONE, dx_add=None, want_dbias=True, stream=None):
+    """Backward of bf16_linear: dout bf16 or fp32 [M, N], z as kept by the forward (needed with an activation).
+    Returns (dx bf16 [M, K], dw bf16 [N, K], dbias fp32 [N] or None)."""
+    import torch
+    M, K = x.shape
+    N, dev, bf = w.shape[0], x.device, torch.bfloat16
+    f32 = dout.dtype == torch.float32
+    _tensor("dout", dout, (M, N), torch.float32 if f32 else bf, dev)
+    _tensor("x", x, (M, K), bf)
+    _tensor("w", w, (N, K), bf, dev)
+    _need(act == MX_ACT_NONE or z is not None, "bf16_linear_bwd: the activation's backward needs z")
+    if z is not None:
+        _tensor("z", z, (M, N), bf, dev)
+    if dx_add is not None:
+        _tensor("dx_add", dx_add, (M, K), bf, dev)
+    dx = torch.empty((M, K), dtype=bf, device=dev)
+    dw = torch.empty((N, K), dtype=bf, device=dev)
+    db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+    if not M:   # empty tensors have no storage to pass
+        dw.zero_()
+        if db is not None:
+            db.zero_()
+        return dx, dw, db
+    wsb = mx_bf16_linear_bwd_workspace_size(M, N, K, act)
+    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        mx_bf16_linear_bwd(dout, MX_OUT_F32 if f32 else MX_OUT_BF16, z, x, w, dx_add, M, N, K, act, dx, dw, db, ws,
+                           wsb, stream)
+    return dx, dw, db
+
+
+def adamw_state(param, state_bits=32):
+    """(m, v, m_scale, v_scale) of a new AdamW state for a parameter: fp32 zeros, or MX codes and scales of zeros."""
+    import torch
+    _need(state_bits in (8, 32), "adamw_state: state_bits is 8 or 32")
+    n, dev = param.numel(), param.device
+    if state_bits == 32:
+        return torch.zeros(n, device=dev), torch.zeros(n, device=dev), None, None
+    z = lambda k: torch.zeros(k, dtype=torch.uint8, device=dev)  # noqa: E731
+    return z(n), z(n), z(-(-n // 32)), z(-(-n // 32))
+
+
 def adamw_table(rows):
     """The host table mx_adamw takes, from (param, grad, m, v, m_scale, v_scale, copy) per tensor (contiguous device
     tensors; None for what is not there).  It keeps its tensors alive and can be used for every step."""

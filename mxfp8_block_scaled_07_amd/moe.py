@@ -21,10 +21,13 @@ combine backward writes); ``zero_pad_rows`` prepares such a tensor.
 
 import torch
 
-from . import (MX_OUT_BF16, MX_OUT_F32, mx_bf16_gather, mx_bf16_grouped_gemm_dgrad, mx_bf16_grouped_gemm_fwd,
-               mx_bf16_grouped_gemm_wgrad, mx_combine, mx_combine_bwd_quantize, mx_grouped_gemm_dgrad,
-               mx_grouped_gemm_fwd, mx_grouped_gemm_wgrad, mx_permute, mx_permute_workspace_size, mx_quantize,
-               mx_route_topk, mx_router_bwd, mx_swiglu_bwd_quantize, mx_swiglu_quantize, scale_shape)
+from . import (MX_ACT_NONE, MX_OUT_BF16, MX_OUT_F32, adamw_state, adamw_table, mx_adamw, mx_bf16_gather,
+               mx_bf16_grouped_gemm_dgrad, mx_bf16_grouped_gemm_fwd, mx_bf16_grouped_gemm_wgrad, mx_bf16_linear,
+               mx_bf16_linear_bwd, mx_bf16_linear_bwd_workspace_size, mx_bf16_linear_workspace_size,
+               mx_bf16_moe_tokens, mx_combine, mx_combine_bwd_quantize, mx_grouped_gemm_dgrad, mx_grouped_gemm_fwd,
+               mx_grouped_gemm_wgrad, mx_moe_tokens, mx_moe_tokens_workspace_size, mx_permute,
+               mx_permute_workspace_size, mx_quantize, mx_route_topk, mx_router_bwd, mx_swiglu_bwd_quantize,
+               mx_swiglu_quantize, scale_shape)
 
 STAGES = ("quant_x", "permute", "quant_w", "gemm_fwd", "quant_dy", "gemm_dgrad", "quant_xt", "gemm_wgrad")
 
@@ -393,3 +396,101 @@ def layer_work(T, H, F, E, topk):
             "unpermute_dx": T * H * (2 * topk + 2) + M * 4,
         },
     }
+
+
+# ---------------------------------------------------------------------------
+# The layer with its gate product (router logits = x Wg^T + bg, Wg [E, H] in
+# bf16, bg [E] and the logits in fp32), forward and backward; AdamW on its
+# weights; and the same layer for a few tokens.
+# ---------------------------------------------------------------------------
+GATED_STAGES = ("gate",) + LAYER_STAGES + ("gate_bwd",)
+
+
+class GatedLayerBuffers(LayerBuffers):
+    """LayerBuffers with the gate's logits and gradients.  b.dx holds the whole
+    gradient of x after a step, b.dwg and b.dbg the gate's."""
+
+    def __init__(self, T, H, F, E, topk, device="cuda:0"):
+        super().__init__(T, H, F, E, topk, device)
+        e = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        self.logits = e(T, E, dt=torch.float32)
+        self.dwg, self.dbg = e(E, H, dt=torch.bfloat16), e(E, dt=torch.float32)
+        self.gate_wsb = max(mx_bf16_linear_workspace_size(T, E, H),
+                            mx_bf16_linear_bwd_workspace_size(T, E, H, MX_ACT_NONE))
+        self.gate_ws = e(max(self.gate_wsb, 16))
+
+
+def run_gated_stage(name, b, x, wg, bg, w1, w2, dout, stream=None):
+    """Launch one named stage of the gated layer on ``stream``."""
+    T, H, E = b.T, b.H, b.E
+    if name == "gate":
+        mx_bf16_linear(x, wg, bg, None, T, E, H, MX_ACT_NONE, None, b.logits, MX_OUT_F32, b.gate_ws, b.gate_wsb, stream)
+    elif name == "gate_bwd":
+        mx_bf16_linear_bwd(b.dlogits, MX_OUT_F32, None, x, wg, b.dx, T, E, H, MX_ACT_NONE, b.dx, b.dwg, b.dbg,
+                           b.gate_ws, b.gate_wsb, stream)
+    else:
+        run_layer_stage(name, b, x, w1, w2, b.logits, dout, stream)
+
+
+def gated_layer_step(b, x, wg, bg, w1, w2, dout, stream=None):
+    """One forward + backward pass of the layer from x through its gate."""
+    for name in GATED_STAGES:
+        run_gated_stage(name, b, x, wg, bg, w1, w2, dout, stream)
+
+
+class Adamw:
+    """AdamW on a list of (param, grad, copy): fp32 or bf16 parameters of one
+    type, gradients of one type, copy the bf16 weights the kernels read (or
+    None).  ``lr``, ``step`` and ``grad_scale`` are device scalars (the first
+    two of this object): a captured step() follows what they hold."""
+
+    def __init__(self, tensors, state_bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 grad_scale=None, seed=0):
+        kinds = {torch.float32: MX_OUT_F32, torch.bfloat16: MX_OUT_BF16}
+        types = {(p.dtype, g.dtype) for p, g, _ in tensors}
+        if len(types) != 1 or not all(t in kinds for t in next(iter(types))):
+            raise ValueError("Adamw: parameters are all fp32 or all bf16, and so are gradients")
+        if any(c is not None and c.dtype != torch.bfloat16 for _, _, c in tensors):
+            raise ValueError("Adamw: copies are bf16")
+        self.device = tensors[0][0].device
+        if any(t is not None and t.device != self.device for row in tensors for t in row):
+            raise ValueError("Adamw: the tensors are on one device")
+        self.param_dtype, self.grad_dtype = (kinds[t] for t in next(iter(types)))
+        self.state_bits, self.betas, self.eps, self.weight_decay, self.seed = state_bits, betas, eps, weight_decay, seed
+        self.lr = torch.full((1,), float(lr), device=self.device)
+        self.count = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.grad_scale = grad_scale
+        self.states = [adamw_state(p, state_bits) for p, _, _ in tensors]
+        self.table = adamw_table([(p, g, *s, c) for (p, g, c), s in zip(tensors, self.states)])
+
+    def step(self, stream=None):
+        """Count the step on torch's current stream, then update every tensor
+        on ``stream`` (by default the same one)."""
+        self.count.add_(1)
+        mx_adamw(self.table, len(self.table), self.param_dtype, self.grad_dtype, self.state_bits, self.lr, self.count,
+                 self.grad_scale, *self.betas, self.eps, self.weight_decay, self.seed, stream)
+
+
+class TokenBuffers:
+    """Device buffers of the layer for T <= 64 tokens, allocated once."""
+
+    def __init__(self, T, H, F, E, topk, device="cuda:0"):
+        self.T, self.H, self.F, self.E, self.topk = T, H, F, E, topk
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
+        self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+        self.gate_wsb = mx_bf16_linear_workspace_size(T, E, H)
+        self.wsb = mx_moe_tokens_workspace_size(T, topk, E, F)
+        self.gate_ws = torch.empty(max(self.gate_wsb, 16), dtype=torch.uint8, device=device)
+        self.ws = torch.empty(max(self.wsb, 16), dtype=torch.uint8, device=device)
+
+
+def token_step(b, x, wg, bg, w1, w2, residual=None, stream=None):
+    """The gate and the whole layer for a few tokens: w1, w2 bf16, or (codes,
+    scales) as a training step leaves them in (b.w1q, b.w1s), (b.w2q, b.w2s).
+    The result is in b.out."""
+    T, H, F, E, k = b.T, b.H, b.F, b.E, b.topk
+    mx_bf16_linear(x, wg, bg, None, T, E, H, MX_ACT_NONE, None, b.logits, MX_OUT_F32, b.gate_ws, b.gate_wsb, stream)
+    if isinstance(w1, tuple):
+        mx_moe_tokens(x, b.logits, T, k, E, H, F, *w1, *w2, residual, b.out, b.ws, b.wsb, stream)
+    else:
+        mx_bf16_moe_tokens(x, b.logits, T, k, E, H, F, w1, w2, residual, b.out, b.ws, b.wsb, stream)

@@ -1,0 +1,55 @@
+"""The allocating helpers of the few-token layer, the dense product and AdamW refuse arguments that do not fit, before
+any call (on the CPU)."""
+
+import pytest
+import torch
+
+import mxfp8_block_scaled_07_amd as mxa
+from mxfp8_block_scaled_07_amd import moe
+
+bf, u8 = torch.bfloat16, torch.uint8
+
+
+def tokens(x=None, logits=None, w1=None, w2=None, res=None):
+    z = lambda *s, dt=bf: torch.zeros(s, dtype=dt)  # noqa: E731
+    return mxa.moe_tokens(z(3, 64) if x is None else x, z(3, 4, dt=torch.float32) if logits is None else logits, 2,
+                          z(4, 64, 64) if w1 is None else w1, z(4, 64, 32) if w2 is None else w2, res)
+
+
+def test_moe_tokens():
+    z = lambda *s, dt=bf: torch.zeros(s, dtype=dt)  # noqa: E731
+    for bad in (dict(x=z(3, 64, dt=torch.float32)), dict(x=z(64, 3).t()), dict(logits=z(3, 4)), dict(logits=z(2, 4, dt=torch.float32)),
+                dict(w1=z(4, 32, 64)), dict(w2=z(4, 32, 64)), dict(res=z(3, 32)), dict(w1=(z(4, 64, 64, dt=u8), z(1, 256, 4, dt=u8))),
+                dict(w1=(z(4, 64, 64, dt=u8), z(1, 255, 4, dt=u8)), w2=(z(4, 64, 32, dt=u8), z(1, 256, 4, dt=u8)))):
+        with pytest.raises(ValueError):
+            tokens(**bad)
+
+
+def test_bf16_linear():
+    x, w = torch.zeros(5, 64, dtype=bf), torch.zeros(8, 64, dtype=bf)
+    for bad in (dict(bias=torch.zeros(8, dtype=bf)), dict(bias=torch.zeros(7)), dict(residual=torch.zeros(5, 7, dtype=bf))):
+        with pytest.raises(ValueError):
+            mxa.bf16_linear(x, w, **bad)
+    with pytest.raises(ValueError):
+        mxa.bf16_linear(x, torch.zeros(8, 32, dtype=bf))
+    d = torch.zeros(5, 8)
+    with pytest.raises(ValueError):
+        mxa.bf16_linear_bwd(d, x, w, act=mxa.MX_ACT_SILU)
+    with pytest.raises(ValueError):
+        mxa.bf16_linear_bwd(torch.zeros(5, 7), x, w)
+    with pytest.raises(ValueError):
+        mxa.bf16_linear_bwd(d, x, w, dx_add=torch.zeros(5, 64))
+
+
+def test_adamw():
+    p, g = torch.zeros(40), torch.zeros(40, dtype=bf)
+    with pytest.raises(ValueError):
+        mxa.adamw_state(p, 16)
+    m, v, ms, vs = mxa.adamw_state(p, 8)
+    assert m.dtype == u8 and m.numel() == 40 and ms.numel() == 2 and not vs.any()
+    with pytest.raises(ValueError):
+        moe.Adamw([(p, g, None), (p.clone(), p.clone(), None)])
+    with pytest.raises(ValueError):
+        moe.Adamw([(p, g, p.clone())])
+    with pytest.raises(ValueError):
+        moe.Adamw([(p.double(), g, None)])
