@@ -191,6 +191,13 @@ __device__ __forceinline__ void dma16(const v4u& r, uint32_t lds, uint32_t voff,
                : "m0", "memory");
 }
 
+__device__ __forceinline__ void dma16_nt(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "m0", "memory");
+}
+
 constexpr int waitcnt_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
 
 // A barrier that waits for nothing by itself (a fence's wait would include
@@ -275,9 +282,12 @@ struct TileLoads {
     }
     return t;
   }
+  template <bool kOnce>
   __device__ void load(const Tile& t, int i, uint32_t lds) const {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    dma16(t.r, lds + 1024u * (uint32_t)(w + kNw * i), kRows && !t.ok ? kOob : voff[i], t.soff);
+    const uint32_t to = lds + 1024u * (uint32_t)(w + kNw * i), from = kRows && !t.ok ? kOob : voff[i];
+    if constexpr (kOnce) dma16_nt(t.r, to, from, t.soff);
+    else dma16(t.r, to, from, t.soff);
   }
 };
 
@@ -325,64 +335,81 @@ constexpr int kStageCols = TN < 64 ? TN : 64;
 template <int TN>
 constexpr int kStageBytes = 32 * (kStageCols<TN> * 4 + 16);
 
+// 32 rows of kStageCols<TN> columns: the lane's bias, the residual, the results.
+template <int TN>
+struct Rows32 {
+  static constexpr int W = kStageCols<TN>, kPitch = W * 4 + 16;
+  static constexpr int kLpr = W / 8, kRpp = 64 / kLpr, kIt = 32 / kRpp;   // lanes per row, rows per pass, passes
+  float bias[8];
+  int64_t j;   // the lane's first column
+
+  __device__ __forceinline__ void init(const Epi& e, int64_t j0, int64_t J) {
+    j = j0 + 8 * ((threadIdx.x & 63) % kLpr);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bias[k] = e.bias && j + k < J ? e.bias[j + k] : 0.0f;
+  }
+  __device__ __forceinline__ void fetch(const Epi& e, uint4 (&res)[kIt], int64_t i0, int64_t I, int64_t J) const {
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int64_t i = i0 + kRpp * it + (threadIdx.x & 63) / kLpr;
+      res[it] = make_uint4(0, 0, 0, 0);
+      if (e.residual && e.wide && i < I && j < J) res[it] = *reinterpret_cast<const uint4*>(e.residual + i * J + j);
+    }
+  }
+  template <int kAct>
+  __device__ __forceinline__ void finish(const Epi& e, const v16f* acc, uint8_t* slice, const uint4 (&res)[kIt],
+                                         int64_t i0, int64_t I, int64_t J) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < W / 32; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(slice + (lane & 31) * kPitch + (32 * n + 8 * g + 4 * (lane >> 5)) * 4) =
+            make_float4(acc[n][4 * g], acc[n][4 * g + 1], acc[n][4 * g + 2], acc[n][4 * g + 3]);
+    // exchanged between the wave's lanes, whose LDS accesses run in order
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      const int row = kRpp * it + lane / kLpr;
+      const float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * (lane % kLpr));
+      const float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * (lane % kLpr) + 16);
+      const int64_t i = i0 + row;
+      if (i < I && j < J) {
+        float v[8] = {x.x + bias[0], x.y + bias[1], x.z + bias[2], x.w + bias[3],
+                      y.x + bias[4], y.y + bias[5], y.z + bias[6], y.w + bias[7]};
+        finish8(e, kAct, v, res[it], i, j, J);
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+};
+
 template <int TM, int TN, int kAct, typename Sums>
 __device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
                                          int64_t j0, int64_t I, int64_t J, Sums sums) {
-  constexpr int FM = TM / 32, FN = TN / 32, W = kStageCols<TN>, kPitch = W * 4 + 16;
-  constexpr int kLpr = W / 8, kRpp = 64 / kLpr, kIt = 32 / kRpp;   // lanes per row, rows per pass, passes
-  const int lane = threadIdx.x & 63;
-  const int wr = lane & 31, h = lane >> 5;
-  const int rr = lane / kLpr, c8 = lane % kLpr;
+  constexpr int FM = TM / 32, FN = TN / 32, W = kStageCols<TN>;
 #pragma unroll
   for (int n0 = 0; n0 < FN; n0 += W / 32) {
-    const int64_t j = j0 + 32 * n0 + 8 * c8;
-    float bias[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) bias[k] = e.bias && j + k < J ? e.bias[j + k] : 0.0f;
-    uint4 res[2][kIt];
-    auto fetch = [&](int m) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int64_t i = i0 + 32 * m + kRpp * it + rr;
-        res[m & 1][it] = make_uint4(0, 0, 0, 0);
-        if (e.residual && e.wide && i < I && j < J)
-          res[m & 1][it] = *reinterpret_cast<const uint4*>(e.residual + i * J + j);
-      }
-    };
-    fetch(0);
+    Rows32<TN> rows;
+    uint4 res[2][Rows32<TN>::kIt];
+    rows.init(e, j0 + 32 * n0, J);
+    rows.fetch(e, res[0], i0, I, J);
     if (n0 == 0) sums();
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
-      if (m + 1 < FM) fetch(m + 1);
-#pragma unroll
-      for (int n = 0; n < W / 32; ++n)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<float4*>(slice + wr * kPitch + (32 * n + 8 * g + 4 * h) * 4) =
-              make_float4(acc[m][n0 + n][4 * g], acc[m][n0 + n][4 * g + 1], acc[m][n0 + n][4 * g + 2],
-                          acc[m][n0 + n][4 * g + 3]);
-      // exchanged between the wave's lanes, whose LDS accesses run in order
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int row = kRpp * it + rr;
-        const float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8);
-        const float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * c8 + 16);
-        const int64_t i = i0 + 32 * m + row;
-        if (i < I && j < J) {
-          float v[8] = {x.x + bias[0], x.y + bias[1], x.z + bias[2], x.w + bias[3],
-                        y.x + bias[4], y.y + bias[5], y.z + bias[6], y.w + bias[7]};
-          finish8(e, kAct, v, res[m & 1][it], i, j, J);
-        }
-      }
-      asm volatile("" ::: "memory");
+      if (m + 1 < FM) rows.fetch(e, res[(m + 1) & 1], i0 + 32 * (m + 1), I, J);
+      rows.template finish<kAct>(e, &acc[m][n0], slice, res[m & 1], i0 + 32 * m, I, J);
     }
   }
 }
 
+// The operand whose every element one workgroup alone reads (the other has one
+// row of tiles): its loads are non-temporal.
+enum { kOnceNone, kOnceA, kOnceB };
+
 // BM x BN result tile, kWm x kWn waves, kSlots LDS tiles of kC contraction
 // elements in flight.
-template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct>
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct, int kOnce>
 __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   constexpr int kNw = kWm * kWn;
   constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
@@ -435,8 +462,8 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   typename decltype(lb)::Tile tb;
   uint32_t dst = 0;
   auto load = [&](int i) {   // load i of the tile in hand
-    if (i < kLa) la.load(ta, i, dst);
-    else lb.load(tb, i - kLa, dst + kABytes);
+    if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, dst);
+    else lb.template load<kOnce == kOnceB>(tb, i - kLa, dst + kABytes);
   };
   auto hand = [&](int64_t t, int s) {
     ta = la.prepare(t, p.C);
@@ -460,8 +487,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   // products: a burst of either stalls the products behind it.
   constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
   // with two slots a tile has one tile's time to arrive: its loads all go into the first part
-  // (one slot serves a contraction of one tile, which loads nothing here)
-  constexpr int kPerPart = kSlots <= 2 ? kLoads : (kLoads + kParts - 1) / kParts;
+  constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
   v8bf_s a[2][FM], b[2][FN];
   // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
   auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
@@ -522,6 +548,77 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
     return;
   }
   epilogue<TM, TN, kAct>(p.epi, acc, lds + wave * kStageBytes<TN>, i0 + wm * TM, j0 + wn * TN, p.I, p.J, [] {});
+}
+
+// Contractions of at most 64 (A stored by rows): the output is all the cost.
+// A workgroup keeps a B tile of 256 columns, each wave 64 of them as fragments
+// in registers, and goes over blocks of 32 rows, every `splits`-th, so that the
+// card writes whole rows together; the next block's rows of A and its residual
+// are on the way while one is finished.
+constexpr int kShortCols = 256;
+constexpr int kShortPerCu = 3;
+
+template <bool kBRows, int kAct>
+__global__ void __launch_bounds__(256, kShortPerCu) k_short(Product p) {
+  constexpr int kTile = kShortCols * 64 * 2;
+  constexpr int kLds = kTile > 4 * kStageBytes<64> ? kTile : 4 * kStageBytes<64>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t j0 = (int64_t)(blockIdx.x % p.tiles_j) * kShortCols, jw = j0 + 64 * wave;
+  TileLoads<kBRows, kShortCols, 4, 64> lb;
+  FragAt<kBRows, kShortCols, 64> fb;
+  lb.init(p.b, j0, p.J, p.C);
+  fb.init();
+  const auto tb = lb.prepare(0, p.C);
+#pragma unroll
+  for (int i = 0; i < lb.kLoads; ++i) lb.template load<false>(tb, i, (uint32_t)(uintptr_t)(const lds_void*)lds);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  lds_barrier();
+  v8bf_s b[4][2];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) b[kk][n] = fb.read(lds, 64 * wave + 32 * n, kk);
+  __syncthreads();   // read: the waves' slices take the tile's place
+  if (jw >= p.J) return;
+  uint8_t* slice = lds + wave * kStageBytes<64>;
+  Rows32<64> rows;
+  rows.init(p.epi, jw, p.J);
+
+  const int64_t blocks = (p.I + 31) / 32;
+  v8bf_s a[4];
+  uint4 res[Rows32<64>::kIt];
+  auto fetch = [&](int64_t blk) {
+    const int64_t left = p.I - 32 * blk;   // rows (none past the end: nothing is read)
+    const int64_t n = left < 0 ? 0 : (left < 32 ? left : 32);
+    const __amdgpu_buffer_rsrc_t r = buf(p.a.p + (n ? 32 * blk : 0) * p.a.ld, n * p.a.ld * 2);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int c = 16 * kk + 8 * (lane >> 5);
+      const uint32_t off = (uint32_t)(lane & 31) * (uint32_t)p.a.ld * 2u + 2u * (uint32_t)c;
+      a[kk] = __builtin_bit_cast(v8bf_s, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(c < p.C ? off : kOob), 0, 0));
+    }
+    rows.fetch(p.epi, res, 32 * blk, p.I, p.J);
+  };
+  int64_t blk = blockIdx.x / p.tiles_j;
+  fetch(blk);
+  for (; blk < blocks; blk += p.splits) {
+    v16f acc[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[n][r] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[kk][n], a[kk], acc[n], 0, 0, 0);
+    uint4 now[Rows32<64>::kIt];
+#pragma unroll
+    for (int it = 0; it < Rows32<64>::kIt; ++it) now[it] = res[it];
+    fetch(blk + p.splits);
+    rows.template finish<kAct>(p.epi, acc, slice, now, 32 * blk, p.I, p.J);
+  }
 }
 
 // The split tiles: one wave per 32 rows of a wave's share of a tile adds the
@@ -729,7 +826,7 @@ __global__ void __launch_bounds__(256) k_dbias(const float* __restrict__ part, i
 constexpr int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // Tile shapes.
-enum Shape { k256x256, k128x128, k128x128One, k128x64, k64x64, kShapes };
+enum Shape { k256x256, k128x128, k128x64, k64x128, k64x64, kShapes };
 constexpr struct {
   int bm, bn, per_cu;   // workgroups per CU (LDS)
   double us;            // microseconds per 64 c of a round with all slots busy and operands in L2
@@ -737,8 +834,8 @@ constexpr struct {
 } kShape[kShapes] = {
     {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
     {128, 128, 2, 1.13, 4.9e6},
-    {128, 128, 4, 2.2, 4.9e6},    // one LDS tile: contractions up to 64 (8191 x 7168 x 64: 56 us, against 61)
     {128, 64, 1, 0.70, 5.6e6},    // 32768 x 64 x 7168: 86 us, against 94 with 64 x 64
+    {64, 128, 1, 0.70, 5.6e6},
     {64, 64, 2, 0.50, 4.9e6}};
 
 // Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
@@ -755,8 +852,6 @@ Plan plan_product(int64_t I, int64_t J, int64_t C) {
   Plan best{};
   double least = 1e30;
   for (int id = 0; id < kShapes; ++id) {
-    // one LDS tile: the output is the cost, and four workgroups per CU overlap it best
-    if (C <= 64 ? id == k256x256 || id == k128x128 : id == k128x128One) continue;
     const auto& sh = kShape[id];
     const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn, t = ti * tj;
     const int64_t slots = sh.per_cu * kCus, rounds = t / slots, rem = t - rounds * slots;
@@ -781,27 +876,50 @@ Plan plan_product(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
-template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct>
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct, int kOnce = kOnceNone>
 void launch_shape(const Product& p, hipStream_t st) {
   auto up8 = [](int32_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
   const int32_t tail = p.tiles_i * p.tiles_j - p.full;
   const dim3 grid((unsigned)(up8(p.full) + up8(tail * p.splits)));
-  hipLaunchKernelGGL((k_product<BM, BN, kWm, kWn, kC, kSlots, kARows, kBRows, kAct>), grid, dim3(64 * kWm * kWn), 0, st, p);
+  hipLaunchKernelGGL((k_product<BM, BN, kWm, kWn, kC, kSlots, kARows, kBRows, kAct, kOnce>), grid, dim3(64 * kWm * kWn), 0, st, p);
   if (tail)
     hipLaunchKernelGGL((k_join<BM, BN, kWm, kWn, kAct>), dim3((unsigned)(BM / 32 * kWn * tail)), dim3(64), 0, st, p);
+}
+
+// A narrow tile's launch.
+template <int BM, int BN, int kSlots, bool kARows, bool kBRows, int kAct>
+void launch_narrow(const Product& p, hipStream_t st) {
+  if (p.tiles_j == 1) launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, kAct, kOnceA>(p, st);
+  else if (p.tiles_i == 1) launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, kAct, kOnceB>(p, st);
+  else launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, kAct>(p, st);
+}
+
+template <bool kBRows, int kAct>
+int launch_short(Product& p, hipStream_t st) {
+  const int64_t tj = (p.J + kShortCols - 1) / kShortCols, blocks = (p.I + 31) / 32;
+  int64_t s = kShortPerCu * kCus / tj;
+  s = s > blocks ? blocks : s;
+  p.tiles_j = (int32_t)tj;
+  p.splits = (int32_t)(s < 1 ? 1 : s);
+  hipLaunchKernelGGL((k_short<kBRows, kAct>), dim3((unsigned)(tj * p.splits)), dim3(256), 0, st, p);
+  return launch_status();
 }
 
 template <bool kARows, bool kBRows, int kAct>
 int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int64_t C, const Epi& epi, float* part,
                    hipStream_t st) {
-  const Plan pl = plan_product(I, J, C);
-  const auto& sh = kShape[pl.shape];
   Product p;
   p.a = a;
   p.b = b;
   p.I = I;
   p.J = J;
   p.C = C;
+  p.epi = epi;
+  if constexpr (kARows) {
+    if (C <= 64) return launch_short<kBRows, kAct>(p, st);
+  }
+  const Plan pl = plan_product(I, J, C);
+  const auto& sh = kShape[pl.shape];
   const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn;
   if (ti * tj >= (1ll << 28)) return MX_EUNSUPPORTED;
   p.tiles_i = (int32_t)ti;
@@ -810,13 +928,12 @@ int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int
   p.splits = pl.splits;
   p.split_c = pl.split_c;
   p.part = part;
-  p.epi = epi;
   switch (pl.shape) {
     case k256x256: launch_shape<256, 256, 2, 4, 64, 2, kARows, kBRows, kAct>(p, st); break;
     case k128x128: launch_shape<128, 128, 2, 2, 64, 2, kARows, kBRows, kAct>(p, st); break;
-    case k128x128One: launch_shape<128, 128, 2, 2, 64, 1, kARows, kBRows, kAct>(p, st); break;
-    case k128x64: launch_shape<128, 64, 2, 2, 64, 5, kARows, kBRows, kAct>(p, st); break;
-    default: launch_shape<64, 64, 2, 2, 64, 4, kARows, kBRows, kAct>(p, st); break;
+    case k128x64: launch_narrow<128, 64, 5, kARows, kBRows, kAct>(p, st); break;
+    case k64x128: launch_narrow<64, 128, 5, kARows, kBRows, kAct>(p, st); break;
+    default: launch_narrow<64, 64, 4, kARows, kBRows, kAct>(p, st); break;
   }
   return launch_status();
 }
