@@ -107,13 +107,21 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
 }
 
+template <bool kNt>
+__device__ __forceinline__ void store16(void* to, const uint4& v) {
+  const v4u w = {v.x, v.y, v.z, v.w};
+  if constexpr (kNt) __builtin_nontemporal_store(w, static_cast<v4u*>(to));
+  else *static_cast<v4u*>(to) = w;
+}
+
 // z of 8 consecutive columns of one row (bias added) to the results; res: the
-// residual's 8 values where accesses are wide.
+// residual's 8 values where accesses are wide.  kNt: non-temporal wide stores.
+template <bool kNt>
 __device__ __forceinline__ void finish8(const Epi& e, int act, float (&v)[8], const uint4& res, int64_t i, int64_t j,
                                         int64_t J) {
   const int64_t at = i * J + j;
   if (e.wide) {
-    if (e.z) *reinterpret_cast<uint4*>(e.z + at) = pack8(v);
+    if (e.z) store16<kNt>(e.z + at, pack8(v));
     if (act != MX_ACT_NONE) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], act);
@@ -128,10 +136,11 @@ __device__ __forceinline__ void finish8(const Epi& e, int act, float (&v)[8], co
     }
     if (e.f32) {
       float* o = static_cast<float*>(e.out) + at;
-      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      const v4f_s lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+      store16<kNt>(o, __builtin_bit_cast(uint4, lo));
+      store16<kNt>(o + 4, __builtin_bit_cast(uint4, hi));
     } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at) = pack8(v);
+      store16<kNt>(static_cast<uint16_t*>(e.out) + at, pack8(v));
     }
     return;
   }
@@ -356,7 +365,7 @@ struct Rows32 {
       if (e.residual && e.wide && i < I && j < J) res[it] = *reinterpret_cast<const uint4*>(e.residual + i * J + j);
     }
   }
-  template <int kAct>
+  template <int kAct, bool kNt>
   __device__ __forceinline__ void finish(const Epi& e, const v16f* acc, uint8_t* slice, const uint4 (&res)[kIt],
                                          int64_t i0, int64_t I, int64_t J) const {
     const int lane = threadIdx.x & 63;
@@ -377,7 +386,7 @@ struct Rows32 {
       if (i < I && j < J) {
         float v[8] = {x.x + bias[0], x.y + bias[1], x.z + bias[2], x.w + bias[3],
                       y.x + bias[4], y.y + bias[5], y.z + bias[6], y.w + bias[7]};
-        finish8(e, kAct, v, res[it], i, j, J);
+        finish8<kNt>(e, kAct, v, res[it], i, j, J);
       }
     }
     asm volatile("" ::: "memory");
@@ -398,7 +407,7 @@ __device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN /
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
       if (m + 1 < FM) rows.fetch(e, res[(m + 1) & 1], i0 + 32 * (m + 1), I, J);
-      rows.template finish<kAct>(e, &acc[m][n0], slice, res[m & 1], i0 + 32 * m, I, J);
+      rows.template finish<kAct, false>(e, &acc[m][n0], slice, res[m & 1], i0 + 32 * m, I, J);
     }
   }
 }
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(256, kShortPerCu) k_short(Product p) {
 #pragma unroll
     for (int it = 0; it < Rows32<64>::kIt; ++it) now[it] = res[it];
     fetch(blk + p.splits);
-    rows.template finish<kAct>(p.epi, acc, slice, now, 32 * blk, p.I, p.J);
+    rows.template finish<kAct, true>(p.epi, acc, slice, now, 32 * blk, p.I, p.J);
   }
 }
 
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __rest
     }
     uint4 res = make_uint4(0, 0, 0, 0);
     if (epi.residual && epi.wide) res = *reinterpret_cast<const uint4*>(epi.residual + m * N + j);
-    finish8(epi, epi.act, v, res, m, j, N);
+    finish8<false>(epi, epi.act, v, res, m, j, N);
   }
 }
 
@@ -834,9 +843,9 @@ constexpr struct {
 } kShape[kShapes] = {
     {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
     {128, 128, 2, 1.13, 4.9e6},
-    {128, 64, 1, 0.70, 5.6e6},    // 32768 x 64 x 7168: 86 us, against 94 with 64 x 64
-    {64, 128, 1, 0.70, 5.6e6},
-    {64, 64, 2, 0.50, 4.9e6}};
+    {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 94 with 64 x 64
+    {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
+    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18 us, against 24 with 128 x 64
 
 // Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
 // tiles of the last, partly filled round are split over the contraction so
