@@ -734,6 +734,9 @@ __global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __rest
 // dz = dout act'(z) in bf16 with rows of pitch elements (zeros past N), and
 // fp32 column sums of the unrounded dz over the block's rows: `part`
 // [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
+template <typename T>
+__device__ __forceinline__ T load_once(const void* p) { return __builtin_nontemporal_load(static_cast<const T*>(p)); }
+
 template <bool kF32>
 __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const uint16_t* __restrict__ z, int64_t M,
                                             int64_t N, int64_t pitch, int32_t act, int32_t ct, int64_t rows_per,
@@ -753,12 +756,15 @@ __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const
       const int64_t at = r * N + j;
       if (wide) {
         if constexpr (kF32) {
-          const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at);
-          const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at + 4);
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+          const v4f_s a = load_once<v4f_s>(static_cast<const float*>(dout) + at);
+          const v4f_s b = load_once<v4f_s>(static_cast<const float*>(dout) + at + 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[k] = a[k];
+            v[4 + k] = b[k];
+          }
         } else {
-          const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dout) + at);
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+          const v4u w = load_once<v4u>(static_cast<const uint16_t*>(dout) + at);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[2 * k] = bf_lo(w[k]);
@@ -774,8 +780,7 @@ __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const
       }
       if (act != MX_ACT_NONE) {
         if (wide) {
-          const uint4 a = *reinterpret_cast<const uint4*>(z + at);
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+          const v4u w = load_once<v4u>(z + at);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[2 * k] *= act_slope(bf_lo(w[k]), act);
