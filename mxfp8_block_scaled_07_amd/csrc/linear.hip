@@ -11,28 +11,21 @@
 // the transposing reads (ds_read_b64_tr_b16), so no operand is ever
 // transposed in memory.
 //
-// Up to 64 tokens the forward streams w once through the code of skinny.h.
+// Up to 16 rows the forward streams w once through the code of stream.h.
 // Sums are fp32 in a fixed order; where the tiles are too few for the card
 // the contraction is split over workgroups, whose fp32 partial sums are
 // added in order by a second launch with the same epilogue.
 
-#include "skinny.h"
-
-#pragma clang diagnostic ignored "-Winline-asm"
+#include "stream.h"
 
 namespace mx {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef unsigned int v4u __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-constexpr int kCus = 256;                    // MI355X
 constexpr int kXcds = 8;
-constexpr uint32_t kOob = 0x80000000u;       // an offset that reads as zero
-constexpr int kSkinny = 64;                  // most rows of the streaming form
 
 // ---------------------------------------------------------------- activations
 // e^x for x <= 0 by the hardware's 2^x: its relative error grows with |x| (the
@@ -136,7 +129,7 @@ __device__ __forceinline__ void finish8(const Epi& e, int act, float (&v)[8], co
     }
     if (e.f32) {
       float* o = static_cast<float*>(e.out) + at;
-      const v4f_s lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+      const v4f lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
       store16<kNt>(o, __builtin_bit_cast(uint4, lo));
       store16<kNt>(o + 4, __builtin_bit_cast(uint4, hi));
     } else {
@@ -184,34 +177,9 @@ __device__ __forceinline__ void tile_at(const Product& p, int32_t q, int bm, int
   j0 = (int64_t)(in / rows) * bn;
 }
 
-__device__ __forceinline__ v4u rsrc(const void* base, int64_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  const uint32_t n = bytes <= 0 ? 0u : (bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes);
-  return v4u{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, n, 0x00020000u};
-}
-
-// One LDS-direct load of 16 bytes per lane, to LDS byte lds + 16 lane.  Inline
-// asm, so that the compiler puts no wait of its own before LDS reads: every
-// wait on these loads is an explicit vmcnt before a barrier.
-__device__ __forceinline__ void dma16(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "m0", "memory");
-}
-
-__device__ __forceinline__ void dma16_nt(const v4u& r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "m0", "memory");
-}
-
-constexpr int waitcnt_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
-
 // A barrier that waits for nothing by itself (a fence's wait would include
 // loads still in flight); nothing may be moved across it.
-__device__ __forceinline__ void lds_barrier() {
+__device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -320,15 +288,15 @@ struct FragAt {
     }
   }
   // i0: the fragment's first row inside the tile, a multiple of 32
-  __device__ v8bf_s read(const uint8_t* tile, int i0, int kk) const {
+  __device__ v8bf read(const uint8_t* tile, int i0, int kk) const {
     if constexpr (kRows) {
-      return *reinterpret_cast<const v8bf_s*>(tile + i0 * (2 * kC) + row + 16 * ((2 * kk + lo) ^ sw));
+      return *reinterpret_cast<const v8bf*>(tile + i0 * (2 * kC) + row + 16 * ((2 * kk + lo) ^ sw));
     } else {
       const uint8_t* p = tile + kk * 16 * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
       // c .. c + 3 and c + 4 .. c + 7: the swizzle depends on c & 3 only
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
       const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * R));
-      return __builtin_bit_cast(v8bf_s, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
@@ -488,7 +456,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
     }
   if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
   else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  lds_barrier();
+  bare_barrier();
 
   // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
   // are read during the part before it, and the loads into the slot that the
@@ -497,7 +465,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
   constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
   // with two slots a tile has one tile's time to arrive: its loads all go into the first part
   constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
-  v8bf_s a[2][FM], b[2][FN];
+  v8bf a[2][FM], b[2][FN];
   // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
   auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
 #pragma unroll
@@ -535,7 +503,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product p) {
     if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     // ... and after the barrier every wave's: the slot takes tile t + kSlots
-    lds_barrier();
+    bare_barrier();
     fill = t + kSlots < t1;
     hand(t + kSlots, slot);
     // (after the last tile this reads an old slot, which is not used)
@@ -583,8 +551,8 @@ __global__ void __launch_bounds__(256, kShortPerCu) k_short(Product p) {
 #pragma unroll
   for (int i = 0; i < lb.kLoads; ++i) lb.template load<false>(tb, i, (uint32_t)(uintptr_t)(const lds_void*)lds);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  lds_barrier();
-  v8bf_s b[4][2];
+  bare_barrier();
+  v8bf b[4][2];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -596,7 +564,7 @@ __global__ void __launch_bounds__(256, kShortPerCu) k_short(Product p) {
   rows.init(p.epi, jw, p.J);
 
   const int64_t blocks = (p.I + 31) / 32;
-  v8bf_s a[4];
+  v8bf a[4];
   uint4 res[Rows32<64>::kIt];
   auto fetch = [&](int64_t blk) {
     const int64_t left = p.I - 32 * blk;   // rows (none past the end: nothing is read)
@@ -606,7 +574,7 @@ __global__ void __launch_bounds__(256, kShortPerCu) k_short(Product p) {
     for (int kk = 0; kk < 4; ++kk) {
       const int c = 16 * kk + 8 * (lane >> 5);
       const uint32_t off = (uint32_t)(lane & 31) * (uint32_t)p.a.ld * 2u + 2u * (uint32_t)c;
-      a[kk] = __builtin_bit_cast(v8bf_s, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(c < p.C ? off : kOob), 0, 0));
+      a[kk] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(c < p.C ? off : kOob), 0, 0));
     }
     rows.fetch(p.epi, res, 32 * blk, p.I, p.J);
   };
@@ -667,67 +635,167 @@ __global__ void __launch_bounds__(64) k_join(Product p) {
 }
 
 // ---------------------------------------------------------------- few rows
-// A workgroup owns 16 rows of w; its eight waves take steps of 128 k in turn.
+// At most 16 rows of x: items of 16 rows of w, each workgroup a run of them.
+// Its eight waves take the chunks of 256 bytes of the items' rows in turn, from
+// rings that go on from one item to the next, and add up through LDS.  x stays
+// in registers, kSkSteps chunks of a wave.  8192 x 5120 (84 MB): 16.7 us for one
+// row (5.0 TB/s), 19.7 for 16; 128 x 64 tiles take 23.5 for 1 to 64 rows.  (With
+// k above 8192 x would have to be read again for each item: 1408 x 16384 took
+// 22 us for one row and 30 for 16, the tiles take 22.5.)
 constexpr int kSkWaves = 8;
+constexpr int kSkDepth = 3;                  // chunks of a wave in flight
+constexpr int kSkItems = 4;                  // items whose sums wait for each other
+constexpr int kSkSlot = 2 * 2048;            // two lines of 16 rows
+constexpr int kSkSteps = 8;
+constexpr int kSkRows = 16;
+constexpr int64_t kSkK = 128 * kSkWaves * kSkSteps;
+bool few_rows(int64_t rows, int64_t k) { return rows <= kSkRows && k <= kSkK; }
 
-template <int NT>
-__global__ void __launch_bounds__(64 * kSkWaves) k_skinny(const uint16_t* __restrict__ x,
-                                                          const uint16_t* __restrict__ w, int64_t M, int64_t N,
-                                                          int64_t K, Epi epi) {
-  __shared__ float red[kSkWaves][NT][4][64];
+__global__ void __launch_bounds__(64 * kSkWaves, 2) k_skinny(const uint16_t* __restrict__ x,
+                                                             const uint16_t* __restrict__ w, int64_t M, int64_t N,
+                                                             int64_t K, Epi epi) {
+  __shared__ __attribute__((aligned(16))) float red[kSkItems][kSkWaves][4][64];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kSkWaves][kSkDepth][kSkSlot];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15;
-  const int64_t n0 = 16 * (int64_t)blockIdx.x;
-  const int64_t rows = N - n0 < 16 ? N - n0 : 16;
-  WRows<false> wr;
-  wr.q = buf(w + n0 * K, rows * K * 2);
-  const __amdgpu_buffer_rsrc_t xr = buf(x, M * K * 2);
-  uint32_t off[NT];
-  v4f_s acc[NT];
+  const int r = lane & 15, h = lane >> 4;
+  const int items = (int)((N + 15) / 16);
+  const int begin = (int)((int64_t)items * blockIdx.x / gridDim.x), end = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+  const int64_t row_bytes = 2 * K;
+  const int chunks = (int)((row_bytes + 255) / 256);
+  const int per = (chunks + kSkWaves - 1) / kSkWaves;   // a wave takes chunks wave, wave + 8, ...
+
+  // the loads' cursor
+  int li = begin, ls = 0, seq = 0;
+  v4u lq;
+  auto open = [&](int item) {
+    const int64_t n0 = 16 * (int64_t)item;
+    lq = rsrc(w + n0 * K, (N - n0 < 16 ? N - n0 : 16) * row_bytes);
+  };
+  open(begin);
+  uint32_t lane_off[2];
+  int32_t lane_c[2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int m = 16 * t + r;
-    off[t] = m < M ? 2u * (uint32_t)m * (uint32_t)K : kNoRow;
-    acc[t] = v4f_s{0.f, 0.f, 0.f, 0.f};
+  for (int q = 0; q < 2; ++q) {
+    const int row = 8 * q + (lane >> 3);
+    lane_c[q] = 16 * ((lane & 7) ^ chunk_swizzle(row));
+    lane_off[q] = (uint32_t)row * (uint32_t)row_bytes + (uint32_t)lane_c[q];
   }
-  const int steps = (int)((K + kStepK - 1) / kStepK);
-  for (int s = wave; s < steps; s += kSkWaves) {
-    WStep<false> ws;
-    XStep xs[NT];
-    load_w<false>(ws, wr, (uint32_t)r, (uint32_t)K, (uint32_t)(s * kStepK), r < rows);
+  auto load = [&]() {
+    const uint32_t dst = lds_addr(ring[wave][0]) + (uint32_t)(seq % kSkDepth) * kSkSlot;
+    const int c = wave + kSkWaves * ls;
+    const bool in = li < end && c < chunks;
+    const int32_t left = in ? (int32_t)(row_bytes - 256 * (int64_t)c) : 0;   // bytes of the rows from here on
+    const uint32_t soff = in ? 256u * (uint32_t)c : 0u;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) load_x(xs[t], xr, off[t], (uint32_t)K, (uint32_t)(s * kStepK));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) mma_step<false>(acc[t], ws, xs[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][t][i][lane] = acc[t][i];
-  __syncthreads();
-  // thread: 8 of the 16 columns of one row
-  for (int q = tid; q < 2 * M; q += 64 * kSkWaves) {
-    const int m = q >> 1, c0 = 8 * (q & 1);
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = c0 + k;
-      v[k] = 0.0f;
-#pragma unroll
-      for (int g = 0; g < kSkWaves; ++g) v[k] += red[g][m >> 4][c & 3][16 * (c >> 2) + (m & 15)];
+    for (int q = 0; q < 4; ++q)   // (rows past N are past the buffer's end)
+      dma16_nt(lq, dst + 1024u * q, lane_c[q & 1] + 128 * (q >> 1) < left ? lane_off[q & 1] + 128u * (q >> 1) : kOob, soff);
+    ++seq;
+    if (++ls == per) {
+      ls = 0;
+      if (++li < end) open(li);
     }
-    const int64_t j = n0 + c0;
-    if (j >= N) continue;
-    if (epi.bias) {
+  };
+
+  v8bf xv[kSkSteps][2][2];
+  const __amdgpu_buffer_rsrc_t xr = buf(x, M * row_bytes);
+  auto tokens = [&] {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (j + k < N) v[k] += epi.bias[j + k];
+    for (int s = 0; s < kSkSteps; ++s) {
+      if (s >= per) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // line i >> 1 of the chunk, half of the lane's 32 bytes
+        const int64_t at = 256 * (int64_t)(wave + kSkWaves * s) + 128 * (i >> 1) + 32 * h + 16 * (i & 1);
+        const uint32_t off = r < M && at < row_bytes ? (uint32_t)r * (uint32_t)row_bytes + (uint32_t)at : kOob;
+        xv[s][i >> 1][i & 1] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)off, 0, 0));
+      }
     }
-    uint4 res = make_uint4(0, 0, 0, 0);
-    if (epi.residual && epi.wide) res = *reinterpret_cast<const uint4*>(epi.residual + m * N + j);
-    finish8<false>(epi, epi.act, v, res, m, j, N);
+  };
+
+  // The items are finished kSkItems at a time: after each, the waves would wait
+  // for each other with the stream running dry.  A thread takes 8 of the 16
+  // columns of one row; what it adds is fetched ahead, as a compiled load that
+  // is waited for in between would wait for the stream's loads too.
+  struct Tail {
+    float bias[8];
+    uint4 res;
+  };
+  const int ti = tid >> 5, m = (tid & 31) >> 1, c0 = 8 * (tid & 1);
+  auto tail = [&](int item0) {
+    Tail t{};
+    const int64_t j = 16 * (int64_t)(item0 + ti) + c0;
+    if (ti < kSkItems && m < M && item0 + ti < end && j < N) {
+      if (epi.bias) {
+        if (epi.wide) {
+          __builtin_memcpy(t.bias, epi.bias + j, 32);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (j + k < N) t.bias[k] = epi.bias[j + k];
+        }
+      }
+      if (epi.residual && epi.wide) t.res = *reinterpret_cast<const uint4*>(epi.residual + m * N + j);
+    }
+    return t;
+  };
+
+  // x lies between the first chunks, and is waited for here: else the compiler
+  // waits at each use, and for the stream's loads too
+#pragma unroll 1
+  for (int d = 0; d < kSkDepth - 1; ++d) load();
+  Tail t = tail(begin);
+  tokens();
+  load();
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(4));
+  int used = 0;
+  for (int item = begin; item < end; ++item) {
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kSkSteps; ++s) {
+      if (s < per) {
+        // the oldest chunk's loads are done, the others may be in flight
+        fence();
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(4 * (kSkDepth - 1)));
+        fence();
+        const uint8_t* slot = ring[wave][used % kSkDepth];
+        const Fragment f0 = read_fragment<false>(slot, nullptr), f1 = read_fragment<false>(slot + 2048, nullptr);
+        fence();
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);   // read: the slot is free
+        fence();
+        load();
+        ++used;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<false>(f0, j, 1.0f), xv[s][0][j], acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights8<false>(f1, j, 1.0f), xv[s][1][j], acc, 0, 0, 0);
+        }
+      }
+    }
+    const int at = (item - begin) % kSkItems;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[at][wave][i][lane] = acc[i];
+    if (at < kSkItems - 1 && item + 1 < end) continue;
+    lds_barrier();
+    const int64_t j = 16 * (int64_t)(item - at + ti) + c0;
+    if (ti <= at && m < M && j < N) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + k;
+        v[k] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kSkWaves; ++g) v[k] += red[ti][g][c & 3][16 * (c >> 2) + m];
+        v[k] += t.bias[k];
+      }
+      finish8<false>(epi, epi.act, v, t.res, m, j, N);
+    }
+    if (item + 1 < end) {
+      t = tail(item + 1);
+      lds_barrier();
+    }
   }
+  // loads past the last item may still be writing LDS
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
 }
 
 // ---------------------------------------------------------------- dz and dbias
@@ -756,8 +824,8 @@ __global__ void __launch_bounds__(256) k_dz(const void* __restrict__ dout, const
       const int64_t at = r * N + j;
       if (wide) {
         if constexpr (kF32) {
-          const v4f_s a = load_once<v4f_s>(static_cast<const float*>(dout) + at);
-          const v4f_s b = load_once<v4f_s>(static_cast<const float*>(dout) + at + 4);
+          const v4f a = load_once<v4f>(static_cast<const float*>(dout) + at);
+          const v4f b = load_once<v4f>(static_cast<const float*>(dout) + at + 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[k] = a[k];
@@ -992,7 +1060,7 @@ BwdSpace bwd_space(int64_t M, int64_t N, int64_t K) {
 using namespace mx;
 
 extern "C" size_t mx_bf16_linear_workspace_size(int64_t rows, int64_t n, int64_t k) {
-  if (rows <= kSkinny || n <= 0 || k <= 0 || too_large(rows, n, k)) return 0;
+  if (rows <= 0 || n <= 0 || k <= 0 || few_rows(rows, k) || too_large(rows, n, k)) return 0;
   return (size_t)plan_product(rows, n, k).part_bytes;
 }
 
@@ -1015,11 +1083,10 @@ extern "C" int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float*
   epi.act = act;
   epi.f32 = out_dtype == MX_OUT_F32;
   epi.wide = n % 8 == 0;
-  if (rows <= kSkinny) {
-    const dim3 grid((unsigned)((n + 15) / 16)), block(64 * kSkWaves);
-    if (rows <= 16) hipLaunchKernelGGL(k_skinny<1>, grid, block, 0, st, x, w, rows, n, k, epi);
-    else if (rows <= 32) hipLaunchKernelGGL(k_skinny<2>, grid, block, 0, st, x, w, rows, n, k, epi);
-    else hipLaunchKernelGGL(k_skinny<4>, grid, block, 0, st, x, w, rows, n, k, epi);
+  if (few_rows(rows, k)) {
+    const int64_t items = (n + 15) / 16;
+    const dim3 grid((unsigned)(items < kCus ? items : kCus));
+    hipLaunchKernelGGL(k_skinny, grid, dim3(64 * kSkWaves), 0, st, x, w, rows, n, k, epi);
     return launch_status();
   }
   const int64_t need = plan_product(rows, n, k).part_bytes;

@@ -96,7 +96,11 @@ class Case:
 # columns that are not a multiple of 8, one column
 SIZES = [(1, 8, 32), (1, 100, 96), (5, 64, 160), (16, 33, 544), (17, 48, 256), (64, 200, 2048), (65, 64, 64),
          (66, 1, 32), (100, 7, 352), (200, 130, 96), (257, 300, 224), (1000, 60, 2048), (300, 1000, 4096),
-         (3000, 200, 320), (70, 2100, 1536), (4100, 3900, 96), (2500, 2700, 1120)]
+         (3000, 200, 320), (70, 2100, 1536), (4100, 3900, 96), (2500, 2700, 1120),
+         # few rows: several items per workgroup, k past the registers; short contractions over several blocks;
+         # whole rounds of tiles before a split one; the narrow tiles of a gate and of its weight gradient
+         (3, 8209, 640), (16, 4500, 9248), (9, 40, 16416), (9000, 520, 64), (8191, 40, 2048), (4100, 4300, 1088),
+         (8200, 64, 4096)]
 
 
 @pytest.mark.parametrize("size", SIZES)
