@@ -409,12 +409,17 @@ def _tensor(name, t, shape, dtype, device=None):
     _need(device is None or t.device == device, f"{name} is on {t.device}, not {device}")
 
 
-def _on(device):
-    """The tensors' device as the current one, whose current stream a call without a stream uses."""
+def _on(device, stream):
+    """The tensors' device as the current one, and the call's stream as its current stream: what a helper allocates
+    inside belongs to that stream, so the memory is not handed out again before the call's kernels have run."""
     import contextlib
 
     import torch
-    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+    if device.type != "cuda":
+        return contextlib.nullcontext()
+    if stream is None:
+        return torch.cuda.device(device)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
 
 
 def moe_tokens(x, logits, topk, w1, w2, residual=None, stream=None):
@@ -438,11 +443,11 @@ def moe_tokens(x, logits, topk, w1, w2, residual=None, stream=None):
         _tensor("w2", w2, (E, H, F), bf, dev)
     if residual is not None:
         _tensor("residual", residual, (T, H), bf, dev)
-    out = torch.empty((T, H), dtype=bf, device=dev)
-    if T:
-        wsb = mx_moe_tokens_workspace_size(T, topk, E, F)
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-        with _on(dev):
+    with _on(dev, stream):
+        out = torch.empty((T, H), dtype=bf, device=dev)
+        if T:
+            wsb = mx_moe_tokens_workspace_size(T, topk, E, F)
+            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
             if mxw:
                 mx_moe_tokens(x, logits, T, topk, E, H, F, w1[0], w1[1], w2[0], w2[1], residual, out, ws, wsb, stream)
             else:
@@ -462,12 +467,12 @@ def bf16_linear(x, w, bias=None, residual=None, act=MX_ACT_NONE, out_dtype=MX_OU
         _tensor("bias", bias, (N,), torch.float32, dev)
     if residual is not None:
         _tensor("residual", residual, (M, N), bf, dev)
-    out = torch.empty((M, N), dtype=bf if out_dtype == MX_OUT_BF16 else torch.float32, device=dev)
-    z = torch.empty((M, N), dtype=bf, device=dev) if want_z else None
-    if M:
-        wsb = mx_bf16_linear_workspace_size(M, N, K)
-        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-        with _on(dev):
+    with _on(dev, stream):
+        out = torch.empty((M, N), dtype=bf if out_dtype == MX_OUT_BF16 else torch.float32, device=dev)
+        z = torch.empty((M, N), dtype=bf, device=dev) if want_z else None
+        if M:
+            wsb = mx_bf16_linear_workspace_size(M, N, K)
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
             mx_bf16_linear(x, w, bias, residual, M, N, K, act, z, out, out_dtype, ws, wsb, stream)
     return out, z
 
@@ -487,19 +492,19 @@ def bf16_linear_bwd(dout, x, w, z=None, act=MX_ACT_NONE, dx_add=None, want_dbias
         _tensor("z", z, (M, N), bf, dev)
     if dx_add is not None:
         _tensor("dx_add", dx_add, (M, K), bf, dev)
-    dx = torch.empty((M, K), dtype=bf, device=dev)
-    dw = torch.empty((N, K), dtype=bf, device=dev)
-    db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
-    if not M:   # empty tensors have no storage to pass
-        dw.zero_()
-        if db is not None:
-            db.zero_()
-        return dx, dw, db
-    wsb = mx_bf16_linear_bwd_workspace_size(M, N, K, act)
-    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        mx_bf16_linear_bwd(dout, MX_OUT_F32 if f32 else MX_OUT_BF16, z, x, w, dx_add, M, N, K, act, dx, dw, db, ws,
-                           wsb, stream)
+    with _on(dev, stream):
+        dx = torch.empty((M, K), dtype=bf, device=dev)
+        dw = torch.empty((N, K), dtype=bf, device=dev)
+        db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+        if M:
+            wsb = mx_bf16_linear_bwd_workspace_size(M, N, K, act)
+            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+            mx_bf16_linear_bwd(dout, MX_OUT_F32 if f32 else MX_OUT_BF16, z, x, w, dx_add, M, N, K, act, dx, dw, db, ws,
+                               wsb, stream)
+        else:   # empty tensors have no storage to pass
+            dw.zero_()
+            if db is not None:
+                db.zero_()
     return dx, dw, db
 
 

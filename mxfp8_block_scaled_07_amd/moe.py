@@ -21,7 +21,7 @@ combine backward writes); ``zero_pad_rows`` prepares such a tensor.
 
 import torch
 
-from . import (MX_ACT_NONE, MX_OUT_BF16, MX_OUT_F32, adamw_state, adamw_table, mx_adamw, mx_bf16_gather,
+from . import (MX_ACT_NONE, MX_OUT_BF16, MX_OUT_F32, _on, adamw_state, adamw_table, mx_adamw, mx_bf16_gather,
                mx_bf16_grouped_gemm_dgrad, mx_bf16_grouped_gemm_fwd, mx_bf16_grouped_gemm_wgrad, mx_bf16_linear,
                mx_bf16_linear_bwd, mx_bf16_linear_bwd_workspace_size, mx_bf16_linear_workspace_size,
                mx_bf16_moe_tokens, mx_combine, mx_combine_bwd_quantize, mx_grouped_gemm_dgrad, mx_grouped_gemm_fwd,
@@ -455,6 +455,8 @@ class Adamw:
         self.device = tensors[0][0].device
         if any(t is not None and t.device != self.device for row in tensors for t in row):
             raise ValueError("Adamw: the tensors are on one device")
+        if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.device != self.device):
+            raise ValueError("Adamw: grad_scale is an fp32 scalar on the tensors' device")
         self.param_dtype, self.grad_dtype = (kinds[t] for t in next(iter(types)))
         self.state_bits, self.betas, self.eps, self.weight_decay, self.seed = state_bits, betas, eps, weight_decay, seed
         self.lr = torch.full((1,), float(lr), device=self.device)
@@ -464,11 +466,12 @@ class Adamw:
         self.table = adamw_table([(p, g, *s, c) for (p, g, c), s in zip(tensors, self.states)])
 
     def step(self, stream=None):
-        """Count the step on torch's current stream, then update every tensor
-        on ``stream`` (by default the same one)."""
-        self.count.add_(1)
-        mx_adamw(self.table, len(self.table), self.param_dtype, self.grad_dtype, self.state_bits, self.lr, self.count,
-                 self.grad_scale, *self.betas, self.eps, self.weight_decay, self.seed, stream)
+        """Count the step and update every tensor on ``stream`` (by default
+        torch's current one)."""
+        with _on(self.device, stream):
+            self.count.add_(1)
+            mx_adamw(self.table, len(self.table), self.param_dtype, self.grad_dtype, self.state_bits, self.lr,
+                     self.count, self.grad_scale, *self.betas, self.eps, self.weight_decay, self.seed, stream)
 
 
 class TokenBuffers:

@@ -151,3 +151,27 @@ def test_helpers():
     assert mxa.bf16_linear(e, w)[0].shape == (0, 24)
     dx, dw, db = mxa.bf16_linear_bwd(dout[:0], e, w)
     assert dx.shape == (0, 64) and not dw.any() and not db.any()
+
+
+def test_helpers_on_another_stream():
+    """Workspaces are freed as the helpers return: what they allocate belongs to the call's stream, so that later
+    allocations of the current stream do not get them while the kernels still run."""
+    g = np.random.default_rng(3)
+    x = dev(workloads.normal_bf16(g, (300, 2048), 1.0)).view(torch.bfloat16)
+    w = dev(workloads.normal_bf16(g, (64, 2048), 0.1)).view(torch.bfloat16)
+    dout = dev(g.standard_normal((300, 64)).astype(np.float32))
+    want = [mxa.bf16_linear(x, w)[0], *mxa.bf16_linear_bwd(dout, x, w)]
+    p, grad = torch.ones(3000, device=x.device), torch.ones(3000, device=x.device)
+    opt = moe.Adamw([(p, grad, None)], lr=0.5, weight_decay=0.0)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [mxa.bf16_linear(x, w, stream=s.cuda_stream)[0], *mxa.bf16_linear_bwd(dout, x, w, stream=s.cuda_stream)]
+        junk = [torch.full((1 << 20,), float("nan"), device=x.device) for _ in range(8)]
+        opt.step(s.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+    # the gradient is constant, so each step moves by lr m / sqrt(v) = lr; the largest rounding in it is that of
+    # 1 - beta2 = 1e-3 from an fp32 beta2, 2^-25 / 1e-3 < 2^-15 relative, with a few of 2^-24 beside it
+    assert (p - (1 - 5 * 0.5)).abs().max() <= 5 * 0.5 * 2.0 ** -14 and int(opt.count) == 5

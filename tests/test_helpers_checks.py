@@ -53,3 +53,5 @@ def test_adamw():
         moe.Adamw([(p, g, p.clone())])
     with pytest.raises(ValueError):
         moe.Adamw([(p.double(), g, None)])
+    with pytest.raises(ValueError):
+        moe.Adamw([(p, g, None)], grad_scale=torch.ones(1, dtype=torch.float64))
