@@ -66,7 +66,9 @@ class Case:
 
 
 SIZES = [(40, 160, 96, 12, 3), (7, 96, 160, 9, 1), (1, 256, 192, 4, 2), (1, 64, 32, 1, 1), (5, 96, 64, 7, 3), (16, 160, 96, 16, 4), (17, 544, 160, 9, 3),
-         (33, 512, 288, 64, 8), (64, 224, 64, 3, 3), (64, 256, 640, 300, 5), (20, 64, 32, 1024, 64), (2, 2048, 1408, 8, 2)]
+         (33, 512, 288, 64, 8), (64, 224, 64, 3, 3), (64, 256, 640, 300, 5), (20, 64, 32, 1024, 64), (2, 2048, 1408, 8, 2),
+         # many tokens of one expert where few tiles of them fit the registers, rows longer than the registers hold
+         (50, 2560, 64, 3, 2), (37, 4128, 96, 2, 1), (21, 8480, 64, 3, 2), (3, 16672, 32, 4, 2)]
 
 
 @pytest.mark.parametrize("mxw", [True, False])
