@@ -916,9 +916,9 @@ constexpr struct {
 } kShape[kShapes] = {
     {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
     {128, 128, 2, 1.13, 4.9e6},
-    {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 94 with 64 x 64
+    {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 107 with 128 x 128
     {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
-    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18 us, against 24 with 128 x 64
+    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18.4 us, against 22 to 23 with the others
 
 // Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
 // tiles of the last, partly filled round are split over the contraction so

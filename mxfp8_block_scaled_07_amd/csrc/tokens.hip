@@ -22,6 +22,10 @@
 // kernel keeps its waves' share of the tokens in registers while it stays with
 // an expert, and the down kernel's waves share theirs through LDS.
 //
+// 64 experts of 2048 x 7168, top-8, MXFP8: one token 69 us (up 42, down 23, join
+// 4.5; 5.3 TB/s of weights), 33 tokens 430 us (6.7 TB/s); 61 tokens, 8 experts of
+// 1408 x 2048 in bf16 47 us.
+//
 // A is kept in bf16 (one rounding of w silu(G) U); everything else between the
 // bf16 inputs and outputs is fp32.  The weight goes into A so that the sum over
 // a token's experts is one fp32 sum.  All sums have a fixed order: the result
