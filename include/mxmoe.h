@@ -352,7 +352,8 @@ int mx_bf16_moe_tokens(const uint16_t* x, const float* logits, int64_t tokens, i
  * Tensors must not overlap each other; each is updated in place and nothing
  * past element n is touched.  Tensors with n == 0 are skipped.  All but the
  * scales 16-byte aligned; 0 <= beta < 1, eps >= 0.  `tensors` is host memory,
- * read before the call returns.  One launch per 48 tensors.
+ * read before the call returns.  One launch per 48 tensors; MX_EUNSUPPORTED
+ * where 48 in turn have 2^34 elements or more (nothing is updated then).
  */
 typedef struct {
   void* param;
@@ -383,8 +384,8 @@ int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t param_dtyp
  *   workspace >= mx_bf16_linear_workspace_size(rows, n, k) bytes (0: may be
  *            NULL); calls that overlap in time need their own
  * Any rows >= 0 and n >= 1 (n % 8 == 0 takes wide stores); k % 32 == 0; all
- * but the bias 16-byte aligned.  MX_EUNSUPPORTED for n or k >= 2^21 or
- * rows >= 2^31.  Repeated calls give the same bits.
+ * but the bias 16-byte aligned.  MX_EUNSUPPORTED for n or k >= 2^21,
+ * rows >= 2^31 or a launch of 2^32 threads (results above 100 GB).  Repeated calls give the same bits.
  */
 enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_GELU = 2, MX_ACT_GELU_TANH = 3, MX_ACT_SILU = 4 };
 

@@ -383,8 +383,10 @@ extern "C" int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return MX_EINVAL;
   if (!(eps >= 0.0 && eps <= 1e30) || !(weight_decay >= -1e30 && weight_decay <= 1e30)) return MX_EINVAL;
   if (((uintptr_t)lr | (uintptr_t)step | (uintptr_t)grad_scale) & 3) return MX_EINVAL;
-  int64_t total = 0;
+  bool any = false;
+  int64_t blocks = 0;   // of one launch
   for (int32_t i = 0; i < count; ++i) {
+    if (i % kBatch == 0) blocks = 0;
     const mx_adamw_tensor_t& t = tensors[i];
     if (t.n < 0) return MX_EINVAL;
     if (t.n == 0) continue;
@@ -393,10 +395,12 @@ extern "C" int mx_adamw(const mx_adamw_tensor_t* tensors, int32_t count, int32_t
     // 16-byte accesses
     if (((uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.m | (uintptr_t)t.v | (uintptr_t)t.copy) & 15)
       return MX_EINVAL;
-    if (t.n >= (1ll << 40) || total >= (1ll << 40)) return MX_EUNSUPPORTED;   // blocks below 2^31
-    total += t.n;
+    if (t.n >= (1ll << 40)) return MX_EUNSUPPORTED;
+    blocks += (t.n + kChunk - 1) / kChunk;
+    if (blocks * kAdamThreads >= (1ll << 32)) return MX_EUNSUPPORTED;   // threads of a launch
+    any = true;
   }
-  if (total == 0) return MX_OK;
+  if (!any) return MX_OK;
   Hyper hp;
   hp.lr = lr;
   hp.grad_scale = grad_scale;

@@ -958,6 +958,14 @@ Plan plan_product(int64_t I, int64_t J, int64_t C) {
   return best;
 }
 
+// Whether a product's launch stays below 2^32 threads (the split tiles' parts are at most 2 kCus workgroups).
+bool grid_fits(int64_t I, int64_t J, int64_t C, bool a_rows) {
+  if (a_rows && C <= 64) return true;   // k_short
+  const int shape = plan_product(I, J, C).shape;
+  const int64_t tiles = (I + kShape[shape].bm - 1) / kShape[shape].bm * ((J + kShape[shape].bn - 1) / kShape[shape].bn);
+  return (tiles + 4 * kCus) * (shape == k256x256 ? 512 : 256) < (1ll << 32);
+}
+
 template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, int kAct, int kOnce = kOnceNone>
 void launch_shape(const Product& p, hipStream_t st) {
   auto up8 = [](int32_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
@@ -1003,7 +1011,6 @@ int launch_product(const Operand& a, const Operand& b, int64_t I, int64_t J, int
   const Plan pl = plan_product(I, J, C);
   const auto& sh = kShape[pl.shape];
   const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn;
-  if (ti * tj >= (1ll << 28)) return MX_EUNSUPPORTED;
   p.tiles_i = (int32_t)ti;
   p.tiles_j = (int32_t)tj;
   p.full = pl.full;
@@ -1074,6 +1081,7 @@ extern "C" int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float*
   if (((uintptr_t)bias & 3) || misaligned(workspace)) return MX_EINVAL;
   if (too_large(rows, n, k)) return MX_EUNSUPPORTED;
   if (rows == 0) return MX_OK;
+  if (!few_rows(rows, k) && !grid_fits(rows, n, k, true)) return MX_EUNSUPPORTED;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   Epi epi;
   epi.bias = bias;
@@ -1120,6 +1128,7 @@ extern "C" int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const ui
       misaligned(dw) || ((uintptr_t)dbias & 3) || misaligned(workspace))
     return MX_EINVAL;
   if (too_large(rows, n, k)) return MX_EUNSUPPORTED;
+  if ((dx && !grid_fits(rows, k, n, true)) || (dw && !grid_fits(n, k, rows, false))) return MX_EUNSUPPORTED;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const BwdSpace s = bwd_space(rows, n, k);
   if (rows > 0 && (!workspace || (int64_t)workspace_bytes < s.dz + s.sums + s.part)) return MX_EINVAL;

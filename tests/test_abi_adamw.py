@@ -33,6 +33,15 @@ def test_nothing_to_do_and_too_much(lib):  # noqa: F811
     assert call(lib, n=1 << 41) == mxa.MX_EUNSUPPORTED
 
 
+def test_one_launch_holds_its_threads(lib):  # noqa: F811
+    """48 tensors in turn with 2^34 elements or more are refused before the first of them is updated."""
+    assert call(lib, n=1 << 34) == mxa.MX_EUNSUPPORTED
+    row = mxa.AdamwTensor(param=16, grad=16, m=16, v=16, n=1 << 33)
+    rows = [mxa.AdamwTensor(param=16, grad=16, m=16, v=16, n=0)] * 48 + [row, row]
+    table = (mxa.AdamwTensor * 50)(*rows)
+    assert lib.mx_adamw(table, 50, 1, 1, 32, P, P, None, 0.9, 0.9, 0.0, 0.0, 0, None) == mxa.MX_EUNSUPPORTED
+
+
 def test_table():
     p = torch.zeros(40)
     t = mxa.adamw_table([(p, p.clone(), p.clone(), p.clone(), torch.zeros(2, dtype=torch.uint8), None, None)])

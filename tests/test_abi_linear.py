@@ -45,3 +45,8 @@ def test_sizes(lib):  # noqa: F811
     assert fwd(lib, k=8192, wsb=need - 1) == mxa.MX_EINVAL and fwd(lib, k=8192, ws=None) == mxa.MX_EINVAL
     b = lib.mx_bf16_linear_bwd_workspace_size
     assert b(100, 64, 64, 1) >= 100 * 64 * 2 and b(0, 64, 64, 1) == 0 and b(100, 64, 64, 9) == 0
+
+
+def test_a_launch_holds_its_threads(lib):  # noqa: F811
+    assert fwd(lib, M=1 << 30, n=1 << 20, k=128) == mxa.MX_EUNSUPPORTED
+    assert bwd(lib, M=1 << 30, n=1 << 10, k=1 << 16) == mxa.MX_EUNSUPPORTED
