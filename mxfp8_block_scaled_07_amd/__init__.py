@@ -412,11 +412,8 @@ def _tensor(name, t, shape, dtype, device=None):
 def _on(device, stream):
     """The tensors' device as the current one, and the call's stream as its current stream: what a helper allocates
     inside belongs to that stream, so the memory is not handed out again before the call's kernels have run."""
-    import contextlib
-
     import torch
-    if device.type != "cuda":
-        return contextlib.nullcontext()
+    _need(device.type == "cuda", f"tensors are on {device}, not on a GPU")
     if stream is None:
         return torch.cuda.device(device)
     return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))

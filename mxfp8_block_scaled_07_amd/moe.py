@@ -455,6 +455,8 @@ class Adamw:
         self.device = tensors[0][0].device
         if any(t is not None and t.device != self.device for row in tensors for t in row):
             raise ValueError("Adamw: the tensors are on one device")
+        if self.device.type != "cuda":
+            raise ValueError(f"Adamw: the tensors are on {self.device}, not on a GPU")
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.device != self.device):
             raise ValueError("Adamw: grad_scale is an fp32 scalar on the tensors' device")
         self.param_dtype, self.grad_dtype = (kinds[t] for t in next(iter(types)))

@@ -55,3 +55,11 @@ def test_adamw():
         moe.Adamw([(p.double(), g, None)])
     with pytest.raises(ValueError):
         moe.Adamw([(p, g, None)], grad_scale=torch.ones(1, dtype=torch.float64))
+
+
+def test_host_tensors_are_refused():
+    x, w, d, p = torch.zeros(5, 64, dtype=bf), torch.zeros(8, 64, dtype=bf), torch.zeros(5, 8), torch.zeros(40)
+    for call in (tokens, lambda: mxa.bf16_linear(x, w), lambda: mxa.bf16_linear_bwd(d, x, w),
+                 lambda: moe.Adamw([(p, p.clone(), None)])):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
