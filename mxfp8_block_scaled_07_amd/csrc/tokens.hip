@@ -97,10 +97,12 @@ __device__ __forceinline__ float wave_add_f(float v) {
   return last_lane(v);
 }
 
-// Order-preserving integer key of a float (-0 as +0).
+// Order-preserving integer key of a float (-0 as +0).  A NaN of either sign has
+// the largest, so that it is always chosen and its token's row becomes NaN: by
+// its bits a negative one would sort below -inf and be dropped.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return v != v ? 0xFFFFFFFFu : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -111,8 +113,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // from the top (the count of keys at or above a candidate is a ballot and a
 // popcount; the search ends when a count is exactly k), ties at it go to the
 // lowest ids.  Then the softmax statistics of the chosen.  kGroups: groups of
-// 64 experts, one key of each per lane; key 0 where there is no expert (also
-// the key of one NaN, which is then never chosen).
+// 64 experts, one key of each per lane; key 0, which no logit has, where there
+// is no expert.
 template <int kGroups>
 __device__ __forceinline__ void route_token(Routing& rt, const uint32_t (&key)[kGroups], int t, int k) {
   const int lane = threadIdx.x & 63;

@@ -163,3 +163,26 @@ def test_two_captured_graphs_replay_as_eager():
         torch.cuda.synchronize()
         for c, w in zip(cs, want):
             assert np.array_equal(host(c.out[:c.T]), w)
+
+
+@pytest.mark.parametrize("mxw", [True, False])
+@pytest.mark.parametrize("E", [6, 70, 300])
+def test_nan_logits_of_either_sign(E, mxw):
+    """A NaN makes its token's row NaN whatever its sign and payload, beside enough other logits, masked ones, +inf and
+    more NaNs than topk."""
+    c = Case(20, 96, 64, E, 2, mxw, residual=True)
+    bits = c.logits.view(np.uint32)
+    bad = []
+    for i, nan in enumerate((0xFFC00000, 0xFFFFFFFF, 0x7FC00000, 0x7FFFFFFF, 0xFF800001, 0x7F800001)):
+        bits[2 * i, E - 1 - i % 3] = nan
+        bad.append(2 * i)
+    c.logits[13, :] = -np.inf
+    bits[13, 1] = 0xFFC00000
+    c.logits[15, 0] = np.inf
+    bits[15, 2] = 0xFFFFFFFF
+    bits[17, :] = 0xFFC00000
+    bad += [13, 15, 17]
+    got = c.run()
+    assert np.isnan(mx.bf16_to_f64(got[bad])).all()
+    c.logits[bad] = 0.0
+    c.check(got, [t for t in range(20) if t not in bad])
