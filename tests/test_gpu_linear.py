@@ -1,6 +1,8 @@
 """GPU parity: the dense product with its epilogue, and its backward, against
 the fp64 oracle (oracle/linear.py), whose bounds count the roundings."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -276,3 +278,65 @@ def test_captured_replays_on_another_stream(size):
             a = host(getattr(c, n))
             k = -1 if n == "db" else slice(None, -1)
             assert np.array_equal(a[:-1], want[n][:-1]), (n, k)
+
+
+TAILS = workloads.f32_to_bf16_bits(np.concatenate([np.linspace(-40, 40, 6001), -np.logspace(-30, 30, 183),
+                                                   np.logspace(-30, 30, 184)]).astype(np.float32))
+
+
+def tail_terms(v, act):
+    """(act, its error in units of 2^-24 of itself, the terms of its slope added up, their error, the slope) in fp64.
+
+    gelu: its exponential of -v^2 / 2 is off by 1.5 v^2 units and its own 2, the factor that makes it the tail by 6,
+    the products by a few.  The sigmoids' 2^x: the product of its argument t is off by 2 |t|, the functions by a few
+    units; gelu_tanh's t itself by 7 |t|, in each of its factors.  Past |t| = 200 (v^2 = 400) all of them are 0 or 1."""
+    a, erfc = np.abs(v), np.vectorize(math.erfc, otypes=[np.float64])
+    if act == "gelu":
+        cdf, pdf = 0.5 * erfc(-v / math.sqrt(2)), np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+        k = 16 + 2 * np.minimum(v * v, 400)
+        return v * cdf, k, cdf + a * pdf, k, cdf + v * pdf
+    if act in ("silu", "gelu_tanh"):
+        c = 2 * math.sqrt(2 / math.pi)
+        t, dt = (v, np.ones_like(v)) if act == "silu" else (c * (v + 0.044715 * v ** 3), c * (1 + 3 * 0.044715 * v * v))
+        s, m = 1 / (1 + np.exp(-t)), 1 / (1 + np.exp(t))
+        b = np.minimum(np.abs(t), 200)
+        k = (16 + 4 * b, 24 + 4 * b) if act == "silu" else (16 + 10 * b, 32 + 20 * b)
+        with np.errstate(invalid="ignore"):
+            p = np.where(s * m == 0, 0, v * s * m * dt)
+        return v * s, k[0], s + np.abs(p), k[1], s + p
+    one = np.ones_like(v) if act == "none" else (v > 0).astype(np.float64)
+    return v * one, 0 * v, one, 0 * v, one
+
+
+@pytest.mark.parametrize("act", ol.ACTS)
+def test_activations_and_slopes_relative_to_their_value(act):
+    """Far into the tails, where the value is far below its argument, an fp32 result still has most of its bits; what
+    the hardware's 2^x flushes (below 2^-126) is all that may be lost beside that."""
+    v = mx.bf16_to_f64(TAILS)
+    n = v.size // 8 * 8
+    v = v[:n]
+    with np.errstate(over="ignore"):
+        want, units, terms, slope_units, slope = tail_terms(v, act)
+    least = 2.0 ** -125 * (1 + np.minimum(np.abs(v), 200)) ** 3
+    x, w = np.zeros((n, 32), np.uint16), np.zeros((8, 32), np.uint16)
+    x[:, 0], w[0, 0] = TAILS[:n], 0x3F80
+    out = torch.empty((n, 8), device=DEV)
+    wsb = mxa.mx_bf16_linear_workspace_size(n, 8, 32)
+    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=DEV)
+    mxa.mx_bf16_linear(dev(x), dev(w), None, None, n, 8, 32, ol.ACTS.index(act), None, out, F32, ws, wsb)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore"):
+        err, bound = np.abs(host(out)[:, 0] - want), units * 2.0 ** -24 * np.abs(want) + least
+    assert (err <= bound).all(), [(v[i], want[i], host(out)[i, 0]) for i in np.flatnonzero(~(err <= bound))[:5]]
+    if act == "none":
+        return
+    # a row of n columns: dbias is the slope of each
+    z, db = dev(TAILS[None, :n]), torch.empty(n, device=DEV)
+    wsb = mxa.mx_bf16_linear_bwd_workspace_size(1, n, 32, ol.ACTS.index(act))
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    mxa.mx_bf16_linear_bwd(torch.ones((1, n), device=DEV), F32, z, None, None, None, 1, n, 32, ol.ACTS.index(act), None,
+                           None, db, ws, wsb)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore", invalid="ignore"):
+        err, bound = np.abs(host(db) - slope), np.where(terms == 0, 0, slope_units * 2.0 ** -24 * terms) + least
+    assert (err <= bound).all(), [(v[i], slope[i], host(db)[i]) for i in np.flatnonzero(~(err <= bound))[:5]]
