@@ -511,7 +511,8 @@ def adamw_state(param, state_bits=32):
     _need(state_bits in (8, 32), "adamw_state: state_bits is 8 or 32")
     n, dev = param.numel(), param.device
     if state_bits == 32:
-        return torch.zeros(n, device=dev), torch.zeros(n, device=dev), None, None
+        z = lambda k: torch.zeros(k, dtype=torch.float32, device=dev)  # noqa: E731
+        return z(n), z(n), None, None
     z = lambda k: torch.zeros(k, dtype=torch.uint8, device=dev)  # noqa: E731
     return z(n), z(n), z(-(-n // 32)), z(-(-n // 32))
 

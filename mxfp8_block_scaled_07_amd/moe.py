@@ -461,7 +461,7 @@ class Adamw:
             raise ValueError("Adamw: grad_scale is an fp32 scalar on the tensors' device")
         self.param_dtype, self.grad_dtype = (kinds[t] for t in next(iter(types)))
         self.state_bits, self.betas, self.eps, self.weight_decay, self.seed = state_bits, betas, eps, weight_decay, seed
-        self.lr = torch.full((1,), float(lr), device=self.device)
+        self.lr = torch.full((1,), float(lr), dtype=torch.float32, device=self.device)
         self.count = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.grad_scale = grad_scale
         self.states = [adamw_state(p, state_bits) for p, _, _ in tensors]

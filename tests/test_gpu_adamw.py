@@ -276,3 +276,19 @@ def test_captured_step_follows_step_and_lr():
         for k in ref[r]:
             assert np.array_equal(got[k], ref[r][k]), (r, k)
         one(b)                                          # eager work between the replays
+
+
+def test_the_class_under_another_default_type():
+    """Its states and its lr are fp32 whatever torch makes by default."""
+    p, g = (torch.linspace(-1, 1, 1000, dtype=torch.float32, device=DEV) for _ in range(2))
+    want = p.clone()
+    moe.Adamw([(want, g, None)], lr=0.25).step()
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        opt = moe.Adamw([(p, g, None)], lr=0.25)
+        assert opt.lr.dtype == torch.float32 and all(t.dtype == torch.float32 for t in opt.states[0][:2])
+        opt.step()
+    finally:
+        torch.set_default_dtype(torch.float32)
+    torch.cuda.synchronize()
+    assert torch.equal(p, want)

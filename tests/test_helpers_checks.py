@@ -63,3 +63,14 @@ def test_host_tensors_are_refused():
                  lambda: moe.Adamw([(p, p.clone(), None)])):
         with pytest.raises(ValueError, match="not on a GPU"):
             call()
+
+
+@pytest.mark.parametrize("other", [torch.bfloat16, torch.float64])
+def test_adamw_state_is_fp32_under_another_default_type(other):
+    """The kernel reads and writes 4 bytes an element of these states."""
+    torch.set_default_dtype(other)
+    try:
+        m, v, _, _ = mxa.adamw_state(torch.zeros(40, dtype=torch.float32), 32)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert m.dtype == v.dtype == torch.float32 and m.numel() == v.numel() == 40
