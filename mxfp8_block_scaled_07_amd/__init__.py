@@ -233,7 +233,9 @@ def mx_bf16_linear_bwd(dout, dout_dtype, z, x, w, dx_add, rows, n, k, act, dx, d
 
 def mx_adamw(tensors, count, param_dtype, grad_dtype, state_bits, lr, step, grad_scale, beta1, beta2, eps,
              weight_decay, seed, stream=None):
-    """tensors: an array of AdamwTensor (see adamw_table)."""
+    """tensors: an array of AdamwTensor; one from adamw_table is checked against the other arguments."""
+    if hasattr(tensors, "kinds"):
+        _adamw_fits(tensors, count, (param_dtype, grad_dtype, state_bits), lr, step, grad_scale)
     _check(lib().mx_adamw(tensors, count, param_dtype, grad_dtype, state_bits, _p(lr), _p(step), _p(grad_scale),
                           beta1, beta2, eps, weight_decay, seed, _s(stream)), "mx_adamw")
 
@@ -519,8 +521,13 @@ def adamw_state(param, state_bits=32):
 
 def adamw_table(rows):
     """The host table mx_adamw takes, from (param, grad, m, v, m_scale, v_scale, copy) per tensor (contiguous device
-    tensors; None for what is not there).  It keeps its tensors alive and can be used for every step."""
+    tensors of the types the header names, the same in every row; None for what is not there).  It keeps its tensors
+    alive and can be used for every step; mx_adamw refuses arguments that do not fit what it holds."""
+    import torch
+    kinds = {torch.float32: MX_OUT_F32, torch.bfloat16: MX_OUT_BF16, torch.int16: MX_OUT_BF16}
+    bytes_ = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
     table = (AdamwTensor * len(rows))()
+    table.device = table.kinds = None
     for t, row in zip(table, rows):
         param, grad, m, v, m_scale, v_scale, copy = row
         n = param.numel()
@@ -530,8 +537,36 @@ def adamw_table(rows):
         for x, want in ((grad, n), (m, n), (v, n), (copy, n), (m_scale, -(-n // 32)), (v_scale, -(-n // 32))):
             if x is not None and x.numel() != want:
                 raise ValueError(f"adamw_table: {x.numel()} elements where {want} belong to a parameter of {n}")
+        for x in row:
+            _need(x is None or x.device == param.device, "adamw_table: a row's tensors are on one device")
+        _need(param.dtype in kinds and grad.dtype in kinds, "adamw_table: parameters and gradients are fp32 or bf16")
+        _need(copy is None or kinds.get(copy.dtype) == MX_OUT_BF16, "adamw_table: copies are bf16")
+        bits = 32 if m.dtype == torch.float32 else 8
+        if bits == 32:
+            _need(v.dtype == torch.float32, "adamw_table: m and v are both fp32 or both codes")
+        else:
+            _need(m.dtype in bytes_ and v.dtype in bytes_, "adamw_table: m and v are both fp32 or both codes (one byte)")
+            _need(all(x is not None and x.dtype in bytes_ for x in (m_scale, v_scale)),
+                  "adamw_table: codes have scales of one byte")
+        found = kinds[param.dtype], kinds[grad.dtype], bits
+        _need(table.kinds in (None, found) and table.device in (None, param.device),
+              "adamw_table: types and device are the same in every row")
+        table.kinds, table.device = found, param.device
         t.param, t.grad, t.m, t.v = (x.data_ptr() for x in (param, grad, m, v))
         t.m_scale, t.v_scale, t.copy = (None if x is None else x.data_ptr() for x in (m_scale, v_scale, copy))
         t.n = n
     table.tensors = rows
     return table
+
+
+def _adamw_fits(table, count, kinds, lr, step, grad_scale):
+    """The arguments of mx_adamw are those of a table that adamw_table made."""
+    import torch
+    _need(count <= len(table), f"mx_adamw: {count} tensors of a table of {len(table)}")
+    if table.kinds is None:
+        return
+    _need(kinds == table.kinds, "mx_adamw: the table's tensors are of other types (param_dtype, grad_dtype, state_bits)")
+    for name, t, dtype in (("lr", lr, torch.float32), ("step", step, torch.int32), ("grad_scale", grad_scale, torch.float32)):
+        _need(t is None or (t.dtype == dtype and t.numel() >= 1 and t.device == table.device),
+              f"mx_adamw: {name} is a {dtype} scalar on the tensors' device")
+    _need(table.device.type == "cuda", f"mx_adamw: tensors are on {table.device}, not on a GPU")

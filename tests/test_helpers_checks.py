@@ -74,3 +74,48 @@ def test_adamw_state_is_fp32_under_another_default_type(other):
     finally:
         torch.set_default_dtype(torch.float32)
     assert m.dtype == v.dtype == torch.float32 and m.numel() == v.numel() == 40
+
+
+def adam_row(n=40, bits=8, pd=torch.float32, gd=bf, copy=True):
+    m, v, ms, vs = mxa.adamw_state(torch.zeros(n), bits)
+    return [torch.zeros(n, dtype=pd), torch.zeros(n, dtype=gd), m, v, ms, vs, torch.zeros(n, dtype=bf) if copy else None]
+
+
+@pytest.mark.parametrize("at,bad", [(0, torch.zeros(40, dtype=torch.float64)), (0, torch.zeros(40, dtype=torch.float16)),
+                                    (1, torch.zeros(40, dtype=u8)), (2, torch.zeros(40)), (3, torch.zeros(40)),
+                                    (2, torch.zeros(40, dtype=bf)), (4, None), (5, None), (4, torch.zeros(2)),
+                                    (5, torch.zeros(2, dtype=bf)), (6, torch.zeros(40)),
+                                    (1, torch.zeros(40, dtype=bf, device="meta"))])
+def test_adamw_table_refuses_types_and_devices(at, bad):
+    row = adam_row()
+    mxa.adamw_table([row])
+    row[at] = bad
+    with pytest.raises(ValueError, match="adamw_table"):
+        mxa.adamw_table([row])
+
+
+@pytest.mark.parametrize("other", [dict(bits=32), dict(pd=bf), dict(gd=torch.float32)])
+def test_adamw_table_takes_rows_of_one_kind(other):
+    mxa.adamw_table([adam_row(), adam_row(n=0, copy=False)])
+    with pytest.raises(ValueError, match="adamw_table"):
+        mxa.adamw_table([adam_row(), adam_row(**other)])
+
+
+def adam_call(table, count=1, pd=mxa.MX_OUT_F32, gd=mxa.MX_OUT_BF16, bits=8, lr=torch.zeros(1),
+              step=torch.zeros(1, dtype=torch.int32), scale=None):
+    mxa.mx_adamw(table, count, pd, gd, bits, lr, step, scale, 0.9, 0.999, 1e-8, 0.0, 0, 0)
+
+
+@pytest.mark.parametrize("bad", [dict(pd=mxa.MX_OUT_BF16), dict(gd=mxa.MX_OUT_F32), dict(bits=32), dict(count=2),
+                                 dict(lr=torch.zeros(1, dtype=torch.float64)), dict(lr=torch.zeros(0)),
+                                 dict(step=torch.zeros(1)), dict(scale=torch.zeros(1, dtype=bf)),
+                                 dict(lr=torch.zeros(1, device="meta"))])
+def test_mx_adamw_refuses_what_its_table_does_not_hold(bad):
+    table = mxa.adamw_table([adam_row()])
+    with pytest.raises(ValueError, match="mx_adamw"):
+        adam_call(table, **bad)
+
+
+def test_mx_adamw_refuses_a_table_of_host_tensors():
+    with pytest.raises(ValueError, match="not on a GPU"):
+        adam_call(mxa.adamw_table([adam_row()]))
