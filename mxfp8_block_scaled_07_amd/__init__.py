@@ -528,6 +528,7 @@ def adamw_table(rows):
     bytes_ = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
     table = (AdamwTensor * len(rows))()
     table.device = table.kinds = None
+    ranges = []   # of each tensor: its addresses, and whether it is written
     for t, row in zip(table, rows):
         param, grad, m, v, m_scale, v_scale, copy = row
         n = param.numel()
@@ -555,6 +556,15 @@ def adamw_table(rows):
         t.param, t.grad, t.m, t.v = (x.data_ptr() for x in (param, grad, m, v))
         t.m_scale, t.v_scale, t.copy = (None if x is None else x.data_ptr() for x in (m_scale, v_scale, copy))
         t.n = n
+        used = [(grad, False)] + [(x, True) for x in (param, m, v, m_scale, v_scale)]
+        if copy is not None and not (copy.dtype == param.dtype and copy.data_ptr() == param.data_ptr()):
+            used.append((copy, True))   # (over a bf16 parameter it writes the same values)
+        ranges += [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), w) for x, w in used
+                   if x is not None and x.numel()]
+    end = end_written = 0
+    for a, b, w in sorted(ranges):
+        _need(a >= (end if w else end_written), "adamw_table: tensors that are written overlap")
+        end, end_written = max(end, b), max(end_written, b if w else 0)
     table.tensors = rows
     return table
 

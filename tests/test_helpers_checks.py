@@ -119,3 +119,22 @@ def test_mx_adamw_refuses_what_its_table_does_not_hold(bad):
 def test_mx_adamw_refuses_a_table_of_host_tensors():
     with pytest.raises(ValueError, match="not on a GPU"):
         adam_call(mxa.adamw_table([adam_row()]))
+
+
+def test_adamw_table_refuses_tensors_written_twice():
+    """Two blocks would update the same element, in either order."""
+    a, b = adam_row(), adam_row()
+    mxa.adamw_table([a, b[:1] + a[1:2] + b[2:]])              # a gradient may be shared: it is only read
+    flat = torch.zeros(80)
+    for i in (0, 2, 3, 4, 5, 6):
+        with pytest.raises(ValueError, match="overlap"):
+            mxa.adamw_table([a, b[:i] + a[i:i + 1] + b[i + 1:]])
+    with pytest.raises(ValueError, match="overlap"):          # partly
+        mxa.adamw_table([[flat[:40]] + a[1:], [flat[39:79]] + b[1:]])
+    with pytest.raises(ValueError, match="overlap"):          # the gradient is written too
+        mxa.adamw_table([a[:1] + [a[6]] + a[2:]])
+    with pytest.raises(ValueError, match="overlap"):          # a copy over its fp32 parameter
+        mxa.adamw_table([[flat[:40]] + a[1:6] + [flat.view(bf)[:40]]])
+    mxa.adamw_table([[flat[:40]] + a[1:], [flat[40:]] + b[1:]])
+    p = torch.zeros(40, dtype=bf)                             # a bf16 parameter's copy has its value
+    mxa.adamw_table([[p] + a[1:6] + [p]])
