@@ -542,6 +542,8 @@ def adamw_table(rows):
             _need(x is None or x.device == param.device, "adamw_table: a row's tensors are on one device")
         _need(param.dtype in kinds and grad.dtype in kinds, "adamw_table: parameters and gradients are fp32 or bf16")
         _need(copy is None or kinds.get(copy.dtype) == MX_OUT_BF16, "adamw_table: copies are bf16")
+        _need(not any(x is not None and x.numel() and x.data_ptr() % 16 for x in (param, grad, m, v, copy)),
+              "adamw_table: tensors (but the scales) are 16-byte aligned")
         bits = 32 if m.dtype == torch.float32 else 8
         if bits == 32:
             _need(v.dtype == torch.float32, "adamw_table: m and v are both fp32 or both codes")

@@ -469,11 +469,15 @@ class Adamw:
 
     def step(self, stream=None):
         """Count the step and update every tensor on ``stream`` (by default
-        torch's current one)."""
+        torch's current one).  A refused step is not counted."""
         with _on(self.device, stream):
             self.count.add_(1)
-            mx_adamw(self.table, len(self.table), self.param_dtype, self.grad_dtype, self.state_bits, self.lr,
-                     self.count, self.grad_scale, *self.betas, self.eps, self.weight_decay, self.seed, stream)
+            try:
+                mx_adamw(self.table, len(self.table), self.param_dtype, self.grad_dtype, self.state_bits, self.lr,
+                         self.count, self.grad_scale, *self.betas, self.eps, self.weight_decay, self.seed, stream)
+            except Exception:
+                self.count.sub_(1)
+                raise
 
 
 class TokenBuffers:

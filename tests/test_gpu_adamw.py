@@ -292,3 +292,14 @@ def test_the_class_under_another_default_type():
         torch.set_default_dtype(torch.float32)
     torch.cuda.synchronize()
     assert torch.equal(p, want)
+
+
+def test_a_refused_step_is_not_counted():
+    p = torch.ones(64, device=DEV)
+    opt = moe.Adamw([(p, torch.ones(64, device=DEV), None)])
+    opt.step()
+    opt.betas = (0.9, 1.5)
+    with pytest.raises(mxa.MXError):
+        opt.step()
+    torch.cuda.synchronize()
+    assert int(opt.count) == 1

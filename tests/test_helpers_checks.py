@@ -130,7 +130,7 @@ def test_adamw_table_refuses_tensors_written_twice():
         with pytest.raises(ValueError, match="overlap"):
             mxa.adamw_table([a, b[:i] + a[i:i + 1] + b[i + 1:]])
     with pytest.raises(ValueError, match="overlap"):          # partly
-        mxa.adamw_table([[flat[:40]] + a[1:], [flat[39:79]] + b[1:]])
+        mxa.adamw_table([[flat[:40]] + a[1:], [flat[32:72]] + b[1:]])
     with pytest.raises(ValueError, match="overlap"):          # the gradient is written too
         mxa.adamw_table([a[:1] + [a[6]] + a[2:]])
     with pytest.raises(ValueError, match="overlap"):          # a copy over its fp32 parameter
@@ -138,3 +138,14 @@ def test_adamw_table_refuses_tensors_written_twice():
     mxa.adamw_table([[flat[:40]] + a[1:], [flat[40:]] + b[1:]])
     p = torch.zeros(40, dtype=bf)                             # a bf16 parameter's copy has its value
     mxa.adamw_table([[p] + a[1:6] + [p]])
+
+
+@pytest.mark.parametrize("at", [0, 1, 2, 3, 6])
+def test_adamw_table_refuses_misaligned_tensors(at):
+    """When the table is built, not at each step."""
+    row, old = adam_row(), adam_row(n=80)[at]
+    row[at] = old[1:41]
+    with pytest.raises(ValueError, match="16-byte aligned"):
+        mxa.adamw_table([row])
+    row[at] = old[32:72]
+    mxa.adamw_table([row])
