@@ -312,8 +312,9 @@ int mx_router_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, int64
  * and a token's row not on the other tokens beyond the order of its fp32 sums.
  * Requires H % 32 == 0, F % 32 == 0, 1 <= topk <= num_experts; x, w1, w2 and
  * the workspace 16-byte, out and residual 4-byte aligned.  MX_EUNSUPPORTED
- * (and a workspace size of 0) above 64 tokens, 1024 experts or top-64, and for
- * one expert's matrix or the scales of 2^31 bytes or more.
+ * above 64 tokens, 1024 experts or top-64, and where one expert's matrix, the
+ * scales, x or the bf16 pairs [tokens topk, F] have 2^31 bytes or more.  The
+ * workspace size is 0 for arguments of its own that the call refuses.
  */
 size_t mx_moe_tokens_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t F);
 

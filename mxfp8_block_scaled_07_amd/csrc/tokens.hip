@@ -820,8 +820,9 @@ int tokens_call(bool mxw, const uint16_t* x, const float* logits, int64_t tokens
 using namespace mx;
 
 extern "C" size_t mx_moe_tokens_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t F) {
-  if (tokens < 0 || topk < 1 || num_experts < 1 || F <= 0) return 0;
-  if (tokens > kMaxTokens || topk > kTokTopk || F >= (1ll << 24)) return 0;
+  if (tokens < 0 || topk < 1 || topk > num_experts || F <= 0) return 0;
+  if (tokens > kMaxTokens || num_experts > kTokExperts || topk > kTokTopk || F >= (1ll << 24)) return 0;
+  if (tokens * topk * F * 2 >= (1ll << 31)) return 0;
   return (size_t)tokens_bytes(tokens, topk, F);
 }
 
