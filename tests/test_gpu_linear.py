@@ -340,3 +340,21 @@ def test_activations_and_slopes_relative_to_their_value(act):
     with np.errstate(over="ignore", invalid="ignore"):
         err, bound = np.abs(host(db) - slope), np.where(terms == 0, 0, slope_units * 2.0 ** -24 * terms) + least
     assert (err <= bound).all(), [(v[i], slope[i], host(db)[i]) for i in np.flatnonzero(~(err <= bound))[:5]]
+
+
+@pytest.mark.parametrize("size", [(9, 96, 512), (40, 96, 256), (200, 130, 512), (300, 520, 64)])
+def test_infinite_rows_are_not_finite(size):
+    """x = inf gives z = +-inf in every column: silu(inf) = inf, silu(-inf) = NaN; a NaN row is NaN; the others stay."""
+    M, N, K = size
+    c = Case(M, N, K, act="silu", residual=False)
+    c.x[7, 3], c.x[5, K - 1] = 0x7FC0, 0x7F80
+    c.d["x"] = dev(c.x)
+    c.fwd()
+    torch.cuda.synchronize()
+    got = val(host(c.out[:M]))
+    assert np.isnan(got[7]).all()
+    assert not np.isfinite(got[5]).any()
+    c.x[7, 3] = c.x[5, K - 1] = 0
+    y, yb, _, _ = ol.forward(val(c.x), val(c.w), c.bias, None, "silu", False)
+    keep = np.delete(np.arange(M), [5, 7])
+    assert (np.abs(got - y)[keep] <= yb[keep]).all()

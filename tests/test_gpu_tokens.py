@@ -186,3 +186,14 @@ def test_nan_logits_of_either_sign(E, mxw):
     assert np.isnan(mx.bf16_to_f64(got[bad])).all()
     c.logits[bad] = 0.0
     c.check(got, [t for t in range(20) if t not in bad])
+
+
+@pytest.mark.parametrize("mxw", [True, False])
+def test_an_infinite_token_is_not_finite(mxw):
+    """g is +-inf in every row of W1: silu(-inf) = -inf / inf is NaN, and NaN times any weight."""
+    c = Case(40, 96, 64, 6, 2, mxw, residual=True)
+    c.x[21, 95] = 0x7F80
+    got = c.run()
+    assert not np.isfinite(mx.bf16_to_f64(got[21])).any()
+    c.x[21, 95] = 0
+    c.check(got, [t for t in range(40) if t != 21])
