@@ -407,7 +407,9 @@ int mx_bf16_linear(const uint16_t* x, const uint16_t* w, const float* bias, cons
  * dz is rounded to bf16 once for the two products (the matrix instruction's
  * operand); dbias sums the unrounded dz.  fp32 sums; repeated calls give the
  * same bits.  rows == 0 gives zero dw and dbias.  Sizes and alignment as in
- * the forward; workspace >= mx_bf16_linear_bwd_workspace_size(...) bytes.
+ * the forward; workspace >= mx_bf16_linear_bwd_workspace_size(...) bytes (the
+ * size for a dout of either type: it holds 2 rows n bytes of dz also where a
+ * bf16 dout serves as dz itself).
  */
 size_t mx_bf16_linear_bwd_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t act);
 

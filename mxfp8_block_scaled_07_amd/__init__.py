@@ -4,7 +4,8 @@ Python binding of ``libmxmoe.so`` (declared in ``include/mxmoe.h``).  The
 functions named ``mx_*`` mirror the C entry points one to one and only
 marshal arguments: torch tensors stand for device buffers (their data
 pointers are passed), ``None`` stands for NULL, and the stream defaults to
-torch's current stream.  The ``alloc_*``/convenience helpers only allocate
+torch's current stream (``mx_adamw`` also refuses what does not fit a table
+that ``adamw_table`` made).  The ``alloc_*``/convenience helpers only allocate
 output tensors with torch and then call the same entry points.  Every
 computation runs in the HIP kernels; there is no fallback: if the library is
 missing or a call fails, an exception is raised.

@@ -11,8 +11,8 @@
 // arguments, so the call needs no table in device memory and can be captured.
 // A block takes 1024 elements of one tensor, a thread 4 consecutive ones (16
 // bytes of fp32); more per block is slower (fp32 states 144, 145, 149 us for 1,
-// 2, 4 times as many on 30M elements; 8-bit states 1.80, 1.91, 1.94 ms on 671M,
-// 6.0 TB/s at best).
+// 2, 4 times as many on 30M elements; 8-bit states 1.80, 1.91, 1.94 ms on 671M).
+// Now 141 us, and 1.74 to 1.79 ms (6.0 to 6.2 TB/s).
 //
 // 8-bit states are MX blocks of 32 consecutive elements (E4M3 codes, one E8M0
 // scale).  m is kept as it is and v as its root: E4M3 spans 2^-9 .. 448 inside

@@ -662,7 +662,9 @@ __global__ void __launch_bounds__(64) k_join(Product p) {
 // Its eight waves take the chunks of 256 bytes of the items' rows in turn, from
 // rings that go on from one item to the next, and add up through LDS.  x stays
 // in registers, kSkSteps chunks of a wave.  8192 x 5120 (84 MB): 16.7 us for one
-// row (5.0 TB/s), 19.7 for 16; 128 x 64 tiles take 23.5 for 1 to 64 rows.  (With
+// row (5.0 TB/s), 19.7 for 16; 128 x 64 tiles take 23.5 for 1 to 64 rows, of
+// which the split tiles' join is 4: above 16 rows x no longer fits the registers
+// beside the stream.  (With
 // k above 8192 x would have to be read again for each item: 1408 x 16384 took
 // 22 us for one row and 30 for 16, the tiles take 22.5.)
 constexpr int kSkWaves = 8;
@@ -822,9 +824,12 @@ __global__ void __launch_bounds__(64 * kSkWaves, 2) k_skinny(const uint16_t* __r
 }
 
 // ---------------------------------------------------------------- dz and dbias
-// dz = dout act'(z) in bf16 with rows of pitch elements (zeros past N), and
-// fp32 column sums of the unrounded dz over the block's rows: `part`
-// [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
+// dz = dout act'(z) in bf16 with rows of pitch elements (zeros past N): the type
+// of the matrix instruction's operand, in which a bf16 dout comes anyway; an fp32
+// one is rounded here too, as keeping its lower half would double both products
+// (dx and dw are then off by 0.0023 of their size, of which their own rounding
+// is 0.0017).  And fp32 column sums of the unrounded dz over the block's
+// rows: `part` [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
 template <typename T>
 __device__ __forceinline__ T load_once(const void* p) { return __builtin_nontemporal_load(static_cast<const T*>(p)); }
 
@@ -941,7 +946,7 @@ constexpr struct {
     {128, 128, 2, 1.13, 4.9e6},
     {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 107 with 128 x 128
     {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
-    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18.4 us, against 22 to 23 with the others
+    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18 us, against 22 to 23 with the others
 
 // Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
 // tiles of the last, partly filled round are split over the contraction so

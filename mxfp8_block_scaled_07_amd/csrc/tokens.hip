@@ -6,8 +6,11 @@
 //   id, -inf never), w_tj their softmax.
 //
 // Bound: each active expert's weights have to come from HBM once (3 F H
-// elements), and every other byte is small beside them.  The layer's path for
-// many tokens pads each expert to 32 rows and makes eighteen launches; here
+// elements), and every other byte is small beside them.  An expert with more
+// rows than the up kernel's register tiles hold (16 above H = 4096, 32 above
+// 2048, else 64) is several entries, and its weights are walked once for each:
+// H = 7168, F = 2048, 2 experts, top-1, MXFP8 takes 33 us for 16 tokens (8 rows
+// an expert) and 53 for 64.  The layer's path for many tokens pads each expert to 32 rows and makes eighteen launches; here
 //   k_tokens_up    every workgroup routes all tokens by itself (a few hundred
 //                  instructions per token, cheaper than a launch of its own),
 //                  then takes a run of items: 16 gate and 16 up rows of one
@@ -22,14 +25,17 @@
 // kernel keeps its waves' share of the tokens in registers while it stays with
 // an expert, and the down kernel's waves share theirs through LDS.
 //
-// 64 experts of 2048 x 7168, top-8, MXFP8: one token 69 us (up 42, down 23, join
-// 4.5; 5.3 TB/s of weights), 33 tokens 430 us (6.7 TB/s); 61 tokens, 8 experts of
-// 1408 x 2048 in bf16 47 us.
+// 64 experts of 2048 x 7168, top-8, MXFP8: one token 68 us (up 42, down 23, join
+// 4.5; 5.3 TB/s of weights), 33 tokens 440 us (6.5 TB/s); 61 tokens, 8 experts of
+// 1408 x 2048 in bf16 48 us.
 //
-// A is kept in bf16 (one rounding of w silu(G) U); everything else between the
-// bf16 inputs and outputs is fp32.  The weight goes into A so that the sum over
-// a token's experts is one fp32 sum.  All sums have a fixed order: the result
-// does not depend on scheduling.
+// A is kept in bf16 (one rounding of w silu(G) U), the type of the matrix
+// instruction's operand: a second bf16 term of it would double the down kernel's
+// products and its loads beside the stream, for an error that goes from 0.0017
+// to 0.0019-0.0023 of the result, whose own rounding is most of that.  Everything
+// else between the bf16 inputs and outputs is fp32.  The weight goes into A so
+// that the sum over a token's experts is one fp32 sum.  All sums have a fixed
+// order: the result does not depend on scheduling.
 
 #include "stream.h"
 
@@ -312,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_tokens_up(TokensProblem p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, h = lane >> 4;
   route_entries(rt, p.logits, p.T, p.E, p.k, 16 * kTiles);
+  // ahead of the stream: its reads of the logits are compiled loads, and waiting
+  // for them would wait for the stream's too.  Behind the first loads 61 tokens
+  // on 8 experts of 1408 x 2048 take 51 us, here 49; one token 67.5 either way.
   route_rows(rt, p.logits, p.E);
   lds_barrier();
   const int V = __builtin_amdgcn_readfirstlane(rt.entries);
