@@ -664,9 +664,8 @@ __global__ void __launch_bounds__(64) k_join(Product p) {
 // in registers, kSkSteps chunks of a wave.  8192 x 5120 (84 MB): 16.7 us for one
 // row (5.0 TB/s), 19.7 for 16; 128 x 64 tiles take 23.5 for 1 to 64 rows, of
 // which the split tiles' join is 4: above 16 rows x no longer fits the registers
-// beside the stream.  (With
-// k above 8192 x would have to be read again for each item: 1408 x 16384 took
-// 22 us for one row and 30 for 16, the tiles take 22.5.)
+// beside the stream.  (With k above 8192 x would have to be read again for each
+// item: 1408 x 16384 took 22 us for one row and 30 for 16, the tiles take 22.5.)
 constexpr int kSkWaves = 8;
 constexpr int kSkDepth = 3;                  // chunks of a wave in flight
 constexpr int kSkItems = 4;                  // items whose sums wait for each other
@@ -828,8 +827,8 @@ __global__ void __launch_bounds__(64 * kSkWaves, 2) k_skinny(const uint16_t* __r
 // of the matrix instruction's operand, in which a bf16 dout comes anyway; an fp32
 // one is rounded here too, as keeping its lower half would double both products
 // (dx and dw are then off by 0.0023 of their size, of which their own rounding
-// is 0.0017).  And fp32 column sums of the unrounded dz over the block's
-// rows: `part` [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
+// is 0.0017).  And fp32 column sums of the unrounded dz over the block's rows:
+// `part` [gridDim.y, N].  256 threads: ct groups of 8 columns x 256 / ct rows.
 template <typename T>
 __device__ __forceinline__ T load_once(const void* p) { return __builtin_nontemporal_load(static_cast<const T*>(p)); }
 

@@ -10,7 +10,8 @@
 // rows than the up kernel's register tiles hold (16 above H = 4096, 32 above
 // 2048, else 64) is several entries, and its weights are walked once for each:
 // H = 7168, F = 2048, 2 experts, top-1, MXFP8 takes 33 us for 16 tokens (8 rows
-// an expert) and 53 for 64.  The layer's path for many tokens pads each expert to 32 rows and makes eighteen launches; here
+// an expert) and 53 for 64.  The layer's path for many tokens pads each expert
+// to 32 rows and makes eighteen launches; here
 //   k_tokens_up    every workgroup routes all tokens by itself (a few hundred
 //                  instructions per token, cheaper than a launch of its own),
 //                  then takes a run of items: 16 gate and 16 up rows of one
@@ -829,7 +830,7 @@ int tokens_call(bool mxw, const uint16_t* x, const float* logits, int64_t tokens
 using namespace mx;
 
 extern "C" size_t mx_moe_tokens_workspace_size(int64_t tokens, int32_t topk, int32_t num_experts, int64_t F) {
-  if (tokens < 0 || topk < 1 || topk > num_experts || F <= 0) return 0;
+  if (tokens < 0 || topk < 1 || topk > num_experts || F <= 0 || F % 32) return 0;
   if (tokens > kMaxTokens || num_experts > kTokExperts || topk > kTokTopk || F >= (1ll << 24)) return 0;
   if (tokens * topk * F * 2 >= (1ll << 31)) return 0;
   return (size_t)tokens_bytes(tokens, topk, F);

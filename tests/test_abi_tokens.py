@@ -49,5 +49,6 @@ def test_no_workspace_for_what_is_refused(lib):  # noqa: F811
     n = lib.mx_moe_tokens_workspace_size
     assert n(64, 8, 1024, 2048) > 0 and n(64, 4, 4, 2048) > 0
     assert n(64, 8, 1025, 2048) == 0 and n(64, 5, 4, 2048) == 0 and n(64, 2, 8, 1 << 24) == 0
+    assert n(64, 2, 8, 33) == 0
     assert n(64, 64, 64, 1 << 18) == 0                  # w silu(g) u of 2^31 bytes
     assert call(lib, T=64, k=64, E=64, H=32, F=1 << 18) == (mxa.MX_EUNSUPPORTED, mxa.MX_EUNSUPPORTED)
