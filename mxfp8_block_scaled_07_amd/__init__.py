@@ -559,7 +559,7 @@ def adamw_table(rows):
         t.param, t.grad, t.m, t.v = (x.data_ptr() for x in (param, grad, m, v))
         t.m_scale, t.v_scale, t.copy = (None if x is None else x.data_ptr() for x in (m_scale, v_scale, copy))
         t.n = n
-        used = [(grad, False)] + [(x, True) for x in (param, m, v, m_scale, v_scale)]
+        used = [(grad, False)] + [(x, True) for x in (param, m, v, *((m_scale, v_scale) if bits == 8 else ()))]
         if copy is not None and not (copy.dtype == param.dtype and copy.data_ptr() == param.data_ptr()):
             used.append((copy, True))   # (over a bf16 parameter it writes the same values)
         ranges += [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), w) for x, w in used

@@ -136,6 +136,8 @@ def test_adamw_table_refuses_tensors_written_twice():
     with pytest.raises(ValueError, match="overlap"):          # a copy over its fp32 parameter
         mxa.adamw_table([[flat[:40]] + a[1:6] + [flat.view(bf)[:40]]])
     mxa.adamw_table([[flat[:40]] + a[1:], [flat[40:]] + b[1:]])
+    f = adam_row(bits=32)                                     # scales beside fp32 states are not touched
+    mxa.adamw_table([f[:4] + a[4:5] * 2 + f[6:]])
     p = torch.zeros(40, dtype=bf)                             # a bf16 parameter's copy has its value
     mxa.adamw_table([[p] + a[1:6] + [p]])
 
