@@ -418,6 +418,46 @@ int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const uint16_t* z, 
                        uint16_t* dw, float* dbias, void* workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * Root-mean-square norm in front of the layer, with the residual's addition
+ * and the MXFP8 quantize of its result (the rows the gate and mx_permute take).
+ *   r = x + residual, rounded to the stream's type (stream_dtype: MX_OUT_BF16
+ *   or MX_OUT_F32);  y = RNE_bf16(r s weight),  s = 1 / sqrt(mean(r^2) + eps)
+ *   x        bf16 [rows, cols]; residual [rows, cols] of the stream's type;
+ *            either may be NULL, not both
+ *   weight   fp32 [cols], or NULL for all ones
+ *   sum      optional [rows, cols] of the stream's type: r (may be residual)
+ *   y        optional bf16 [rows, cols]
+ *   row_q/row_s  optional rowwise MX of y (exactly the quantize of the bf16 y,
+ *            whether or not y is written): codes [rows, cols], scales
+ * fp32 sums in a fixed order.  At least one output; cols % 32 == 0; eps > 0;
+ * tensors 16-byte, row_q 8-byte, weight and row_s 4-byte aligned.
+ * MX_EUNSUPPORTED for cols > 65536 or rows >= 2^31.
+ */
+int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t stream_dtype, const float* weight, int64_t rows,
+               int64_t cols, double eps, void* sum, uint16_t* y, uint8_t* row_q, uint8_t* row_s, mx_stream_t stream);
+
+/*
+ * Backward of mx_rmsnorm; nothing but r is kept by the forward.
+ *   dr = s (dy weight - r s^2 mean(dy weight r)) + dsum
+ *   dy       bf16 [rows, cols]; sum [rows, cols] of the stream's type: the r of
+ *            the forward (its x, where it had no residual)
+ *   dsum     optional [rows, cols] of the stream's type: the gradient that
+ *            reaches r from elsewhere (the residual stream's)
+ *   dres     optional [rows, cols] of the stream's type: dr (may be dsum)
+ *   dx       optional bf16 [rows, cols]: dr for what made x
+ *   dweight  optional fp32 [cols]: sum_rows dy r s (zero for rows == 0)
+ * At least one output.  With dweight, workspace >=
+ * mx_rmsnorm_bwd_workspace_size(rows, cols) bytes (0 for what the call
+ * refuses); calls that overlap in time need their own.  Sizes and alignment as
+ * in the forward, workspace 16-byte; repeated calls give the same bits.
+ */
+size_t mx_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols);
+
+int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_t stream_dtype, const float* weight,
+                   int64_t rows, int64_t cols, double eps, void* dres, uint16_t* dx, float* dweight, void* workspace,
+                   size_t workspace_bytes, mx_stream_t stream);
+
+/*
  * BF16 baseline of the expert step: the same permute and grouped GEMMs with
  * bf16 operands, so the MXFP8 path can be timed against the BF16 MoE layer
  * the digest page compares with (Overview and Key Statistics & Figures: the

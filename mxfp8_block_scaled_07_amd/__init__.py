@@ -60,6 +60,9 @@ _SIGNATURES = {
     "mx_bf16_grouped_gemm_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_dgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_bf16_grouped_gemm_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
+    "mx_rmsnorm": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _vp]),
+    "mx_rmsnorm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "mx_rmsnorm_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -260,6 +263,21 @@ def mx_bf16_grouped_gemm_dgrad(dy, wt, group_offsets, num_groups, m_cap, n_out, 
 def mx_bf16_grouped_gemm_wgrad(dyt, xt, group_offsets, num_groups, m_cap, n, k, dw, out_dtype, stream=None):
     _check(lib().mx_bf16_grouped_gemm_wgrad(_p(dyt), _p(xt), _p(group_offsets), num_groups, m_cap, n, k, _p(dw),
                                             out_dtype, _s(stream)), "mx_bf16_grouped_gemm_wgrad")
+
+
+def mx_rmsnorm(x, residual, stream_dtype, weight, rows, cols, eps, sum, y, row_q, row_s, stream=None):
+    _check(lib().mx_rmsnorm(_p(x), _p(residual), stream_dtype, _p(weight), rows, cols, eps, _p(sum), _p(y), _p(row_q),
+                            _p(row_s), _s(stream)), "mx_rmsnorm")
+
+
+def mx_rmsnorm_bwd_workspace_size(rows, cols):
+    return int(lib().mx_rmsnorm_bwd_workspace_size(rows, cols))
+
+
+def mx_rmsnorm_bwd(dy, sum, dsum, stream_dtype, weight, rows, cols, eps, dres, dx, dweight, workspace, workspace_bytes,
+                   stream=None):
+    _check(lib().mx_rmsnorm_bwd(_p(dy), _p(sum), _p(dsum), stream_dtype, _p(weight), rows, cols, eps, _p(dres), _p(dx),
+                                _p(dweight), _p(workspace), workspace_bytes, _s(stream)), "mx_rmsnorm_bwd")
 
 
 # --- allocating helpers ----------------------------------------------------
@@ -506,6 +524,66 @@ def bf16_linear_bwd(dout, x, w, z=None, act=MX_ACT_NONE, dx_add=None, want_dbias
             if db is not None:
                 db.zero_()
     return dx, dw, db
+
+
+def _stream_kind(name, t):
+    """MX_OUT_BF16 or MX_OUT_F32 of a tensor of the residual stream, and its torch type."""
+    import torch
+    if t is None or t.dtype in (torch.bfloat16, torch.int16):
+        return MX_OUT_BF16, torch.bfloat16
+    _need(t.dtype == torch.float32, f"{name} is {t.dtype}, not bf16 or fp32")
+    return MX_OUT_F32, torch.float32
+
+
+def rmsnorm(x, weight=None, residual=None, eps=1e-6, want_bf16=True, rowwise=False, stream=None):
+    """Norm of x + residual: x bf16 [R, C], residual bf16 or fp32 [R, C], weight fp32 [C].  Returns (sum, y, row_q,
+    row_s): the new residual stream (x itself without a residual), the bf16 rows and their rowwise MX, None for what is
+    not asked for."""
+    import torch
+    R, C = x.shape
+    dev, bf = x.device, torch.bfloat16
+    _need(want_bf16 or rowwise, "rmsnorm: at least one of want_bf16 and rowwise")
+    _tensor("x", x, (R, C), bf)
+    kind, dtype = _stream_kind("residual", residual)
+    if residual is not None:
+        _tensor("residual", residual, (R, C), dtype, dev)
+    if weight is not None:
+        _tensor("weight", weight, (C,), torch.float32, dev)
+    with _on(dev, stream):
+        total = x if residual is None else torch.empty((R, C), dtype=dtype, device=dev)
+        y = torch.empty((R, C), dtype=bf, device=dev) if want_bf16 else None
+        rq, rs = _mx_pair(R, C, dev, rowwise)
+        if R:
+            mx_rmsnorm(x, residual, kind, weight, R, C, eps, None if residual is None else total, y, rq, rs, stream)
+    return total, y, rq, rs
+
+
+def rmsnorm_bwd(dy, sum, weight=None, dsum=None, eps=1e-6, want_dweight=True, stream=None):
+    """Backward of rmsnorm: dy bf16 [R, C]; sum, and the gradient dsum that reaches it from elsewhere, of the residual
+    stream's type.  Returns (dres in that type, dx in bf16, dweight fp32 [C] or None); dx is dres where the stream is
+    bf16."""
+    import torch
+    R, C = sum.shape
+    dev, bf = sum.device, torch.bfloat16
+    kind, dtype = _stream_kind("sum", sum)
+    _tensor("sum", sum, (R, C), dtype)
+    _tensor("dy", dy, (R, C), bf, dev)
+    if dsum is not None:
+        _tensor("dsum", dsum, (R, C), dtype, dev)
+    if weight is not None:
+        _tensor("weight", weight, (C,), torch.float32, dev)
+    with _on(dev, stream):
+        dres = torch.empty((R, C), dtype=dtype, device=dev)
+        dx = dres if kind == MX_OUT_BF16 else torch.empty((R, C), dtype=bf, device=dev)
+        dw = torch.empty(C, dtype=torch.float32, device=dev) if want_dweight else None
+        if R:
+            wsb = mx_rmsnorm_bwd_workspace_size(R, C) if want_dweight else 0
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+            mx_rmsnorm_bwd(dy, sum, dsum, kind, weight, R, C, eps, dres, None if kind == MX_OUT_BF16 else dx, dw, ws, wsb,
+                           stream)
+        elif dw is not None:   # empty tensors have no storage to pass
+            dw.zero_()
+    return dres, dx, dw
 
 
 def adamw_state(param, state_bits=32):
