@@ -418,6 +418,65 @@ int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const uint16_t* z, 
                        uint16_t* dw, float* dbias, void* workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * Activations kept in MXFP8 between the forward and the backward of the SwiGLU
+ * expert FFN: the forward keeps the gate/up product as MX codes and the tokens
+ * as the codes mx_permute took, and the backward works from those.
+ *
+ * mx_swiglu_keep: SwiGLU with both quantizes that the forward leaves.
+ *   h      bf16 [rows, 2F] (as in mx_swiglu_quantize)
+ *   row_q/row_s    rowwise MX of A [rows, F], as mx_swiglu_quantize gives it
+ *   keep_q/keep_s  rowwise MX of h [rows, 2F], as mx_quantize gives it
+ * Requires F % 32 == 0; h 16-byte, codes 8-byte, scales 4-byte aligned.
+ */
+int mx_swiglu_keep(const uint16_t* h, int64_t rows, int64_t F, uint8_t* row_q, uint8_t* row_s, uint8_t* keep_q,
+                   uint8_t* keep_s, mx_stream_t stream);
+
+/*
+ * SwiGLU backward from the kept codes; h' is their mx_dequantize.
+ *   da     bf16 [rows, F]
+ *   row_q/row_s, col_q/col_s  MX of dH [rows, 2F] and of its transpose, as
+ *          mx_swiglu_bwd_quantize(h', da) gives them; either pair may be NULL
+ *   a_col_q/a_col_s  columnwise MX of A' [F, rows], as mx_swiglu_quantize(h')
+ *          gives it; may be NULL
+ *   dots   optional fp32 [rows]: sum_f da[r, f] silu(g') u' (fp32, unrounded)
+ * At least one output; rows % 32 == 0 with a columnwise one; F % 32 == 0; da
+ * and columnwise codes 16-byte, other codes 8-byte, scales 4-byte aligned.
+ * With dots, workspace >= mx_swiglu_bwd_kept_workspace_size(rows, F) bytes (0
+ * for F <= 128: may be NULL), 16-byte aligned; calls that overlap in time need
+ * their own.  MX_EUNSUPPORTED for F > 2^22.  Repeated calls give the same bits.
+ */
+size_t mx_swiglu_bwd_kept_workspace_size(int64_t rows, int64_t F);
+
+int mx_swiglu_bwd_kept(const uint8_t* keep_q, const uint8_t* keep_s, const uint16_t* da, int64_t rows, int64_t F,
+                       uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* a_col_q,
+                       uint8_t* a_col_s, float* dots, void* workspace, size_t workspace_bytes, mx_stream_t stream);
+
+/*
+ * Router backward from those dots, without the down product's rows: with
+ * da the gradient behind the weighted combine, dots[dst_row[t topk + j]] =
+ * w[t,j] dw[t,j] of mx_router_bwd, and
+ *   dlogits[t, e] = dots_j - w[t,j] sum_i dots_i for e = expert_ids[t,j], 0 for
+ *   experts not chosen (fp32 [tokens, num_experts])
+ *   dots fp32 [rows]; dst_row, expert_ids, weights as in mx_router_bwd
+ * A dst_row entry outside [0, rows) counts as a dot of 0.  topk <= 64.
+ */
+int mx_router_bwd_dots(const float* dots, int64_t rows, const int32_t* dst_row, const int32_t* expert_ids,
+                       const float* weights, int64_t tokens, int32_t num_experts, int32_t topk, float* dlogits,
+                       mx_stream_t stream);
+
+/*
+ * Columnwise MX from rowwise MX: mx_quantize's columnwise result of the
+ * mx_dequantize of (q, s) [rows, cols], with its gather, in one pass over the
+ * codes (the up weight gradient's operand from the tokens' kept codes).
+ *   gather   optional int32 [rows_out], rows_out as in mx_quantize
+ *   col_q/col_s  codes [cols, rows_out], scales [cols, rows_out]
+ * Requires cols % 32 == 0, rows_out % 32 == 0; q 8-byte, col_q 16-byte, scales
+ * 4-byte aligned.
+ */
+int mx_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, const int32_t* gather,
+                  int64_t rows_out, uint8_t* col_q, uint8_t* col_s, mx_stream_t stream);
+
+/*
  * Root-mean-square norm in front of the layer, with the residual's addition
  * and the MXFP8 quantize of its result (the rows the gate and mx_permute take).
  *   r = x + residual, rounded to the stream's type (stream_dtype: MX_OUT_BF16

@@ -62,6 +62,11 @@ _SIGNATURES = {
     "mx_bf16_grouped_gemm_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp]),
     "mx_rmsnorm": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _vp]),
     "mx_rmsnorm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "mx_swiglu_keep": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "mx_swiglu_bwd_kept_workspace_size": (_sz, [_i64, _i64]),
+    "mx_swiglu_bwd_kept": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mx_router_bwd_dots": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp]),
+    "mx_requantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
     "mx_rmsnorm_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
@@ -280,6 +285,32 @@ def mx_rmsnorm_bwd(dy, sum, dsum, stream_dtype, weight, rows, cols, eps, dres, d
                                 _p(dweight), _p(workspace), workspace_bytes, _s(stream)), "mx_rmsnorm_bwd")
 
 
+def mx_swiglu_keep(h, rows, F, row_q, row_s, keep_q, keep_s, stream=None):
+    _check(lib().mx_swiglu_keep(_p(h), rows, F, _p(row_q), _p(row_s), _p(keep_q), _p(keep_s), _s(stream)),
+           "mx_swiglu_keep")
+
+
+def mx_swiglu_bwd_kept_workspace_size(rows, F):
+    return int(lib().mx_swiglu_bwd_kept_workspace_size(rows, F))
+
+
+def mx_swiglu_bwd_kept(keep_q, keep_s, da, rows, F, row_q, row_s, col_q, col_s, a_col_q, a_col_s, dots, workspace,
+                       workspace_bytes, stream=None):
+    _check(lib().mx_swiglu_bwd_kept(_p(keep_q), _p(keep_s), _p(da), rows, F, _p(row_q), _p(row_s), _p(col_q),
+                                    _p(col_s), _p(a_col_q), _p(a_col_s), _p(dots), _p(workspace), workspace_bytes,
+                                    _s(stream)), "mx_swiglu_bwd_kept")
+
+
+def mx_router_bwd_dots(dots, rows, dst_row, expert_ids, weights, tokens, num_experts, topk, dlogits, stream=None):
+    _check(lib().mx_router_bwd_dots(_p(dots), rows, _p(dst_row), _p(expert_ids), _p(weights), tokens, num_experts, topk,
+                                    _p(dlogits), _s(stream)), "mx_router_bwd_dots")
+
+
+def mx_requantize(q, s, rows, cols, gather, rows_out, col_q, col_s, stream=None):
+    _check(lib().mx_requantize(_p(q), _p(s), rows, cols, _p(gather), rows_out, _p(col_q), _p(col_s), _s(stream)),
+           "mx_requantize")
+
+
 # --- allocating helpers ----------------------------------------------------
 def scale_shape(rows, cols):
     """Shape of the scale bytes of an MX tensor with ``rows`` rows (batch
@@ -366,6 +397,74 @@ def swiglu_bwd_quantize(h, da, rowwise=True, colwise=True, want_bf16=False, stre
     if rows:
         mx_swiglu_bwd_quantize(h, da, rows, F, dh, rq, rs, cq, cs, stream)
     return dh, rq, rs, cq, cs
+
+
+def swiglu_keep(h, stream=None):
+    """h: bf16 [rows, 2F].  Returns (row_q, row_s, keep_q, keep_s): the rowwise MX of A and of h itself."""
+    import torch
+    rows, F = h.shape[0], h.shape[1] // 2
+    _tensor("h", h, (rows, 2 * F), torch.bfloat16)
+    with _on(h.device, stream):
+        rq, rs = _mx_pair(rows, F, h.device, True)
+        kq, ks = _mx_pair(rows, 2 * F, h.device, True)
+        if rows:
+            mx_swiglu_keep(h, rows, F, rq, rs, kq, ks, stream)
+    return rq, rs, kq, ks
+
+
+def swiglu_bwd_kept(keep_q, keep_s, da, rowwise=True, colwise=True, a_colwise=True, want_dots=True, stream=None):
+    """keep_q, keep_s as swiglu_keep left them, da bf16 [rows, F].  Returns (row_q, row_s, col_q, col_s) of dH, (a_col_q,
+    a_col_s) of the rebuilt A and the dots fp32 [rows], None for what is not asked for."""
+    import torch
+    rows, F, dev = da.shape[0], da.shape[1], da.device
+    _tensor("da", da, (rows, F), torch.bfloat16)
+    _tensor("keep_q", keep_q, (rows, 2 * F), torch.uint8, dev)
+    _tensor("keep_s", keep_s, scale_shape(rows, 2 * F), torch.uint8, dev)
+    with _on(dev, stream):
+        rq, rs = _mx_pair(rows, 2 * F, dev, rowwise)
+        cq, cs = _mx_pair(2 * F, rows, dev, colwise)
+        aq, as_ = _mx_pair(F, rows, dev, a_colwise)
+        dots = torch.empty(rows, dtype=torch.float32, device=dev) if want_dots else None
+        if rows:
+            wsb = mx_swiglu_bwd_kept_workspace_size(rows, F) if want_dots else 0
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+            mx_swiglu_bwd_kept(keep_q, keep_s, da, rows, F, rq, rs, cq, cs, aq, as_, dots, ws, wsb, stream)
+    return rq, rs, cq, cs, aq, as_, dots
+
+
+def router_bwd_dots(dots, dst_row, expert_ids, weights, num_experts, stream=None):
+    """The logits' gradient, fp32 [tokens, num_experts], from the dots of swiglu_bwd_kept."""
+    import torch
+    T, topk = weights.shape
+    dev = dots.device
+    _tensor("dots", dots, dots.shape, torch.float32)
+    _tensor("dst_row", dst_row, (T * topk,), torch.int32, dev)
+    _tensor("expert_ids", expert_ids, (T, topk), torch.int32, dev)
+    _tensor("weights", weights, (T, topk), torch.float32, dev)
+    with _on(dev, stream):
+        dl = torch.empty((T, num_experts), dtype=torch.float32, device=dev)
+        if T and not dots.numel():   # (no storage to pass; every pair's row is outside it)
+            dl.zero_()
+        elif T:
+            mx_router_bwd_dots(dots, dots.numel(), dst_row, expert_ids, weights, T, num_experts, topk, dl, stream)
+    return dl
+
+
+def requantize(q, s, rows_out=None, gather=None, stream=None):
+    """q, s: rowwise MX [rows, cols].  Returns (col_q, col_s), its columnwise MX of rows_out rows."""
+    import torch
+    rows, cols = q.shape
+    rows_out = (rows if gather is None else gather.numel()) if rows_out is None else rows_out
+    _tensor("q", q, (rows, cols), torch.uint8)
+    _tensor("s", s, scale_shape(rows, cols), torch.uint8, q.device)
+    if gather is not None:
+        _tensor("gather", gather, (rows_out,), torch.int32, q.device)
+    _need(rows > 0 or not rows_out, "requantize: no rows to take from")
+    with _on(q.device, stream):
+        cq, cs = _mx_pair(cols, rows_out, q.device, True)
+        if rows_out:
+            mx_requantize(q, s, rows, cols, gather, rows_out, cq, cs, stream)
+    return cq, cs
 
 
 def combine(y, dst_row, weights, tokens, topk, stream=None):

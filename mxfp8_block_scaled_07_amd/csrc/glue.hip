@@ -14,34 +14,12 @@
 //   dg = dA u sigmoid(g) (1 + g (1 - sigmoid(g))),  du = dA silu(g)
 //   out[t] = sum_j w[t,j] Y[dst_row[t k + j]]  (fma, j ascending)
 //   dY[dst_row[i]] = w[i] dOut[i / k]          (one fp32 product)
-// sigmoid uses e = exp(-|g|) in (0, 1]: sigmoid(|g|) = 1 / (1 + e) and
-// sigmoid(-|g|) = e / (1 + e), so neither 1 - sigmoid nor a large exponent
-// is ever formed.  1 + e lies in (1, 2], so its reciprocal is the hardware
-// one (V_RCP_F32, within 1 ulp; no denormal can occur) instead of a
-// correctly rounded division sequence.
 
+#include "swiglu.h"
 #include "tile_quant.h"
 
 namespace mx {
 namespace {
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// silu(g) and the two sigmoids sigmoid(g), sigmoid(-g).
-__device__ __forceinline__ float silu_parts(float g, float& s, float& sm) {
-  const float e = expf(-fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  const float er = e * r;
-  s = g >= 0.0f ? r : er;
-  sm = g >= 0.0f ? er : r;
-  return g * s;
-}
-
-__device__ __forceinline__ float swiglu1(float g, float u) {
-  float s, sm;
-  return silu_parts(g, s, sm) * u;
-}
 
 // SwiGLU forward: output [rows, F] from H [rows, 2F].
 struct SrcSwiglu {
@@ -120,23 +98,14 @@ struct SrcSwigluBwd {
     x.d = *reinterpret_cast<const uint4*>(w.pd + c);
     return x;
   }
-  __device__ static float dgate(float g, float u, float d) {
-    float s, sm;
-    silu_parts(g, s, sm);
-    return d * u * s * (1.0f + g * sm);
-  }
-  __device__ static float dup(float g, float d) {
-    float s, sm;
-    return d * silu_parts(g, s, sm);
-  }
   __device__ uint4 finish(const Raw& x, const Row&, int64_t col) const {
     const bool gate = col < F;
     uint4 o;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t g = tq_comp(x.g, k), u = tq_comp(x.u, k), d = tq_comp(x.d, k);
-      const float lo = gate ? dgate(bf_lo(g), bf_lo(u), bf_lo(d)) : dup(bf_lo(g), bf_lo(d));
-      const float hi = gate ? dgate(bf_hi(g), bf_hi(u), bf_hi(d)) : dup(bf_hi(g), bf_hi(d));
+      const float lo = gate ? swiglu_dgate(bf_lo(g), bf_lo(u), bf_lo(d)) : swiglu_dup(bf_lo(g), bf_lo(d));
+      const float hi = gate ? swiglu_dgate(bf_hi(g), bf_hi(u), bf_hi(d)) : swiglu_dup(bf_hi(g), bf_hi(d));
       const uint32_t v = bf16x2_rne(lo, hi);
       if (k == 0) o.x = v; else if (k == 1) o.y = v; else if (k == 2) o.z = v; else o.w = v;
     }

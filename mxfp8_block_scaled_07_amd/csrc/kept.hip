@@ -1,0 +1,371 @@
+// Activations of the SwiGLU expert FFN kept in MXFP8 between the forward and
+// the backward (gfx950).
+//
+// The forward keeps H = [g | u] as rowwise MX codes and the tokens as the codes
+// the permute took; the backward rebuilds from them what else it needs:
+//   A' = silu(g') u'        columnwise MX (the down weight gradient's operand)
+//   dH = [dA u' s (1 + g' (1 - s)) | dA silu(g')], s = sigmoid(g')   row and column MX
+//   dots[r] = sum_f dA[r, f] A'[r, f]
+//   X^T                     columnwise MX in permuted order, from the tokens' codes
+// with g', u' the decoded values.  dA = w_j W2^T dout, so dots[r] = w_j <dout,
+// W2 A'> of the pair (t, j) in row r: the router's gradient needs neither the
+// down product's rows nor another pass over H columns,
+//   dlogit[t, e_j] = dots_j - w_j sum_i dots_i.
+// A pair's activations between the passes are 33/32 2F bytes instead of 4F of H
+// in bf16, 33/32 F of A^T and 2H of the down product.
+//
+// All are HBM-bound streams in the tiles and orders of the tile quantizer.
+
+#include "stream.h"
+#include "swiglu.h"
+#include "tile_quant.h"
+
+namespace mx {
+namespace {
+
+// 8 codes with their block's scale byte to bf16, as the dequantize does it.
+__device__ __forceinline__ uint4 decode8(const uint2& c, uint32_t sb) {
+  const float sc = e8m0_to_f32(sb);
+  const uint2 a = cvt4_bf16(c.x, sc), b = cvt4_bf16(c.y, sc);
+  const uint4 v = make_uint4(a.x, a.y, b.x, b.y);
+  return sb == 255u ? make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u) : v;
+}
+
+// tq_store_rows for columns base + c0 .. of a matrix where base is a multiple of
+// 32 but panels may be shared with another tile: scales go out as bytes, the
+// last block's lane zeroes the panel's pad bytes.
+__device__ __forceinline__ void store_rows_bytes(const uint4 (&v)[8], uint8_t* row_q, uint8_t* row_s, int64_t R,
+                                                 int64_t cols, int64_t r, int64_t rows, int64_t col, bool col_ok) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool ok = r + i < rows && col_ok;
+    const uint32_t sb = scale_byte_from_amax(quad_max(amax8(v[i])));
+    const float sc = e8m0_to_f32(sb);
+    if (ok)
+      *reinterpret_cast<uint2*>(row_q + (r + i) * cols + col) =
+          make_uint2(cvt4_e4m3(v[i].x, v[i].y, sc), cvt4_e4m3(v[i].z, v[i].w, sc));
+    if (ok && !(threadIdx.x & 3)) put_scale(row_s, R, r + i, col >> 5, cols >> 5, sb);
+  }
+}
+
+// Half (gate or up) of a matrix [rows, 2F], at the tile's columns c0 .. of it.
+__device__ __forceinline__ void store_half(const uint4 (&v)[8], uint8_t* q, uint8_t* s, int64_t rows, int64_t F, int64_t r,
+                                           int64_t half, int64_t c0, bool col_ok) {
+  if (F % 128 == 0)
+    tq_store_rows<true, false>(v, q, s, nullptr, rows, 2 * F, r, r, rows, half + c0, col_ok);
+  else
+    store_rows_bytes(v, q, s, rows, 2 * F, r, rows, half + c0 + 8 * (threadIdx.x & 15), col_ok);
+}
+
+__global__ void __launch_bounds__(kTqThreads) k_swiglu_keep(const uint16_t* __restrict__ h, int64_t rows, int64_t F,
+                                                            int32_t n_tc, uint8_t* __restrict__ row_q,
+                                                            uint8_t* __restrict__ row_s, uint8_t* __restrict__ keep_q,
+                                                            uint8_t* __restrict__ keep_s) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ch = lane & 15;
+  const int64_t r = (int64_t)(blockIdx.x / (uint32_t)n_tc) * kTq + 32 * w + 8 * (lane >> 4);
+  const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)n_tc) * kTq, col = c0 + 8 * ch;
+  const bool col_ok = col < F;
+  uint4 g[8], u[8], a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    g[i] = u[i] = make_uint4(0, 0, 0, 0);
+    if (r + i < rows && col_ok) {
+      g[i] = *reinterpret_cast<const uint4*>(h + (r + i) * 2 * F + col);
+      u[i] = *reinterpret_cast<const uint4*>(h + (r + i) * 2 * F + F + col);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = tq_comp(g[i], k), y = tq_comp(u[i], k);
+      o[k] = bf16x2_rne(swiglu1(bf_lo(x), bf_lo(y)), swiglu1(bf_hi(x), bf_hi(y)));
+    }
+    a[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  tq_store_rows<true, false>(a, row_q, row_s, nullptr, rows, F, r, r, rows, c0, col_ok);
+  store_half(g, keep_q, keep_s, rows, F, r, 0, c0, col_ok);
+  store_half(u, keep_q, keep_s, rows, F, r, F, c0, col_ok);
+}
+
+struct KeptBwd {
+  const uint8_t* q;      // codes [rows, 2F]
+  const uint8_t* s;      // their scales
+  const uint16_t* da;    // bf16 [rows, F]
+  int64_t rows, F;
+  int32_t n_tc;
+  uint8_t *row_q, *row_s, *col_q, *col_s;   // dH
+  uint8_t *a_q, *a_s;                       // A' columnwise
+  float* dots;           // [n_tc, rows] partial sums, or the sums where n_tc is 1; or null
+};
+
+// Sum over the 16 lanes of a DPP row.
+__device__ __forceinline__ float row16_sum(float v) {
+#define MX_DPP_ADD(ctrl) v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xF, 0xF, true))
+  MX_DPP_ADD(0xB1);    // lane ^ 1
+  MX_DPP_ADD(0x4E);    // lane ^ 2
+  MX_DPP_ADD(0x141);   // the other quad of 8 lanes
+  MX_DPP_ADD(0x140);   // the other 8 lanes
+#undef MX_DPP_ADD
+  return v;
+}
+
+__global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kTq * kTq * 2];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ch = lane & 15;
+  const int32_t tc = (int32_t)(blockIdx.x % (uint32_t)p.n_tc);
+  const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)p.n_tc) * kTq, r = r0 + 32 * w + 8 * (lane >> 4);
+  const int64_t F = p.F, c0 = (int64_t)tc * kTq, col = c0 + 8 * ch;
+  const bool col_ok = col < F;
+  uint2 gq[8], uq[8];
+  uint32_t gs[8], us[8];
+  uint4 d[8];
+  // Loads through buffers: past the rows' end they give zeros, and a lane keeps
+  // one offset for all of its rows (as pointers they do not fit the registers).
+  const int64_t left = p.rows - r0 < kTq ? p.rows - r0 : kTq;
+  const __amdgpu_buffer_rsrc_t bq = buf(p.q + r0 * 2 * F, left * 2 * F), bd = buf(p.da + r0 * F, left * 2 * F);
+  const uint32_t lr = (uint32_t)(r - r0), stride = (uint32_t)(2 * F);   // (both have rows of 2 F bytes)
+  const uint32_t og = col_ok ? lr * stride + (uint32_t)col : kOob, od = col_ok ? lr * stride + 2u * (uint32_t)col : kOob;
+  const uint32_t ou = col_ok ? og + (uint32_t)F : kOob;
+  const uint8_t* sg = p.s + scale_index(p.rows, r, col >> 5);   // the rows' bytes are 4 apart
+  const uint8_t* su = p.s + scale_index(p.rows, r, (F + col) >> 5);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    gq[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bq, (int)(og + i * stride), 0, 0));
+    uq[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bq, (int)(ou + i * stride), 0, 0));
+    d[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(bd, (int)(od + i * stride), 0, 0));
+    gs[i] = us[i] = 0;
+    if (r + i < p.rows && col_ok) {
+      gs[i] = sg[4 * i];
+      us[i] = su[4 * i];
+    }
+  }
+  uint4 vg[8], vu[8], va[8];
+  float mine = 0.0f;   // lane ch < 8: the dot of row r + ch
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 g4 = decode8(gq[i], gs[i]), u4 = decode8(uq[i], us[i]);
+    float dot = 0.0f;
+    uint32_t wg[4], wu[4], wa[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = tq_comp(g4, k), y = tq_comp(u4, k), z = tq_comp(d[i], k);
+      const float gl = bf_lo(x), gh = bf_hi(x), ul = bf_lo(y), uh = bf_hi(y), dl = bf_lo(z), dh = bf_hi(z);
+      const float al = swiglu1(gl, ul), ah = swiglu1(gh, uh);
+      wg[k] = bf16x2_rne(swiglu_dgate(gl, ul, dl), swiglu_dgate(gh, uh, dh));
+      wu[k] = bf16x2_rne(swiglu_dup(gl, dl), swiglu_dup(gh, dh));
+      wa[k] = bf16x2_rne(al, ah);
+      // rounded here: put off to their uses, the unrounded values of all rows would have to be kept
+      asm volatile("" : "+v"(wg[k]), "+v"(wu[k]), "+v"(wa[k]));
+      dot = fmaf(dl, al, dot);
+      dot = fmaf(dh, ah, dot);
+    }
+    vg[i] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+    vu[i] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+    va[i] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+    if (p.dots) {
+      dot = row16_sum(dot);
+      mine = ch == i ? dot : mine;
+    }
+    __builtin_amdgcn_sched_barrier(0);   // a row at a time: interleaved, the rows' terms do not fit the registers
+  }
+  if (p.dots && ch < 8 && r + ch < p.rows) p.dots[(int64_t)tc * p.rows + r + ch] = mine;
+  if (p.row_q) {
+    store_half(vg, p.row_q, p.row_s, p.rows, F, r, 0, c0, col_ok);
+    store_half(vu, p.row_q, p.row_s, p.rows, F, r, F, c0, col_ok);
+  }
+  if (p.col_q) {
+    tq_store_cols<false>(vg, lds, p.col_q, p.col_s, 2 * F, c0, F - c0, p.rows, r0);
+    __syncthreads();
+    tq_store_cols<false>(vu, lds, p.col_q, p.col_s, 2 * F, F + c0, F - c0, p.rows, r0);
+  }
+  if (p.a_q) {
+    if (p.col_q) __syncthreads();
+    tq_store_cols<false>(va, lds, p.a_q, p.a_s, F, c0, F - c0, p.rows, r0);
+  }
+}
+
+// The tiles' partial sums of a row, in order.
+__global__ void __launch_bounds__(256) k_dots_join(const float* __restrict__ part, int64_t rows, int32_t n_tc,
+                                                   float* __restrict__ dots) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (r >= rows) return;
+  float t = 0.0f;
+#pragma unroll 8
+  for (int32_t c = 0; c < n_tc; ++c) t += part[(int64_t)c * rows + r];
+  dots[r] = t;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// One wave per token: lane j holds the dot of its pair j.
+__global__ void __launch_bounds__(256) k_router_bwd_dots(const float* __restrict__ dots, int64_t rows,
+                                                         const int32_t* __restrict__ dst_row,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ weights, int64_t tokens, int32_t E,
+                                                         int32_t topk, float* __restrict__ dlogits) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= tokens) return;
+  const int lane = threadIdx.x & 63;
+  float p = 0.0f, w = 0.0f;
+  int32_t esel = -1;
+  if (lane < topk) {
+    const int32_t r = dst_row[t * topk + lane];
+    if (r >= 0 && r < rows) p = dots[r];
+    w = weights[t * topk + lane];
+    esel = ids[t * topk + lane];
+  }
+  const float gsel = p - w * wave_sum(p);
+  for (int e0 = 0; e0 < E; e0 += 64) {   // every lane stays in the loop: the others read its pair
+    const int e = e0 + lane;
+    float val = 0.0f;
+    for (int32_t j = 0; j < topk; ++j) {
+      const int32_t ej = __shfl(esel, j, 64);
+      const float gj = __shfl(gsel, j, 64);
+      if (ej == e) val += gj;   // (a repeated expert sums its terms)
+    }
+    if (e < E) dlogits[t * E + e] = val;
+  }
+}
+
+// Source of the tile quantizer: rowwise MX rows, decoded; gathered or in order.
+template <bool kGather>
+struct SrcMx {
+  const uint8_t* q;
+  const uint8_t* s;
+  const int32_t* gather;
+  int64_t rows_in, cols;
+  struct Table {
+    int32_t src[kGather ? kTq : 1];
+  };
+  static constexpr bool kTable = kGather;
+  static constexpr bool kGathered = kGather;
+  static constexpr int kSub = 1;
+  static constexpr bool kFetchAll = false;
+  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out) const {
+    const int t = threadIdx.x;
+    if (kGather && t < kTq) {
+      int32_t g = r0 + t < rows_out ? gather[r0 + t] : -1;
+      tb.src[t] = g < rows_in ? g : -1;
+    }
+  }
+  struct Row {
+    bool ok;
+    int64_t r;
+  };
+  __device__ Row row(const Table& tb, int64_t, int64_t r, int lr, bool in_range) const {
+    Row w;
+    w.r = kGather ? tb.src[lr] : r;
+    w.ok = in_range && w.r >= 0 && w.r < rows_in;
+    return w;
+  }
+  struct Raw {
+    uint2 c;
+    uint32_t sb;
+  };
+  __device__ Raw fetch(const Row& w, int64_t col, bool) const {
+    Raw x;
+    x.c = *reinterpret_cast<const uint2*>(q + w.r * cols + col);
+    x.sb = s[scale_index(rows_in, w.r, col >> 5)];
+    return x;
+  }
+  __device__ uint4 finish(const Raw& x, const Row&, int64_t) const { return decode8(x.c, x.sb); }
+};
+
+// 128 rows of H in bytes stay below the 2^31 of a buffer's offsets.
+constexpr int64_t kMaxF = 1 << 22;
+
+inline bool misaligned(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)); }
+
+// A pair of codes and scales: both or none, codes aligned to `a`.
+inline bool bad_pair(const uint8_t* q, const uint8_t* s, uintptr_t a) {
+  return (q == nullptr) != (s == nullptr) || misaligned(q, a) || misaligned(s, 4);
+}
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" int mx_swiglu_keep(const uint16_t* h, int64_t rows, int64_t F, uint8_t* row_q, uint8_t* row_s,
+                              uint8_t* keep_q, uint8_t* keep_s, mx_stream_t stream) {
+  if (!h || !row_q || !keep_q || rows < 0 || F <= 0 || F % 32) return MX_EINVAL;
+  if (misaligned(h, 16) || bad_pair(row_q, row_s, 8) || bad_pair(keep_q, keep_s, 8)) return MX_EINVAL;
+  if (rows == 0) return MX_OK;
+  TqShape sh;
+  unsigned grid;
+  if (!tq_shape(1, rows, F, sh, grid)) return MX_EINVAL;
+  hipLaunchKernelGGL(k_swiglu_keep, dim3(grid), dim3(kTqThreads), 0, reinterpret_cast<hipStream_t>(stream), h, rows, F,
+                     sh.n_tc, row_q, row_s, keep_q, keep_s);
+  return launch_status();
+}
+
+extern "C" size_t mx_swiglu_bwd_kept_workspace_size(int64_t rows, int64_t F) {
+  TqShape sh;
+  unsigned grid;
+  if (rows <= 0 || F <= 0 || F % 32 || F > kMaxF || !tq_shape(1, rows, F, sh, grid) || sh.n_tc == 1) return 0;
+  return (size_t)(4 * rows * sh.n_tc);
+}
+
+extern "C" int mx_swiglu_bwd_kept(const uint8_t* keep_q, const uint8_t* keep_s, const uint16_t* da, int64_t rows,
+                                  int64_t F, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s,
+                                  uint8_t* a_col_q, uint8_t* a_col_s, float* dots, void* workspace,
+                                  size_t workspace_bytes, mx_stream_t stream) {
+  if (!keep_q || !keep_s || !da || rows < 0 || F <= 0 || F % 32) return MX_EINVAL;
+  if (bad_pair(keep_q, keep_s, 8) || misaligned(da, 16) || bad_pair(row_q, row_s, 8) || bad_pair(col_q, col_s, 16) ||
+      bad_pair(a_col_q, a_col_s, 16) || misaligned(dots, 4) || misaligned(workspace, 16))
+    return MX_EINVAL;
+  if ((!row_q && !col_q && !a_col_q && !dots) || ((col_q || a_col_q) && rows % 32)) return MX_EINVAL;
+  if (F > kMaxF) return MX_EUNSUPPORTED;
+  if (rows == 0) return MX_OK;
+  TqShape sh;
+  unsigned grid;
+  if (!tq_shape(1, rows, F, sh, grid)) return MX_EINVAL;
+  const size_t need = dots ? mx_swiglu_bwd_kept_workspace_size(rows, F) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return MX_EINVAL;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const KeptBwd p{keep_q, keep_s, da, rows, F, sh.n_tc, row_q, row_s, col_q, col_s, a_col_q, a_col_s,
+                  need ? static_cast<float*>(workspace) : dots};
+  hipLaunchKernelGGL(k_swiglu_bwd_kept, dim3(grid), dim3(kTqThreads), 0, st, p);
+  if (need)
+    hipLaunchKernelGGL(k_dots_join, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, st,
+                       static_cast<const float*>(workspace), rows, sh.n_tc, dots);
+  return launch_status();
+}
+
+extern "C" int mx_router_bwd_dots(const float* dots, int64_t rows, const int32_t* dst_row, const int32_t* expert_ids,
+                                  const float* weights, int64_t tokens, int32_t num_experts, int32_t topk,
+                                  float* dlogits, mx_stream_t stream) {
+  if (!dots || !dst_row || !expert_ids || !weights || !dlogits || rows < 0 || tokens < 0) return MX_EINVAL;
+  if (num_experts < 1 || topk < 1 || topk > 64) return MX_EINVAL;
+  if (tokens == 0) return MX_OK;
+  const int64_t blocks = (tokens + 3) / 4;
+  if (blocks > 0x7FFFFFFF) return MX_EINVAL;
+  hipLaunchKernelGGL(k_router_bwd_dots, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                     dots, rows, dst_row, expert_ids, weights, tokens, num_experts, topk, dlogits);
+  return launch_status();
+}
+
+extern "C" int mx_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, const int32_t* gather,
+                             int64_t rows_out, uint8_t* col_q, uint8_t* col_s, mx_stream_t stream) {
+  if (!q || !s || !col_q || rows < 0 || cols <= 0 || cols % 32 || rows_out < 0 || rows_out % 32) return MX_EINVAL;
+  if (bad_pair(q, s, 8) || bad_pair(col_q, col_s, 16) || misaligned(gather, 4)) return MX_EINVAL;
+  if (rows_out == 0) return MX_OK;
+  TqShape sh;
+  unsigned grid;
+  if (!tq_shape(1, rows_out, cols, sh, grid)) return MX_EINVAL;
+  const TqOut o = {nullptr, nullptr, col_q, col_s, nullptr};
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (gather)
+    hipLaunchKernelGGL((k_tile_quant<SrcMx<true>, false, true, false>), dim3(grid), dim3(kTqThreads), 0, st,
+                       SrcMx<true>{q, s, gather, rows, cols}, sh, o);
+  else
+    hipLaunchKernelGGL((k_tile_quant<SrcMx<false>, false, true, false>), dim3(grid), dim3(kTqThreads), 0, st,
+                       SrcMx<false>{q, s, gather, rows, cols}, sh, o);
+  return launch_status();
+}

@@ -71,6 +71,98 @@ __device__ __forceinline__ uint32_t amax8(const uint4& v) {
   return hmax(m);
 }
 
+// The row phase of a 128 x 128 tile: rows lr0 .. lr0 + 7 (of rows_out) at the
+// thread's 8 columns of the tile's columns c0 .. (a multiple of 128), v zero
+// where the tile hangs over.  R: rows of the whole output, row: the output row
+// of v[0], r: its index below rows_out.
+template <bool kRow, bool kY>
+__device__ __forceinline__ void tq_store_rows(const uint4 (&v)[8], uint8_t* row_q, uint8_t* row_s, uint16_t* y, int64_t R,
+                                              int64_t cols, int64_t row, int64_t r, int64_t rows_out, int64_t c0,
+                                              bool col_ok) {
+  const int ch = threadIdx.x & 15;
+  const int64_t col = c0 + 8 * ch;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool r_ok = r + i < rows_out;
+    const int64_t orow = row + i;
+    if (kY && r_ok && col_ok) *reinterpret_cast<uint4*>(y + orow * cols + col) = v[i];
+    if (kRow) {
+      const uint32_t sb = scale_byte_from_amax(quad_max(amax8(v[i])));
+      const float sc = e8m0_to_f32(sb);
+      if (r_ok && col_ok)
+        *reinterpret_cast<uint2*>(row_q + orow * cols + col) =
+            make_uint2(cvt4_e4m3(v[i].x, v[i].y, sc), cvt4_e4m3(v[i].z, v[i].w, sc));
+      uint32_t d = sb << (8 * (ch >> 2));
+      d |= dpp_row_shr(d, 4);
+      d |= dpp_row_shr(d, 8);
+      if (r_ok && ch == 12) *reinterpret_cast<uint32_t*>(row_s + ((c0 >> 7) * R + orow) * 4) = d;
+    }
+  }
+}
+
+// The column phase: the tile's columns, of which n_cols exist, become rows
+// crow .. of the transposed output (C rows of rows_out); r0: the tile's first
+// row.  lds: the tile's 32 KB, free of other uses.
+template <bool kNt>
+__device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds, uint8_t* col_q, uint8_t* col_s, int64_t C,
+                                              int64_t crow, int64_t n_cols, int64_t rows_out, int64_t r0) {
+  const int t = threadIdx.x;
+  const int lane = t & 63, w = t >> 6;
+  const int ch = lane & 15, ry = lane >> 4;
+  const int lr0 = 32 * w + 8 * ry;
+  const int slot = lr0 >> 3;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int cc = 8 * ch + j;
+    const int k = j >> 1;
+    uint32_t d[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t a = tq_comp(v[2 * p], k), bb = tq_comp(v[2 * p + 1], k);
+      d[p] = (j & 1) ? (a >> 16) | (bb & 0xFFFF0000u) : (a & 0xFFFFu) | (bb << 16);
+    }
+    *reinterpret_cast<uint4*>(lds + cc * 256 + 16 * (slot ^ tq_swz(cc))) = make_uint4(d[0], d[1], d[2], d[3]);
+  }
+  __syncthreads();
+  // 8 lanes per column, 16 rows each (two slots): the 8 lanes of a column
+  // store its 128 code bytes as one whole line.  Lanes 2q and 2q + 1 share
+  // the 32-row block q (amax exchanged with a DPP quad permute); the
+  // column's 4 scale bytes (lanes 0, 2, 4, 6 of the group) are merged with
+  // row shifts into lane 6, which stores the panel dword.
+  const int p = t & 7;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int c = 32 * it + (t >> 3);
+    const uint4 q0 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p) ^ tq_swz(c)));
+    const uint4 q1 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p + 1) ^ tq_swz(c)));
+    const uint32_t m0 = amax8(q0), m1 = amax8(q1);
+    uint32_t m = m0 > m1 ? m0 : m1;
+    const uint32_t mo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+    m = m > mo ? m : mo;
+    const uint32_t sb = scale_byte_from_amax(m);
+    const float sc = e8m0_to_f32(sb);
+    const int64_t gr = r0 + 16 * p;   // rows_out % 32 == 0: the 16 rows are all in or all out
+    if (c < n_cols && gr < rows_out) {
+      typedef unsigned int v4u_ __attribute__((ext_vector_type(4)));
+      const v4u_ cw = {cvt4_e4m3(q0.x, q0.y, sc), cvt4_e4m3(q0.z, q0.w, sc), cvt4_e4m3(q1.x, q1.y, sc),
+                       cvt4_e4m3(q1.z, q1.w, sc)};
+      v4u_* dst = reinterpret_cast<v4u_*>(col_q + (crow + c) * rows_out + gr);
+      // Gathered sources walk the row bands of a column tile, so their
+      // columnwise lines are written front to back: streamed (non-temporal)
+      // stores are faster there (measured 7% on the gathered columnwise
+      // quantize) and slightly slower for the plain order.
+      if constexpr (kNt) __builtin_nontemporal_store(cw, dst);
+      else *dst = cw;
+    }
+    uint32_t d = (p & 1) ? 0u : sb << (8 * (p >> 1));
+    const uint32_t d2 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x112, 0xF, 0xF, true);  // lane - 2
+    d |= p >= 2 ? d2 : 0u;
+    const uint32_t d4 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x114, 0xF, 0xF, true);  // lane - 4
+    d |= p >= 4 ? d4 : 0u;
+    if (p == 6 && c < n_cols) *reinterpret_cast<uint32_t*>(col_s + ((r0 >> 7) * C + crow + c) * 4) = d;
+  }
+}
+
 // Source concept:
 //   struct Table;                          LDS table filled once per tile (may be empty)
 //   static constexpr bool kTable;          whether fill_table must run
@@ -158,86 +250,16 @@ __global__ void __launch_bounds__(kTqThreads) k_tile_quant(const Src src, const 
         v[i] = rw[i].ok && col_ok ? src.finish(raw[i], rw[i], col) : make_uint4(0, 0, 0, 0);
     }
 
-    if (kRow || kY) {
-      const int64_t R = (int64_t)sh.batch * sh.rows_out;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + lr0 + i;
-        const bool r_ok = r < sh.rows_out;
-        const int64_t orow = (int64_t)b * sh.rows_out + r;
-        if (kY && r_ok && col_ok) *reinterpret_cast<uint4*>(o.y + orow * sh.cols + col) = v[i];
-        if (kRow) {
-          const uint32_t sb = scale_byte_from_amax(quad_max(amax8(v[i])));
-          const float sc = e8m0_to_f32(sb);
-          if (r_ok && col_ok)
-            *reinterpret_cast<uint2*>(o.row_q + orow * sh.cols + col) =
-                make_uint2(cvt4_e4m3(v[i].x, v[i].y, sc), cvt4_e4m3(v[i].z, v[i].w, sc));
-          uint32_t d = sb << (8 * (ch >> 2));
-          d |= dpp_row_shr(d, 4);
-          d |= dpp_row_shr(d, 8);
-          if (r_ok && ch == 12) *reinterpret_cast<uint32_t*>(o.row_s + ((c0 >> 7) * R + orow) * 4) = d;
-        }
-      }
-    }
+    if (kRow || kY)
+      tq_store_rows<kRow, kY>(v, o.row_q, o.row_s, o.y, (int64_t)sh.batch * sh.rows_out, sh.cols,
+                              (int64_t)b * sh.rows_out + r0 + lr0, r0 + lr0, sh.rows_out, c0, col_ok);
 
     if (kCol) {
       // every wave is done with the row table (it shares the LDS tile) and with
       // the previous column tile's reads
       if (Src::kTable || kSub > 1) __syncthreads();
-      const int slot = lr0 >> 3;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int cc = 8 * ch + j;
-        const int k = j >> 1;
-        uint32_t d[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t a = tq_comp(v[2 * p], k), bb = tq_comp(v[2 * p + 1], k);
-          d[p] = (j & 1) ? (a >> 16) | (bb & 0xFFFF0000u) : (a & 0xFFFFu) | (bb << 16);
-        }
-        *reinterpret_cast<uint4*>(lds + cc * 256 + 16 * (slot ^ tq_swz(cc))) = make_uint4(d[0], d[1], d[2], d[3]);
-      }
-      __syncthreads();
-      // 8 lanes per column, 16 rows each (two slots): the 8 lanes of a column
-      // store its 128 code bytes as one whole line.  Lanes 2q and 2q + 1 share
-      // the 32-row block q (amax exchanged with a DPP quad permute); the
-      // column's 4 scale bytes (lanes 0, 2, 4, 6 of the group) are merged with
-      // row shifts into lane 6, which stores the panel dword.
-      const int p = t & 7;
-      const int64_t C = (int64_t)sh.batch * sh.cols;
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int c = 32 * it + (t >> 3);
-        const int64_t gc = c0 + c;
-        const uint4 q0 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p) ^ tq_swz(c)));
-        const uint4 q1 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p + 1) ^ tq_swz(c)));
-        const uint32_t m0 = amax8(q0), m1 = amax8(q1);
-        uint32_t m = m0 > m1 ? m0 : m1;
-        const uint32_t mo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true);  // lane ^ 1
-        m = m > mo ? m : mo;
-        const uint32_t sb = scale_byte_from_amax(m);
-        const float sc = e8m0_to_f32(sb);
-        const int64_t gr = r0 + 16 * p;   // rows_out % 32 == 0: the 16 rows are all in or all out
-        if (gc < sh.cols && gr < sh.rows_out) {
-          typedef unsigned int v4u_ __attribute__((ext_vector_type(4)));
-          const v4u_ cw = {cvt4_e4m3(q0.x, q0.y, sc), cvt4_e4m3(q0.z, q0.w, sc), cvt4_e4m3(q1.x, q1.y, sc),
-                           cvt4_e4m3(q1.z, q1.w, sc)};
-          v4u_* dst = reinterpret_cast<v4u_*>(o.col_q + ((int64_t)b * sh.cols + gc) * sh.rows_out + gr);
-          // Gathered sources walk the row bands of a column tile, so their
-          // columnwise lines are written front to back: streamed (non-temporal)
-          // stores are faster there (measured 7% on the gathered columnwise
-          // quantize) and slightly slower for the plain order.
-          if constexpr (Src::kGathered) __builtin_nontemporal_store(cw, dst);
-          else *dst = cw;
-        }
-        uint32_t d = (p & 1) ? 0u : sb << (8 * (p >> 1));
-        const uint32_t d2 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x112, 0xF, 0xF, true);  // lane - 2
-        d |= p >= 2 ? d2 : 0u;
-        const uint32_t d4 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x114, 0xF, 0xF, true);  // lane - 4
-        d |= p >= 4 ? d4 : 0u;
-        if (p == 6 && gc < sh.cols)
-          *reinterpret_cast<uint32_t*>(o.col_s + ((r0 >> 7) * C + (int64_t)b * sh.cols + gc) * 4) = d;
-      }
+      tq_store_cols<Src::kGathered>(v, lds, o.col_q, o.col_s, (int64_t)sh.batch * sh.cols, (int64_t)b * sh.cols + c0,
+                                    sh.cols - c0, sh.rows_out, r0);
     }
   }
 }
