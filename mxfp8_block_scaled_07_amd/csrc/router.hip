@@ -148,14 +148,15 @@ __global__ void __launch_bounds__(256) k_router_bwd(const uint16_t* __restrict__
     const float inner = wave_sum(w * my_dw);
     const float gsel = mine ? w * (my_dw - inner) : 0.0f;
     const int32_t esel = mine ? ids[t * topk + lane] : -1;
-    for (int e = lane; e < E; e += 64) {
+    for (int e0 = 0; e0 < E; e0 += 64) {   // every lane stays in the loop: the others read its pair
+      const int e = e0 + lane;
       float val = 0.0f;
       for (int32_t j = 0; j < topk; ++j) {
         const int32_t ej = __shfl(esel, j, 64);
         const float gj = __shfl(gsel, j, 64);
         if (ej == e) val += gj;
       }
-      dlogits[t * E + e] = val;
+      if (e < E) dlogits[t * E + e] = val;
     }
   }
 }
