@@ -517,6 +517,37 @@ int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_
                    size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * Softmax cross entropy over a vocabulary, from the hidden rows and the output
+ * weights, with its gradient; the logits are not kept.
+ *   z = x w^T;  lse_i = log sum_v exp z[i,v];  loss_i = lse_i - z[i, targets[i]]
+ *   dz[i] = row_weight[i] (softmax(z[i]) - onehot(targets[i]))
+ *   dx = dz w,  dw = dz^T x      (the gradient of sum_i row_weight[i] loss[i])
+ *   x        bf16 [rows, k]; w bf16 [vocab, k]
+ *   targets  int32 [rows]; a row whose target is outside [0, vocab) is left out:
+ *            its loss is 0 and it adds nothing to dx or dw, whatever x holds there
+ *            (its lse is still that of its logits)
+ *   row_weight  optional fp32 [rows] (NULL: ones), of the gradient alone
+ *   loss, lse   optional fp32 [rows]
+ *   dx       optional bf16 [rows, k]; dw optional bf16 [vocab, k]
+ *   workspace >= mx_bf16_xent_workspace_size(rows, vocab, k, backward) bytes,
+ *            backward != 0 with dx or dw; calls that overlap in time need their
+ *            own.  The size is 0 for arguments of its own that the call refuses.
+ * fp32 sums; dz is rounded to bf16 once for the two products (the matrix
+ * instruction's operand).  At least one output.  Any rows >= 0 (with 0, dw is
+ * zero) and vocab >= 1; k % 32 == 0; x, w, dx, dw and workspace 16-byte, the
+ * others 4-byte aligned.  MX_EUNSUPPORTED for vocab or k >= 2^21, rows >= 2^31 or
+ * a launch of 2^32 threads.  With gradients, rows are taken in chunks whose
+ * exponentials (2 bytes a logit) fill at most 2 GiB of the workspace (256 rows at
+ * least); with several, 4 vocab k bytes of it hold the sum of dw.  Repeated calls
+ * give the same bits.
+ */
+size_t mx_bf16_xent_workspace_size(int64_t rows, int64_t vocab, int64_t k, int32_t backward);
+
+int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t* targets, const float* row_weight, int64_t rows,
+                 int64_t vocab, int64_t k, float* loss, float* lse, uint16_t* dx, uint16_t* dw, void* workspace,
+                 size_t workspace_bytes, mx_stream_t stream);
+
+/*
  * BF16 baseline of the expert step: the same permute and grouped GEMMs with
  * bf16 operands, so the MXFP8 path can be timed against the BF16 MoE layer
  * the digest page compares with (Overview and Key Statistics & Figures: the

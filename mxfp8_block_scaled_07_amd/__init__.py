@@ -67,6 +67,8 @@ _SIGNATURES = {
     "mx_swiglu_bwd_kept": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mx_router_bwd_dots": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp]),
     "mx_requantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "mx_bf16_xent_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "mx_bf16_xent": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mx_rmsnorm_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
@@ -309,6 +311,15 @@ def mx_router_bwd_dots(dots, rows, dst_row, expert_ids, weights, tokens, num_exp
 def mx_requantize(q, s, rows, cols, gather, rows_out, col_q, col_s, stream=None):
     _check(lib().mx_requantize(_p(q), _p(s), rows, cols, _p(gather), rows_out, _p(col_q), _p(col_s), _s(stream)),
            "mx_requantize")
+
+
+def mx_bf16_xent_workspace_size(rows, vocab, k, backward):
+    return int(lib().mx_bf16_xent_workspace_size(rows, vocab, k, int(bool(backward))))
+
+
+def mx_bf16_xent(x, w, targets, row_weight, rows, vocab, k, loss, lse, dx, dw, workspace, workspace_bytes, stream=None):
+    _check(lib().mx_bf16_xent(_p(x), _p(w), _p(targets), _p(row_weight), rows, vocab, k, _p(loss), _p(lse), _p(dx),
+                              _p(dw), _p(workspace), workspace_bytes, _s(stream)), "mx_bf16_xent")
 
 
 # --- allocating helpers ----------------------------------------------------
@@ -683,6 +694,31 @@ def rmsnorm_bwd(dy, sum, weight=None, dsum=None, eps=1e-6, want_dweight=True, st
         elif dw is not None:   # empty tensors have no storage to pass
             dw.zero_()
     return dres, dx, dw
+
+
+def bf16_xent(x, w, targets, row_weight=None, want_grad=False, stream=None):
+    """Cross entropy of x w^T: x bf16 [M, K], w bf16 [V, K], targets int32 [M] (outside [0, V): left out), row_weight
+    fp32 [M], of the gradient.  Returns (loss fp32 [M], lse fp32 [M], dx bf16 [M, K], dw bf16 [V, K]), the last two None
+    without want_grad."""
+    import torch
+    M, K = x.shape
+    V, dev, bf = w.shape[0], x.device, torch.bfloat16
+    _tensor("x", x, (M, K), bf)
+    _tensor("w", w, (V, K), bf, dev)
+    _tensor("targets", targets, (M,), torch.int32, dev)
+    if row_weight is not None:
+        _tensor("row_weight", row_weight, (M,), torch.float32, dev)
+    with _on(dev, stream):
+        loss, lse = (torch.empty(M, dtype=torch.float32, device=dev) for _ in range(2))
+        dx = torch.empty((M, K), dtype=bf, device=dev) if want_grad else None
+        dw = torch.empty((V, K), dtype=bf, device=dev) if want_grad else None
+        if M:
+            wsb = mx_bf16_xent_workspace_size(M, V, K, want_grad)
+            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+            mx_bf16_xent(x, w, targets, row_weight, M, V, K, loss, lse, dx, dw, ws, wsb, stream)
+        elif want_grad:   # empty tensors have no storage to pass
+            dw.zero_()
+    return loss, lse, dx, dw
 
 
 def adamw_state(param, state_bits=32):

@@ -1,0 +1,487 @@
+// The tiled bf16 product behind the dense product, its backward and the cross
+// entropy (gfx950): C[i, j] = sum_c A(i, c) B(j, c), each operand stored either
+// with c contiguous ("rows") or with i or j contiguous ("columns").  Tiles of 64
+// c come into LDS by LDS-direct loads in their stored layout.  Rows are read as
+// fragments with 16-byte LDS reads, columns with the transposing reads
+// (ds_read_b64_tr_b16), so no operand is ever transposed in memory.
+//
+// Sums are fp32 in a fixed order; where the tiles are too few for the card the
+// contraction is split over workgroups, whose fp32 partial sums are added in
+// order by a second launch with the same epilogue.
+//
+// What becomes of the sums is an epilogue's matter, a class E with
+//   struct Args;                     passed by value to the kernels
+//   template <int TM, int TN, typename Sums>
+//   static void run(const Args&, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0, int64_t j0, int64_t I,
+//                   int64_t J, Sums sums);
+// run() gets a wave's TM x TN sums at (i0, j0) of the I x J result and an LDS
+// slice of kStageBytes<TN> of its own, and calls sums() once before it reads
+// them.  Lane l, register r of acc[m][n] holds row i0 + 32 m + (l & 31), column
+// j0 + 32 n + 8 (r >> 2) + 4 (l >> 5) + (r & 3).
+#pragma once
+
+#include "stream.h"
+
+namespace mx {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kXcds = 8;
+
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;        // elements between stored rows
+};
+
+template <class Args>
+struct Product {
+  Operand a, b;
+  int64_t I, J, C;       // rows and columns of the result, contraction length
+  int32_t tiles_i, tiles_j;
+  int32_t full;          // tiles computed whole; the others are split over the contraction
+  int32_t splits;
+  int32_t split_c;       // contraction elements per split (a multiple of 64)
+  float* part;           // fp32 sums of the split tiles [splits, tiles - full, BM x BN in register order]
+  Args epi;              // of the epilogue
+};
+
+// The q-th tile: bands of 8 row tiles, so that tiles that run together share
+// operands in an XCD's L2.
+template <class Args>
+__device__ __forceinline__ void tile_at(const Product<Args>& p, int32_t q, int bm, int bn, int64_t& i0, int64_t& j0) {
+  constexpr int kBand = 8;
+  const int32_t band = q / (kBand * p.tiles_j), in = q % (kBand * p.tiles_j);
+  const int32_t rows = p.tiles_i - band * kBand < kBand ? p.tiles_i - band * kBand : kBand;
+  i0 = (int64_t)(band * kBand + in % rows) * bm;
+  j0 = (int64_t)(in / rows) * bn;
+}
+
+// A barrier that waits for nothing by itself (a fence's wait would include
+// loads still in flight); nothing may be moved across it.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Swizzles of 16-byte chunks.  Rows: 128-byte LDS rows, chunk ^ (r >> 1) & 7,
+// so the 16-byte reads of 32 consecutive rows spread over all banks.  Columns:
+// an LDS row is one c with R columns; a transposing read takes 64 bytes of 4
+// consecutive c at once, which the swizzle moves to different 64-byte banks.
+template <int kC>
+__device__ __forceinline__ int row_swizzle(int r) { return kC == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
+template <int R>
+__device__ __forceinline__ int col_swizzle(int c) { return R >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2; }
+
+// The LDS-direct loads of one operand tile: kLoads per wave and 64-c tile.
+template <bool kRows, int R, int kNw, int kC>
+struct TileLoads {
+  static constexpr int kLoads = R * kC * 2 / 1024 / kNw;
+  static_assert(R * kC * 2 % (1024 * kNw) == 0, "whole loads per wave");
+  uint32_t voff[kLoads];
+  int32_t kc;   // rows: the lane's first c in a tile
+  const uint8_t* base;
+  int64_t bytes, step;
+
+  // first: the tile's first row (i or j), n: rows of the operand, C: contraction length
+  __device__ void init(const Operand& o, int64_t first, int64_t n, int64_t C) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (kRows) {
+      const int64_t rows = n - first < R ? n - first : R;
+      base = reinterpret_cast<const uint8_t*>(o.p + first * o.ld);
+      bytes = rows * o.ld * 2;
+      step = 0;
+      kc = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        constexpr int kPer = kC / 8;         // chunks per LDS row
+        const int r = 64 / kPer * (w + kNw * i) + lane / kPer;
+        const int ch = (lane % kPer) ^ row_swizzle<kC>(r);
+        kc = 8 * ch;   // the same for every i (kNw is even)
+        voff[i] = (uint32_t)r * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch;
+      }
+    } else {
+      base = reinterpret_cast<const uint8_t*>(o.p + first);
+      bytes = C * o.ld * 2 - first * 2;
+      step = kC * o.ld * 2;
+      kc = 0;
+      constexpr int kPer = R / 8;          // chunks per LDS row
+      constexpr int kRowsPer = 64 / kPer;  // LDS rows of one load
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int c = kRowsPer * (w + kNw * i) + lane / kPer;
+        const int ch = (lane % kPer) ^ col_swizzle<R>(c);
+        // columns past the operand's are other rows' data, or past the end: masked
+        voff[i] = first + 8 * ch < n ? (uint32_t)c * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch : kOob;
+      }
+    }
+  }
+
+  // The loads of a tile: prepare() once per tile, then load(i).
+  struct Tile {
+    v4u r;
+    uint32_t soff;
+    bool ok;
+  };
+  __device__ Tile prepare(int64_t tile, int64_t C) const {
+    Tile t;
+    if constexpr (kRows) {
+      t.r = rsrc(base, bytes);
+      t.soff = (uint32_t)(tile * kC * 2);
+      t.ok = tile * kC + kc < C;
+    } else {
+      t.r = rsrc(base + tile * step, bytes - tile * step);
+      t.soff = 0;
+      t.ok = true;
+    }
+    return t;
+  }
+  template <bool kOnce>
+  __device__ void load(const Tile& t, int i, uint32_t lds) const {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t to = lds + 1024u * (uint32_t)(w + kNw * i), from = kRows && !t.ok ? kOob : voff[i];
+    if constexpr (kOnce) dma16_nt(t.r, to, from, t.soff);
+    else dma16(t.r, to, from, t.soff);
+  }
+};
+
+// Lane offsets of a 32 (i) x 16 (c) fragment; kk = 0..3 in a 64-c tile.
+template <bool kRows, int R, int kC>
+struct FragAt {
+  int row, sw, lo, hi;
+  __device__ void init() {
+    const int lane = threadIdx.x & 63;
+    if constexpr (kRows) {
+      row = (lane & 31) * (2 * kC);
+      sw = row_swizzle<kC>(lane & 31);
+      lo = lane >> 5;
+    } else {
+      const int l = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
+      const int c = 8 * h + (l >> 2);
+      row = c * (2 * R);
+      sw = col_swizzle<R>(c);
+      lo = 2 * half + ((l & 3) >> 1);   // 16-byte chunk inside the fragment's 32 columns
+      hi = 8 * (l & 1);
+    }
+  }
+  // i0: the fragment's first row inside the tile, a multiple of 32
+  __device__ v8bf read(const uint8_t* tile, int i0, int kk) const {
+    if constexpr (kRows) {
+      return *reinterpret_cast<const v8bf*>(tile + i0 * (2 * kC) + row + 16 * ((2 * kk + lo) ^ sw));
+    } else {
+      const uint8_t* p = tile + kk * 16 * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
+      // c .. c + 3 and c + 4 .. c + 7: the swizzle depends on c & 3 only
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * R));
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+// A wave's LDS slice of the epilogue: 32 rows of fp32 sums, at most 64 columns at a time.
+template <int TN>
+constexpr int kStageCols = TN < 64 ? TN : 64;
+template <int TN>
+constexpr int kStageBytes = 32 * (kStageCols<TN> * 4 + 16);
+
+// The operand whose every element one workgroup alone reads (the other has one
+// row of tiles): its loads are non-temporal.
+enum { kOnceNone, kOnceA, kOnceB };
+
+// BM x BN result tile, kWm x kWn waves, kSlots LDS tiles of kC contraction
+// elements in flight.
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, class E, int kOnce>
+__global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::Args> p) {
+  constexpr int kNw = kWm * kWn;
+  constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
+  constexpr int kABytes = BM * kC * 2, kSlot = (BM + BN) * kC * 2;
+  constexpr int kLds = kSlots * kSlot > kNw * kStageBytes<TN> ? kSlots * kSlot : kNw * kStageBytes<TN>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / kWn, wn = wave % kWn;
+
+  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous range of the
+  // whole tiles, then one of the split tiles' parts.
+  const int32_t tiles = p.tiles_i * p.tiles_j, tail = tiles - p.full;
+  const int32_t full8 = (p.full + kXcds - 1) / kXcds * kXcds;
+  const bool whole = (int32_t)blockIdx.x < full8;
+  const int32_t bid = whole ? blockIdx.x : blockIdx.x - full8;
+  const int32_t total = whole ? p.full : tail * p.splits;
+  const int32_t per = (total + kXcds - 1) / kXcds;
+  const int32_t L = (bid % kXcds) * per + bid / kXcds;
+  if (bid / kXcds >= per || L >= total) return;
+  const int32_t split = whole ? 0 : L / tail;
+  int64_t i0, j0;
+  tile_at(p, whole ? L : p.full + L % tail, BM, BN, i0, j0);
+  const int64_t all = (p.C + kC - 1) / kC;
+  const int64_t t0 = whole ? 0 : (int64_t)split * (p.split_c / kC);
+  const int64_t t1 = whole || t0 + p.split_c / kC > all ? all : t0 + p.split_c / kC;
+
+  TileLoads<kARows, BM, kNw, kC> la;
+  TileLoads<kBRows, BN, kNw, kC> lb;
+  la.init(p.a, i0, p.I, p.C);
+  lb.init(p.b, j0, p.J, p.C);
+  constexpr int kLoads = TileLoads<kARows, BM, kNw, kC>::kLoads + TileLoads<kBRows, BN, kNw, kC>::kLoads;
+  const uint32_t base = (uint32_t)(uintptr_t)(const lds_void*)lds;
+  FragAt<kARows, BM, kC> fa;
+  FragAt<kBRows, BN, kC> fb;
+  fa.init();
+  fb.init();
+
+  v16f acc[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
+
+  // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.
+  constexpr int kLa = decltype(la)::kLoads;
+  typename decltype(la)::Tile ta;
+  typename decltype(lb)::Tile tb;
+  uint32_t dst = 0;
+  auto load = [&](int i) {   // load i of the tile in hand
+    if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, dst);
+    else lb.template load<kOnce == kOnceB>(tb, i - kLa, dst + kABytes);
+  };
+  auto hand = [&](int64_t t, int s) {
+    ta = la.prepare(t, p.C);
+    tb = lb.prepare(t, p.C);
+    dst = base + (uint32_t)s * kSlot;
+  };
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s)
+    if (t0 + s < t1) {
+      hand(t0 + s, s);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(i);
+    }
+  if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
+  else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  bare_barrier();
+
+  // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
+  // are read during the part before it, and the loads into the slot that the
+  // last tile left are spread over a tile's parts, all placed between the
+  // products: a burst of either stalls the products behind it.
+  constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
+  // with two slots a tile has one tile's time to arrive: its loads all go into the first part
+  constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
+  v8bf a[2][FM], b[2][FN];
+  // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
+  auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
+#pragma unroll
+    for (int i = 0; i < kMfma; ++i) {
+      const int m = i / FN, n = i % FN;
+      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[q][n], a[q][m], acc[m][n], 0, 0, 0);
+#pragma unroll
+      for (int f = i * kFrags / kMfma; f < (i + 1) * kFrags / kMfma; ++f) {
+        if (f < FN) b[1 - q][f] = fb.read(tile + kABytes, wn * TN + 32 * f, kk);
+        else a[1 - q][f - FN] = fa.read(tile, wm * TM + 32 * (f - FN), kk);
+      }
+      if (fill) {
+#pragma unroll
+        for (int l = i * kPerPart / kMfma; l < (i + 1) * kPerPart / kMfma; ++l)
+          if (first + l < kLoads) load(first + l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+#pragma unroll
+  for (int n = 0; n < FN; ++n) b[0][n] = fb.read(lds + kABytes, wn * TN + 32 * n, 0);
+#pragma unroll
+  for (int m = 0; m < FM; ++m) a[0][m] = fa.read(lds, wm * TM + 32 * m, 0);
+  int slot = 0;
+  bool fill = false;   // whether the tile in hand is loaded
+  for (int64_t t = t0; t < t1; ++t) {
+    const uint8_t* tile = lds + slot * kSlot;
+    const int next = slot + 1 == kSlots ? 0 : slot + 1;
+#pragma unroll
+    for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, kk, fill, kk * kPerPart);
+    // this wave has read its share of the slot, and its loads of tile t + 1
+    // are done (the kSlots - 2 tiles after it may be in flight; near the end
+    // fewer are, so everything is waited for) ...
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+    if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    // ... and after the barrier every wave's: the slot takes tile t + kSlots
+    bare_barrier();
+    fill = t + kSlots < t1;
+    hand(t + kSlots, slot);
+    // (after the last tile this reads an old slot, which is not used)
+    part(1, lds + next * kSlot, 0, fill, 0);
+    slot = next;
+  }
+  __syncthreads();
+
+  if (!whole) {
+    float4* o = reinterpret_cast<float4*>(p.part) + (int64_t)L * (BM * BN / 4) + wave * (TM * TN / 4) + lane;
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          o[((m * FN + n) * 4 + g) * 64] =
+              make_float4(acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2], acc[m][n][4 * g + 3]);
+    return;
+  }
+  E::template run<TM, TN>(p.epi, acc, lds + wave * kStageBytes<TN>, i0 + wm * TM, j0 + wn * TN, p.I, p.J, [] {});
+}
+// The split tiles: one wave per 32 rows of a wave's share of a tile adds the
+// partial sums in the splits' order, then the epilogue.
+template <int BM, int BN, int kWm, int kWn, class E>
+__global__ void __launch_bounds__(64) k_join(Product<typename E::Args> p) {
+  constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t slice[kStageBytes<TN>];
+  const int32_t tail = p.tiles_i * p.tiles_j - p.full;
+  const int32_t t = blockIdx.x / (kWm * kWn * FM), in = blockIdx.x % (kWm * kWn * FM);
+  const int32_t wave = in / FM, m = in % FM;
+  int64_t i0, j0;
+  tile_at(p, p.full + t, BM, BN, i0, j0);
+  v16f acc[1][FN];
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[0][n][r] = 0.f;
+  const float4* o = reinterpret_cast<const float4*>(p.part) + (int64_t)t * (BM * BN / 4) + wave * (TM * TN / 4) +
+                    m * (FN * 256) + threadIdx.x;
+  auto sums = [&] {
+#pragma unroll 2
+    for (int s = 0; s < p.splits; ++s, o += (int64_t)tail * (BM * BN / 4)) {
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 v = o[(n * 4 + g) * 64];
+          acc[0][n][4 * g] += v.x;
+          acc[0][n][4 * g + 1] += v.y;
+          acc[0][n][4 * g + 2] += v.z;
+          acc[0][n][4 * g + 3] += v.w;
+        }
+    }
+  };
+  E::template run<32, TN>(p.epi, acc, slice, i0 + wave / kWn * TM + 32 * m, j0 + wave % kWn * TN, p.I, p.J, sums);
+}
+// ---------------------------------------------------------------- host side
+constexpr int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// Tile shapes.
+enum Shape { k256x256, k128x128, k128x64, k64x128, k64x64, kShapes };
+constexpr struct {
+  int bm, bn, per_cu;   // workgroups per CU (LDS)
+  double us;            // microseconds per 64 c of a round with all slots busy and operands in L2
+  double stream;        // bytes per microsecond at which it streams operands that are read once
+} kShape[kShapes] = {
+    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
+    {128, 128, 2, 1.13, 4.9e6},
+    {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 107 with 128 x 128
+    {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
+    {64, 64, 2, 0.50, 4.0e6}};    // 1000 x 1408 x 2048: 18 us, against 22 to 23 with the others
+
+// Tile and split of a product.  Tiles run in rounds of `slots` workgroups; the
+// tiles of the last, partly filled round are split over the contraction so
+// that it is filled.
+struct Plan {
+  int shape;
+  int32_t full, splits, split_c;
+  int64_t part_bytes;
+};
+
+Plan plan_product(int64_t I, int64_t J, int64_t C) {
+  const int64_t all = (C + 63) / 64;
+  Plan best{};
+  double least = 1e30;
+  for (int id = 0; id < kShapes; ++id) {
+    const auto& sh = kShape[id];
+    const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn, t = ti * tj;
+    const int64_t slots = sh.per_cu * kCus, rounds = t / slots, rem = t - rounds * slots;
+    int64_t s = rem ? slots / rem : 1;
+    if (s > all / 8) s = all / 8;     // at least 512 c per split
+    if (s < 1) s = 1;
+    const int64_t per = all ? (all + s - 1) / s : 1;
+    s = all ? (all + per - 1) / per : 1;
+    double us = sh.us * ((double)rounds * all + (rem ? (double)per : 0.0)) + 3.0 * (rounds + (rem != 0));
+    if (us < 2.0 * C * (I + J) / sh.stream) us = 2.0 * C * (I + J) / sh.stream;
+    const double part = 4.0 * s * rem * sh.bm * sh.bn;
+    if (s > 1) us += 4.0 + 2.0 * part / 4e6;   // the join's launch, its bytes at 4 TB/s
+    if (us < least) {
+      least = us;
+      best.shape = id;
+      best.full = (int32_t)(s > 1 ? rounds * slots : t);
+      best.splits = (int32_t)s;
+      best.split_c = (int32_t)(64 * per);
+      best.part_bytes = s > 1 ? (int64_t)part : 0;
+    }
+  }
+  return best;
+}
+// Whether a product's launch stays below 2^32 threads (the split tiles' parts are at most 2 kCus workgroups).
+bool tiles_fit(int64_t I, int64_t J, int64_t C) {
+  const int shape = plan_product(I, J, C).shape;
+  const int64_t tiles = (I + kShape[shape].bm - 1) / kShape[shape].bm * ((J + kShape[shape].bn - 1) / kShape[shape].bn);
+  return (tiles + 4 * kCus) * (shape == k256x256 ? 512 : 256) < (1ll << 32);
+}
+
+template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, class E, int kOnce = kOnceNone>
+void launch_shape(const Product<typename E::Args>& p, hipStream_t st) {
+  auto up8 = [](int32_t v) { return (v + kXcds - 1) / kXcds * kXcds; };
+  const int32_t tail = p.tiles_i * p.tiles_j - p.full;
+  const dim3 grid((unsigned)(up8(p.full) + up8(tail * p.splits)));
+  hipLaunchKernelGGL((k_product<BM, BN, kWm, kWn, kC, kSlots, kARows, kBRows, E, kOnce>), grid, dim3(64 * kWm * kWn), 0, st, p);
+  if (tail)
+    hipLaunchKernelGGL((k_join<BM, BN, kWm, kWn, E>), dim3((unsigned)(BM / 32 * kWn * tail)), dim3(64), 0, st, p);
+}
+
+// A narrow tile's launch.
+template <int BM, int BN, int kSlots, bool kARows, bool kBRows, class E>
+void launch_narrow(const Product<typename E::Args>& p, hipStream_t st) {
+  if (p.tiles_j == 1) launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, E, kOnceA>(p, st);
+  else if (p.tiles_i == 1) launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, E, kOnceB>(p, st);
+  else launch_shape<BM, BN, 2, 2, 64, kSlots, kARows, kBRows, E>(p, st);
+}
+// The product of A [I, C] and B [J, C] with the epilogue E; part: plan_product(I, J, C).part_bytes.
+template <bool kARows, bool kBRows, class E>
+int launch_tiles(const Operand& a, const Operand& b, int64_t I, int64_t J, int64_t C, const typename E::Args& epi, float* part,
+                   hipStream_t st) {
+  Product<typename E::Args> p;
+  p.a = a;
+  p.b = b;
+  p.I = I;
+  p.J = J;
+  p.C = C;
+  p.epi = epi;
+  const Plan pl = plan_product(I, J, C);
+  const auto& sh = kShape[pl.shape];
+  const int64_t ti = (I + sh.bm - 1) / sh.bm, tj = (J + sh.bn - 1) / sh.bn;
+  p.tiles_i = (int32_t)ti;
+  p.tiles_j = (int32_t)tj;
+  p.full = pl.full;
+  p.splits = pl.splits;
+  p.split_c = pl.split_c;
+  p.part = part;
+  switch (pl.shape) {
+    case k256x256: launch_shape<256, 256, 2, 4, 64, 2, kARows, kBRows, E>(p, st); break;
+    case k128x128: launch_shape<128, 128, 2, 2, 64, 2, kARows, kBRows, E>(p, st); break;
+    case k128x64: launch_narrow<128, 64, 5, kARows, kBRows, E>(p, st); break;
+    case k64x128: launch_narrow<64, 128, 5, kARows, kBRows, E>(p, st); break;
+    default: launch_narrow<64, 64, 4, kARows, kBRows, E>(p, st); break;
+  }
+  return launch_status();
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// Sizes the 32-bit offsets of the tiles allow (256 rows of an operand below 2^31 bytes).
+bool too_large(int64_t rows, int64_t n, int64_t k) {
+  return k >= (1 << 21) || n >= (1 << 21) || rows >= (1ll << 31);
+}
+
+}  // namespace
+}  // namespace mx

@@ -1,0 +1,385 @@
+// Softmax cross entropy over a large vocabulary, from the hidden rows and the
+// output weights, with its gradient (gfx950):
+//
+//   z = x w^T,  lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_{i, t_i}
+//   dz = g_i (softmax(z_i) - onehot(t_i)),  dx = dz w,  dw = dz^T x
+//
+// The logits are never kept.  The product's epilogue reduces a wave's columns of
+// a row to their largest value m and the sum of exp(z - m) (a strip of 32 or 64
+// columns); a second launch joins a row's strips.  For the gradient the epilogue
+// also leaves exp(z - m) of a chunk of rows in fp16: a value in [0, 1] to 11
+// bits (2^-12 of it, or 2^-25 of the strip's largest), an eighth of what dz is
+// rounded by afterwards, so that a second product of the logits (a quarter of
+// all the work) is saved and dz = g (exp(z - m) exp(m - lse) - onehot) is rounded
+// to bf16, the matrix instruction's operand, once.  Chunks bound the workspace;
+// with several, dw is added up in fp32.
+//
+// The products run in the tiles of product.h.  Everything is added in a fixed
+// order: repeated calls give the same bits.
+
+#include "product.h"
+
+namespace mx {
+namespace {
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }   // x <= 0
+
+__device__ __forceinline__ uint32_t half2_rne(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2h));
+}
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+
+struct XentArgs {
+  const int32_t* targets;   // [I]
+  float2* part;             // [strips, I]: a strip's largest logit and sum of exponentials
+  float* zt;                // [I]: the target's logit
+  uint16_t* e;              // fp16 [I, pitch]: exp(z - m)
+  int64_t pitch;            // J rounded up to 8: the columns past J are zeros
+};
+
+template <bool kGrad>
+struct XentEpi {
+  typedef XentArgs Args;
+  template <int TM, int TN, typename Sums>
+  __device__ static __forceinline__ void run(const XentArgs& p, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
+                                             int64_t j0, int64_t I, int64_t J, Sums sums) {
+    constexpr int FM = TM / 32, FN = TN / 32, kPitch = 2 * TN + 16;
+    static_assert(32 * kPitch <= kStageBytes<TN>, "the slice holds 32 rows of fp16");
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    sums();
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      const int64_t i = i0 + 32 * m + (lane & 31);
+      float z[FN * 16];
+#pragma unroll
+      for (int r = 0; r < FN * 16; ++r) z[r] = acc[m][r / 16][r % 16];
+      // the lane's column of register r: j0 + at(r) + 4 h
+      auto at = [](int r) { return 32 * (r / 16) + 8 * (r % 16 / 4) + r % 4; };
+      if (j0 + TN > J) {
+#pragma unroll
+        for (int r = 0; r < FN * 16; ++r)
+          if (j0 + at(r) + 4 * h >= J) z[r] = -INFINITY;
+      }
+      float top = z[0];
+#pragma unroll
+      for (int r = 1; r < FN * 16; ++r) top = fmaxf(top, z[r]);
+      top = fmaxf(top, other_half(top));
+      const int64_t t = i < I ? p.targets[i] : -1;
+      const int32_t rel = t >= j0 && t < J && t - j0 < TN ? (int32_t)(t - j0) : -1;   // the target's column, if it is here
+      if (__any(rel >= 0)) {
+#pragma unroll
+        for (int r = 0; r < FN * 16; ++r)
+          if (rel == at(r) + 4 * h) p.zt[i] = z[r];
+      }
+      const float ref = top == -INFINITY ? 0.0f : top;   // (a strip of nothing: exponentials of zero)
+#pragma unroll
+      for (int r = 0; r < FN * 16; ++r) z[r] = exp_of(z[r] - ref);
+      if constexpr (kGrad) {
+#pragma unroll
+        for (int g = 0; g < FN * 4; ++g)
+          *reinterpret_cast<uint2*>(slice + (lane & 31) * kPitch + 2 * (at(4 * g) + 4 * h)) =
+              make_uint2(half2_rne(z[4 * g], z[4 * g + 1]), half2_rne(z[4 * g + 2], z[4 * g + 3]));
+        asm volatile("" ::: "memory");   // exchanged between the wave's lanes, whose LDS accesses run in order
+        constexpr int kLpr = TN / 8, kRpp = 64 / kLpr;
+#pragma unroll
+        for (int it = 0; it < 32 / kRpp; ++it) {
+          const int row = kRpp * it + lane / kLpr, c = 8 * (lane % kLpr);
+          const uint4 v = *reinterpret_cast<const uint4*>(slice + row * kPitch + 2 * c);
+          const int64_t ri = i0 + 32 * m + row;
+          if (ri < I && j0 + c < p.pitch) *reinterpret_cast<uint4*>(p.e + ri * p.pitch + j0 + c) = v;
+        }
+        asm volatile("" ::: "memory");
+      }
+#pragma unroll
+      for (int w = FN * 8; w > 0; w /= 2)
+#pragma unroll
+        for (int r = 0; r < w; ++r) z[r] += z[r + w];
+      const float s = z[0] + other_half(z[0]);
+      if (h == 0 && i < I) p.part[j0 / TN * I + i] = make_float2(top, s);
+      __builtin_amdgcn_sched_barrier(0);   // 32 rows at a time: interleaved, they do not fit the registers
+    }
+  }
+};
+
+// Joins a row's strips: 16 rows per workgroup, 16 threads to a row, each every
+// 16th strip in order, then the threads' sums in order.
+__global__ void __launch_bounds__(256) k_xent_join(const float2* __restrict__ part, int64_t rows, int32_t strips,
+                                                   const int32_t* __restrict__ targets, int64_t vocab,
+                                                   const float* __restrict__ zt, float* __restrict__ lse,
+                                                   float* __restrict__ lse_out, float* __restrict__ loss) {
+  __shared__ float2 sum[16][17];
+  const int rl = threadIdx.x & 15, sl = threadIdx.x >> 4;
+  const int64_t i = 16 * (int64_t)blockIdx.x + rl;
+  float m = -INFINITY, s = 0.0f;
+  auto add = [&](const float2& v) {
+    if (v.y == 0.0f) return;   // nothing in it (a NaN is something)
+    const float n = fmaxf(m, v.x);
+    s = (s == 0.0f ? 0.0f : s * exp_of(m - n)) + v.y * exp_of(v.x - n);
+    m = n;
+  };
+  if (i < rows) {
+#pragma unroll 4
+    for (int32_t k = sl; k < strips; k += 16) add(part[(int64_t)k * rows + i]);
+  }
+  sum[sl][rl] = make_float2(m, s);
+  __syncthreads();
+  if (sl > 0 || i >= rows) return;
+  for (int k = 1; k < 16; ++k) add(sum[k][rl]);
+  const float l = m + logf(s);
+  const int32_t t = targets[i];
+  if (lse) lse[i] = l;
+  if (lse_out) lse_out[i] = l;
+  if (loss) loss[i] = t >= 0 && t < vocab ? l - zt[i] : 0.0f;
+}
+
+// dz in place of the exponentials: a thread takes 8 columns of a row in each of
+// kDzStrips strips.  Rows without a target are zeros whatever they held.
+constexpr int kDzStrips = 8;
+
+template <int TN>
+__global__ void __launch_bounds__(256) k_xent_dz(const float2* __restrict__ part, const float* __restrict__ lse,
+                                                 const int32_t* __restrict__ targets,
+                                                 const float* __restrict__ row_weight, int64_t rows, int64_t vocab,
+                                                 int64_t pitch, uint32_t blocks_j, uint16_t* __restrict__ e) {
+  constexpr int kLpr = TN / 8, kRows = 256 / kLpr;
+  const int64_t i = (int64_t)(blockIdx.x / blocks_j) * kRows + threadIdx.x / kLpr;
+  if (i >= rows) return;
+  const int32_t t = targets[i];
+  const bool live = t >= 0 && t < vocab;
+  const float g = row_weight ? row_weight[i] : 1.0f, l = lse[i];
+  const int32_t s0 = (int32_t)(blockIdx.x % blocks_j) * kDzStrips;
+  uint4 v[kDzStrips];
+  float m[kDzStrips];
+#pragma unroll
+  for (int s = 0; s < kDzStrips; ++s) {
+    const int64_t c = (int64_t)(s0 + s) * TN + 8 * (threadIdx.x % kLpr);
+    if (c < pitch) {
+      v[s] = *reinterpret_cast<const uint4*>(e + i * pitch + c);
+      m[s] = part[(int64_t)(s0 + s) * rows + i].x;
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kDzStrips; ++s) {
+    const int64_t c = (int64_t)(s0 + s) * TN + 8 * (threadIdx.x % kLpr);
+    if (c >= pitch) break;
+    const float f = g * exp_of(m[s] - l);
+    const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const v2h x = __builtin_bit_cast(v2h, w[k]);
+      float lo = (float)x[0] * f, hi = (float)x[1] * f;
+      if (c + 2 * k == t) lo -= g;
+      if (c + 2 * k + 1 == t) hi -= g;
+      o[k] = live ? bf16x2_rne(lo, hi) : 0u;
+    }
+    *reinterpret_cast<uint4*>(e + i * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// x with zeros in the rows without a target: what they hold, infinities and NaN
+// among it, must not reach dw (their dz is zero, which does not hide them).
+__global__ void __launch_bounds__(256) k_live_rows(const uint16_t* __restrict__ x, const int32_t* __restrict__ targets,
+                                                   int64_t rows, int64_t vocab, int64_t k, uint16_t* __restrict__ out) {
+  const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (at >= rows * k) return;
+  const int32_t t = targets[at / k];
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (t >= 0 && t < vocab) v = *reinterpret_cast<const uint4*>(x + at);
+  *reinterpret_cast<uint4*>(out + at) = v;
+}
+
+// The gradients' epilogue: out = add + sums, in bf16 or fp32.  J % 8 == 0.
+struct SumArgs {
+  const float* add;   // fp32 [I, J] or null
+  void* out;          // [I, J] (fp32: may be add)
+  bool f32;
+};
+
+struct SumEpi {
+  typedef SumArgs Args;
+  template <int TM, int TN, typename Sums>
+  __device__ static __forceinline__ void run(const SumArgs& p, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
+                                             int64_t j0, int64_t I, int64_t J, Sums sums) {
+    constexpr int W = kStageCols<TN>, kPitch = W * 4 + 16, kLpr = W / 8, kRpp = 64 / kLpr;
+    const int lane = threadIdx.x & 63;
+    sums();
+#pragma unroll
+    for (int n0 = 0; n0 < TN / 32; n0 += W / 32) {
+      const int64_t j = j0 + 32 * n0 + 8 * (lane % kLpr);
+#pragma unroll
+      for (int m = 0; m < TM / 32; ++m) {
+#pragma unroll
+        for (int n = 0; n < W / 32; ++n)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const v16f& a = acc[m][n0 + n];
+            *reinterpret_cast<float4*>(slice + (lane & 31) * kPitch + (32 * n + 8 * g + 4 * (lane >> 5)) * 4) =
+                make_float4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]);
+          }
+        asm volatile("" ::: "memory");   // exchanged between the wave's lanes, whose LDS accesses run in order
+#pragma unroll
+        for (int it = 0; it < 32 / kRpp; ++it) {
+          const int row = kRpp * it + lane / kLpr;
+          float4 x = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * (lane % kLpr));
+          float4 y = *reinterpret_cast<const float4*>(slice + row * kPitch + 32 * (lane % kLpr) + 16);
+          const int64_t i = i0 + 32 * m + row;
+          if (i >= I || j >= J) continue;
+          const int64_t o = i * J + j;
+          if (p.add) {
+            const float4 a = *reinterpret_cast<const float4*>(p.add + o), b = *reinterpret_cast<const float4*>(p.add + o + 4);
+            x = make_float4(x.x + a.x, x.y + a.y, x.z + a.z, x.w + a.w);
+            y = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);
+          }
+          if (p.f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = x;
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o + 4) = y;
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) =
+                make_uint4(bf16x2_rne(x.x, x.y), bf16x2_rne(x.z, x.w), bf16x2_rne(y.x, y.y), bf16x2_rne(y.z, y.w));
+          }
+        }
+        asm volatile("" ::: "memory");
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- host side
+// Columns of a wave in a tile shape.
+int strip_cols(int shape) { return kShape[shape].bn >= 128 ? 64 : 32; }
+
+int32_t strips_of(int64_t rows, int64_t vocab, int64_t k) {
+  const int shape = plan_product(rows, vocab, k).shape;
+  const int bn = kShape[shape].bn;
+  return (int32_t)((vocab + bn - 1) / bn * (bn / strip_cols(shape)));
+}
+
+// Rows that are in work together: their exponentials and their copies of x
+// (without a gradient: the strips' sums) take 2 GiB at most.
+int64_t chunk_rows(int64_t rows, int64_t vocab, int64_t k, bool grad) {
+  const int64_t row_bytes = grad ? 2 * (vocab > k ? up(vocab, 8) : k) : (vocab + 255) / 256 * 8 * 8;
+  int64_t most = (2ll << 30) / row_bytes / 256 * 256;
+  if (most < 256) most = 256;
+  if (rows <= most) return rows;
+  const int64_t chunks = (rows + most - 1) / most;
+  return up((rows + chunks - 1) / chunks, 256);
+}
+
+// Sections of the workspace.
+struct XentSpace {
+  int64_t chunk, pitch;
+  int64_t e, part, row, x, acc, prod;   // bytes; row: of one float per row
+};
+
+XentSpace xent_space(int64_t rows, int64_t vocab, int64_t k, bool grad) {
+  XentSpace s{};
+  s.chunk = chunk_rows(rows, vocab, k, grad);
+  s.pitch = up(vocab, 8);
+  const int64_t last = rows % s.chunk ? rows % s.chunk : s.chunk;
+  for (const int64_t r : {s.chunk, last}) {
+    const int64_t part = up(8 * (int64_t)strips_of(r, vocab, k) * r, 256);
+    if (part > s.part) s.part = part;
+    int64_t prod = plan_product(r, vocab, k).part_bytes;
+    if (grad) {
+      const int64_t a = plan_product(r, k, vocab).part_bytes, b = plan_product(vocab, k, r).part_bytes;
+      prod = prod > a ? prod : a;
+      prod = prod > b ? prod : b;
+    }
+    if (prod > s.prod) s.prod = prod;
+  }
+  s.row = up(4 * s.chunk, 256);
+  if (grad) {
+    s.e = up(2 * s.chunk * s.pitch, 256);
+    s.x = up(2 * s.chunk * k, 256);
+    s.acc = s.chunk < rows ? 4 * vocab * k : 0;
+  }
+  return s;
+}
+
+int64_t total(const XentSpace& s) { return s.e + s.part + 2 * s.row + s.x + s.acc + s.prod; }
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" size_t mx_bf16_xent_workspace_size(int64_t rows, int64_t vocab, int64_t k, int32_t backward) {
+  if (rows <= 0 || vocab <= 0 || k <= 0 || k % 32 || too_large(rows, vocab, k)) return 0;
+  return (size_t)total(xent_space(rows, vocab, k, backward != 0));
+}
+
+extern "C" int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t* targets, const float* row_weight,
+                            int64_t rows, int64_t vocab, int64_t k, float* loss, float* lse, uint16_t* dx, uint16_t* dw,
+                            void* workspace, size_t workspace_bytes, mx_stream_t stream) {
+  if (rows < 0 || vocab <= 0 || k <= 0 || k % 32 || !x || !w || !targets) return MX_EINVAL;
+  if (!loss && !lse && !dx && !dw) return MX_EINVAL;
+  if (misaligned(x) || misaligned(w) || misaligned(dx) || misaligned(dw) || misaligned(workspace)) return MX_EINVAL;
+  if (((uintptr_t)targets | (uintptr_t)row_weight | (uintptr_t)loss | (uintptr_t)lse) & 3) return MX_EINVAL;
+  if (too_large(rows, vocab, k)) return MX_EUNSUPPORTED;
+  const bool grad = dx || dw;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (rows == 0) {
+    if (!dw) return MX_OK;
+    if (!tiles_fit(vocab, k, 0)) return MX_EUNSUPPORTED;
+    return launch_tiles<false, false, SumEpi>(Operand{x, up(vocab, 8)}, Operand{x, k}, vocab, k, 0,
+                                              SumArgs{nullptr, dw, false}, nullptr, st);   // a sum of nothing
+  }
+  const XentSpace s = xent_space(rows, vocab, k, grad);
+  if (!workspace || (int64_t)workspace_bytes < total(s)) return MX_EINVAL;
+  for (int64_t r0 = 0; r0 < rows; r0 += s.chunk) {
+    const int64_t r = rows - r0 < s.chunk ? rows - r0 : s.chunk;
+    if (!tiles_fit(r, vocab, k) || (dx && !tiles_fit(r, k, vocab)) || (dw && !tiles_fit(vocab, k, r))) return MX_EUNSUPPORTED;
+  }
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = at;
+    at += bytes;
+    return p;
+  };
+  uint16_t* e = reinterpret_cast<uint16_t*>(take(s.e));
+  float2* part = reinterpret_cast<float2*>(take(s.part));
+  float* zt = reinterpret_cast<float*>(take(s.row));
+  float* own_lse = reinterpret_cast<float*>(take(s.row));
+  uint16_t* xl = reinterpret_cast<uint16_t*>(take(s.x));
+  float* acc = reinterpret_cast<float*>(take(s.acc));
+  float* prod = reinterpret_cast<float*>(take(s.prod));
+
+  for (int64_t r0 = 0; r0 < rows; r0 += s.chunk) {
+    const int64_t r = rows - r0 < s.chunk ? rows - r0 : s.chunk;
+    const uint16_t* xr = x + r0 * k;
+    const int32_t* tr = targets + r0;
+    const XentArgs a{tr, part, zt, e, s.pitch};
+    const Operand ox{xr, k}, ow{w, k};
+    int rc = grad ? launch_tiles<true, true, XentEpi<true>>(ox, ow, r, vocab, k, a, prod, st)
+                  : launch_tiles<true, true, XentEpi<false>>(ox, ow, r, vocab, k, a, prod, st);
+    if (rc != MX_OK) return rc;
+    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((r + 15) / 16)), dim3(256), 0, st, part, r,
+                       strips_of(r, vocab, k), tr, vocab, zt, grad ? own_lse : nullptr, lse ? lse + r0 : nullptr,
+                       loss ? loss + r0 : nullptr);
+    if (!grad) continue;
+    const int tn = strip_cols(plan_product(r, vocab, k).shape), per = 256 / (tn / 8);
+    const uint32_t bj = (uint32_t)((s.pitch + kDzStrips * tn - 1) / (kDzStrips * tn));
+    const dim3 grid((unsigned)(bj * ((r + per - 1) / per)));
+    const float* rw = row_weight ? row_weight + r0 : nullptr;
+    if (tn == 64) hipLaunchKernelGGL(k_xent_dz<64>, grid, dim3(256), 0, st, part, own_lse, tr, rw, r, vocab, s.pitch, bj, e);
+    else hipLaunchKernelGGL(k_xent_dz<32>, grid, dim3(256), 0, st, part, own_lse, tr, rw, r, vocab, s.pitch, bj, e);
+    const Operand dz{e, s.pitch};
+    if (dx) {
+      rc = launch_tiles<true, false, SumEpi>(dz, ow, r, k, vocab, SumArgs{nullptr, dx + r0 * k, false}, prod, st);
+      if (rc != MX_OK) return rc;
+    }
+    if (dw) {
+      hipLaunchKernelGGL(k_live_rows, dim3((unsigned)((r * k / 8 + 255) / 256)), dim3(256), 0, st, xr, tr, r, vocab, k, xl);
+      const bool last = r0 + r == rows;
+      const SumArgs sum{r0 ? acc : nullptr, last ? static_cast<void*>(dw) : acc, !last};
+      rc = launch_tiles<false, false, SumEpi>(dz, Operand{xl, k}, vocab, k, r, sum, prod, st);
+      if (rc != MX_OK) return rc;
+    }
+  }
+  return launch_status();
+}
