@@ -7,12 +7,13 @@
 //   dr = s (dy w - r s^2 mean(dy w r)) + dsum,  dw = sum_rows dy r s
 //
 // Both are HBM-bound streams: every element is read once, held in registers
-// over the row's reduction, and written once.  G threads share a row, a thread
-// holds N chunks of 8 columns (chunk t + G i), w of its columns in registers
-// over all rows of its workgroup.  Sums are fp32 in a fixed order.
+// over the row's reduction, and written once.  A workgroup takes a row at a
+// time, a thread 8 of its columns (N times 8 above 8192 columns), w of them in
+// registers over all rows.  Sums are fp32 in a fixed order.
 
 #include <type_traits>
 
+#include "stream.h"
 #include "tile_quant.h"
 
 namespace mx {
@@ -34,33 +35,60 @@ __device__ __forceinline__ uint4 narrow(const F8& f) {
                     bf16x2_rne(f.v[6], f.v[7]));
 }
 
-// 8 elements of the residual stream, bf16 or fp32, as they are loaded.
+// A row of a tensor as a buffer: columns past its end load as zeros and are not
+// stored, and a thread keeps one offset per chunk for all rows and tensors (as
+// pointers and predicates these took more registers than the row itself).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* p, int64_t r, int64_t row_bytes, bool ok) {
+  return buf(static_cast<const uint8_t*>(p) + r * row_bytes, ok && p ? row_bytes : 0);
+}
+
+constexpr int kNt = 2;   // non-temporal: rows pass through once
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, kNt));
+}
+
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t b, uint32_t at, const uint4& v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), b, (int)at, 0, kNt);
+}
+
+// Keeps a row's bf16 packed over the reduction: widened before it, they would
+// be held twice as large.
+__device__ __forceinline__ void pin16(uint4& v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+
+// 8 elements of the residual stream, bf16 or fp32, as they are stored; at: the
+// offset of 8 bf16.
 template <bool kF32> struct Raw;
 template <> struct Raw<false> {
   uint4 a;
-  __device__ void load(const void* p, int64_t at) { a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at); }
+  __device__ void load(__amdgpu_buffer_rsrc_t b, uint32_t at) { a = load16(b, at); }
+  __device__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at) const { store16(b, at, a); }
   __device__ F8 value() const { return widen(a); }
+  __device__ void set(const F8& f) { a = narrow(f); }
+  __device__ void pin() { pin16(a); }
 };
 template <> struct Raw<true> {
-  float4 a, b;
-  __device__ void load(const void* p, int64_t at) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    a = f[0];
-    b = f[1];
+  uint4 a, b;
+  __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    a = load16(r, 2 * at);
+    b = load16(r, 2 * at + 16);
   }
-  __device__ F8 value() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+  __device__ void store(__amdgpu_buffer_rsrc_t r, uint32_t at) const {
+    store16(r, 2 * at, a);
+    store16(r, 2 * at + 16, b);
+  }
+  __device__ F8 value() const {
+    F8 f;
+    __builtin_memcpy(f.v, &a, 16);
+    __builtin_memcpy(f.v + 4, &b, 16);
+    return f;
+  }
+  __device__ void set(const F8& f) {
+    __builtin_memcpy(&a, f.v, 16);
+    __builtin_memcpy(&b, f.v + 4, 16);
+  }
+  __device__ void pin() {}
 };
-
-template <bool kF32>
-__device__ __forceinline__ void store_stream(void* p, int64_t at, const F8& f) {
-  if constexpr (kF32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    o[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-    o[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = narrow(f);
-  }
-}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -68,38 +96,41 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Sums over the G threads of a row, the same bits in each of them.  slot: one
-// of two LDS slices in turn, so that one barrier per row is enough.
-template <int G, int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float* slot) {
+// Sums over the workgroup, the same bits in each thread.  slot: one of two LDS
+// slices in turn, so that one barrier per row is enough.
+constexpr int kMaxWaves = 16;
+
+template <int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*slot)[K], int waves) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-  if constexpr (G > 64) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    if (lane == 0) {
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) slot[wave * K + k] = v[k];
-    }
-    __syncthreads();
+    for (int k = 0; k < K; ++k) slot[threadIdx.x >> 6][k] = v[k];
+  }
+  lds_barrier();   // the next row's loads stay in flight
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float t = 0.0f;
+  for (int k = 0; k < K; ++k) v[k] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < G / 64; ++w) t += slot[w * K + k];
-      v[k] = t;
-    }
+  for (int w = 0; w < kMaxWaves; ++w) {   // (waves that are not there left zeros)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += slot[w][k];
   }
 }
 
-template <int G> constexpr int kThreads = G < 256 ? 256 : G;
-template <int G> constexpr int kGroups = kThreads<G> / G;   // rows in work at once
+template <int K>
+__device__ __forceinline__ void clear_slots(float (*slots)[kMaxWaves][K]) {
+  for (int i = threadIdx.x; i < 2 * kMaxWaves * K; i += blockDim.x) reinterpret_cast<float*>(slots)[i] = 0.0f;
+  __syncthreads();
+}
 
-// The columns' weights of a thread's chunks (1 without weights, 0 past the row's end).
-template <int G, int N>
-__device__ __forceinline__ void load_weights(F8 (&w)[N], const float* weight, int t, int64_t cols) {
+// The weights of a thread's chunks (1 without weights, 0 past the row's end).
+template <int N>
+__device__ __forceinline__ void load_weights(F8 (&w)[N], const float* weight, int64_t cols) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int64_t c = 8 * (int64_t)(t + G * i);
+    const int64_t c = 8 * (int64_t)(threadIdx.x + blockDim.x * i);
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[i].v[k] = c < cols ? (weight ? weight[c + k] : 1.0f) : 0.0f;
   }
@@ -115,92 +146,80 @@ struct Norm {
   uint16_t* y;
   uint8_t* row_q;
   uint8_t* row_s;
-  int32_t band;            // rows per workgroup
-  bool staged;             // scales go through LDS
 };
 
-template <int G, int N, bool kF32>
-__global__ void __launch_bounds__(kThreads<G>) k_rmsnorm(const Norm p) {
-  extern __shared__ uint32_t panels[];   // [ceil(cols / 128)][band] panel dwords
-  __shared__ float slots[2][kThreads<G> / 64];
-  const int g = threadIdx.x / G, t = threadIdx.x % G;
-  const int64_t r0 = (int64_t)blockIdx.x * p.band;
-  const int32_t band = p.rows - r0 < p.band ? (int32_t)(p.rows - r0) : p.band;
+// Workgroup b takes rows b, b + gridDim, ...: the card walks through the rows
+// together, the next row on the way while one is finished (two rows ahead
+// measure the same).
+template <int N, bool kF32>
+__global__ void __launch_bounds__(1024) k_rmsnorm(const Norm p) {
+  __shared__ float slots[2][kMaxWaves][1];
+  const int T = blockDim.x, t = threadIdx.x, waves = T >> 6;
+  if (waves > 1) clear_slots(slots);
   F8 w[N];
-  load_weights<G, N>(w, p.weight, t, p.cols);
+  load_weights<N>(w, p.weight, p.cols);
   const float inv_cols = 1.0f / (float)p.cols;
 
-  for (int32_t j = 0; j < band; j += kGroups<G>) {
-    const bool ok = j + g < band;
-    const int64_t r = r0 + j + g;
-    uint4 rx[N];
-    Raw<kF32> rr[N];
+  uint4 rx[N];
+  Raw<kF32> rr[N];
+  auto load = [&](int64_t r) {
+    const bool ok = r < p.rows;
+    const __amdgpu_buffer_rsrc_t bx = row_of(p.x, r, 2 * p.cols, ok);
+    const __amdgpu_buffer_rsrc_t br = row_of(p.residual, r, (kF32 ? 4 : 2) * p.cols, ok);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      if (ok && c < p.cols) {
-        if (p.x) rx[i] = *reinterpret_cast<const uint4*>(p.x + r * p.cols + c);
-        if (p.residual) rr[i].load(p.residual, r * p.cols + c);
-      }
+      rx[i] = load16(bx, 16u * (t + T * i));   // (without x or a residual: zeros)
+      rr[i].load(br, 16u * (t + T * i));
     }
-    F8 v[N];
+  };
+  load(blockIdx.x);
+  int odd = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, odd ^= 1) {
+    const __amdgpu_buffer_rsrc_t bs = row_of(p.sum, r, (kF32 ? 4 : 2) * p.cols, true), by = row_of(p.y, r, 2 * p.cols, true);
+    const __amdgpu_buffer_rsrc_t bq = row_of(p.row_q, r, p.cols, true);
+    Raw<kF32> v[N];   // r as it is stored
     float ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      if (ok && c < p.cols) {
-        if (p.x) v[i] = widen(rx[i]);
-        if (p.residual) {
-          const F8 a = rr[i].value();
+      F8 f = widen(rx[i]);
+      if (p.residual) {
+        const F8 a = rr[i].value();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[i].v[k] = p.x ? v[i].v[k] + a.v[k] : a.v[k];
-          if constexpr (!kF32) v[i] = widen(narrow(v[i]));   // the norm is of the stored value
-        }
-        if (p.sum) store_stream<kF32>(p.sum, r * p.cols + c, v[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i].v[k] = 0.0f;
+        for (int k = 0; k < 8; ++k) f.v[k] = p.x ? f.v[k] + a.v[k] : a.v[k];   // (0 + -0 is no -0)
       }
-      float q[8];
+      v[i].set(f);
+      if (p.sum) v[i].store(bs, 16u * (t + T * i));
+      f = v[i].value();
+      float s[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = v[i].v[k] * v[i].v[k];
-      ss[0] += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+      for (int k = 0; k < 8; ++k) s[k] = f.v[k] * f.v[k];
+      ss[0] += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     }
-    row_sums<G>(ss, slots[(j / kGroups<G>) & 1]);
+    load(r + gridDim.x);
+    row_sums(ss, slots[odd], waves);
     const float s = rsqrtf(fmaf(ss[0], inv_cols, p.eps));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      const bool in = ok && c < p.cols;
-      F8 f;
+      const int chunk = t + T * i;
+      v[i].pin();
+      F8 f = v[i].value();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f.v[k] = v[i].v[k] * s * w[i].v[k];
-      // (past the row's end or the band's: zeros, whatever s is)
-      const uint4 o = in ? narrow(f) : make_uint4(0, 0, 0, 0);
-      if (p.y && in) *reinterpret_cast<uint4*>(p.y + r * p.cols + c) = o;
+      for (int k = 0; k < 8; ++k) f.v[k] = f.v[k] * s * w[i].v[k];
+      // (past the row's end zeros, whatever s is: a quad of lanes is in or out)
+      const uint4 o = 8 * chunk < p.cols ? narrow(f) : make_uint4(0, 0, 0, 0);
+      if (p.y) store16(by, 16u * chunk, o);
       if (p.row_q) {
         // a quad of lanes holds a block, 16 lanes a panel of 4 blocks
         const uint32_t sb = scale_byte_from_amax(quad_max(amax8(o)));
         const float sc = e8m0_to_f32(sb);
-        if (in) *reinterpret_cast<uint2*>(p.row_q + r * p.cols + c) = make_uint2(cvt4_e4m3(o.x, o.y, sc), cvt4_e4m3(o.z, o.w, sc));
-        const int ch = threadIdx.x & 15;
+        typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(v2u{cvt4_e4m3(o.x, o.y, sc), cvt4_e4m3(o.z, o.w, sc)}, bq, 8 * chunk, 0, kNt);
+        const int ch = t & 15, panel = chunk >> 4;
         uint32_t d = sb << (8 * (ch >> 2));
         d |= dpp_row_shr(d, 4);
         d |= dpp_row_shr(d, 8);
-        const int32_t panel = (t + G * i) >> 4;
-        if (ok && ch == 12 && 128 * (int64_t)panel < p.cols) {
-          if (p.staged) panels[panel * p.band + j + g] = d;
-          else reinterpret_cast<uint32_t*>(p.row_s)[(int64_t)panel * p.rows + r] = d;
-        }
+        if (ch == 12 && 128 * (int64_t)panel < p.cols) reinterpret_cast<uint32_t*>(p.row_s)[(int64_t)panel * p.rows + r] = d;
       }
-    }
-  }
-  if (p.row_q && p.staged) {
-    __syncthreads();
-    const int32_t n = (int32_t)((p.cols + 127) / 128) * p.band;
-    for (int32_t e = threadIdx.x; e < n; e += kThreads<G>) {
-      const int32_t panel = e / p.band, j = e % p.band;
-      if (j < band) reinterpret_cast<uint32_t*>(p.row_s)[(int64_t)panel * p.rows + r0 + j] = panels[e];
     }
   }
 }
@@ -215,111 +234,100 @@ struct NormBwd {
   void* dres;
   uint16_t* dx;
   float* part;             // [workgroups, cols] or null
-  int32_t band;            // rows per workgroup
 };
 
-template <int G, int N, bool kF32>
-__global__ void __launch_bounds__(kThreads<G>) k_rmsnorm_bwd(const NormBwd p) {
-  __shared__ float slots[2][2 * kThreads<G> / 64];
-  __shared__ float cols_sum[kGroups<G> > 1 ? kGroups<G> - 1 : 1][kGroups<G> > 1 ? 8 * G * N : 1];
-  const int g = threadIdx.x / G, t = threadIdx.x % G;
-  const int64_t r0 = (int64_t)blockIdx.x * p.band;
-  const int32_t band = p.rows - r0 < p.band ? (int32_t)(p.rows - r0) : p.band;
+template <int N, bool kF32>
+__global__ void __launch_bounds__(1024) k_rmsnorm_bwd(const NormBwd p) {
+  __shared__ float slots[2][kMaxWaves][2];
+  const int T = blockDim.x, t = threadIdx.x, waves = T >> 6;
+  if (waves > 1) clear_slots(slots);
   F8 w[N], dw[N];
-  load_weights<G, N>(w, p.weight, t, p.cols);
+  load_weights<N>(w, p.weight, p.cols);
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i].v[k] = 0.0f;
   const float inv_cols = 1.0f / (float)p.cols;
 
-  for (int32_t j = 0; j < band; j += kGroups<G>) {
-    const bool ok = j + g < band;
-    const int64_t r = r0 + j + g;
-    uint4 rd[N];
-    Raw<kF32> rr[N], rs[N];
+  uint4 nd[N];
+  Raw<kF32> nr[N], ns[N];
+  auto load = [&](int64_t r) {
+    const bool ok = r < p.rows;
+    const int64_t bytes = (kF32 ? 4 : 2) * p.cols;
+    const __amdgpu_buffer_rsrc_t br = row_of(p.sum, r, bytes, ok), bd = row_of(p.dy, r, 2 * p.cols, ok);
+    const __amdgpu_buffer_rsrc_t bs = row_of(p.dsum, r, bytes, ok);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      if (ok && c < p.cols) {
-        rr[i].load(p.sum, r * p.cols + c);
-        rd[i] = *reinterpret_cast<const uint4*>(p.dy + r * p.cols + c);
-        if (p.dsum) rs[i].load(p.dsum, r * p.cols + c);
-      }
+      nr[i].load(br, 16u * (t + T * i));
+      nd[i] = load16(bd, 16u * (t + T * i));
+      ns[i].load(bs, 16u * (t + T * i));   // (without one: zeros)
     }
+  };
+  load(blockIdx.x);
+  int odd = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, odd ^= 1) {
+    uint4 rd[N];
+    Raw<kF32> rr[N], rs[N];
     float s2[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      if (ok && c < p.cols) {
-        const F8 a = rr[i].value(), d = widen(rd[i]);
-        float q[8], h[8];
+      rr[i] = nr[i];
+      rd[i] = nd[i];
+      rs[i] = ns[i];
+      const F8 a = rr[i].value(), d = widen(rd[i]);
+      float s[8], h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          q[k] = a.v[k] * a.v[k];
-          h[k] = d.v[k] * w[i].v[k] * a.v[k];
-        }
-        s2[0] += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
-        s2[1] += ((h[0] + h[1]) + (h[2] + h[3])) + ((h[4] + h[5]) + (h[6] + h[7]));
+      for (int k = 0; k < 8; ++k) {
+        s[k] = a.v[k] * a.v[k];
+        h[k] = d.v[k] * w[i].v[k] * a.v[k];
       }
+      s2[0] += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      s2[1] += ((h[0] + h[1]) + (h[2] + h[3])) + ((h[4] + h[5]) + (h[6] + h[7]));
     }
-    row_sums<G>(s2, slots[(j / kGroups<G>) & 1]);
+    load(r + gridDim.x);
+    row_sums(s2, slots[odd], waves);
     const float s = rsqrtf(fmaf(s2[0], inv_cols, p.eps));
     const float m = s * s * (s2[1] * inv_cols);
+    const __amdgpu_buffer_rsrc_t bo = row_of(p.dres, r, (kF32 ? 4 : 2) * p.cols, true), bx = row_of(p.dx, r, 2 * p.cols, true);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t c = 8 * (int64_t)(t + G * i);
-      if (ok && c < p.cols) {
-        const F8 a = rr[i].value(), d = widen(rd[i]);
-        F8 o;
+      rr[i].pin();
+      pin16(rd[i]);
+      const F8 a = rr[i].value(), d = widen(rd[i]), e = rs[i].value();
+      F8 o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o.v[k] = s * fmaf(-m, a.v[k], d.v[k] * w[i].v[k]);
-          dw[i].v[k] = fmaf(d.v[k], a.v[k] * s, dw[i].v[k]);
-        }
-        if (p.dsum) {
-          const F8 e = rs[i].value();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o.v[k] += e.v[k];
-        }
-        if (p.dres) store_stream<kF32>(p.dres, r * p.cols + c, o);
-        if (p.dx) *reinterpret_cast<uint4*>(p.dx + r * p.cols + c) = narrow(o);
+      for (int k = 0; k < 8; ++k) {
+        o.v[k] = s * fmaf(-m, a.v[k], d.v[k] * w[i].v[k]) + e.v[k];
+        dw[i].v[k] = fmaf(d.v[k], a.v[k] * s, dw[i].v[k]);
       }
+      if (p.dres) {
+        Raw<kF32> x;
+        x.set(o);
+        x.store(bo, 16u * (t + T * i));
+      }
+      if (p.dx) store16(bx, 16u * (t + T * i), narrow(o));
     }
   }
   if (!p.part) return;
-  // the row groups' sums in order, then one row of partial sums per workgroup
-  if constexpr (kGroups<G> > 1) {
-    if (g > 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) cols_sum[g - 1][k * G * N + t + G * i] = dw[i].v[k];
-    }
-    __syncthreads();
-    if (g > 0) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int o = 0; o < kGroups<G> - 1; ++o) dw[i].v[k] += cols_sum[o][k * G * N + t + G * i];
-  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int64_t c = 8 * (int64_t)(t + G * i);
-    if (c < p.cols) store_stream<true>(p.part, (int64_t)blockIdx.x * p.cols + c, dw[i]);
+    const int64_t c = 8 * (int64_t)(t + T * i);
+    if (c < p.cols) {
+      float4* o = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * p.cols + c);
+      o[0] = make_float4(dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]);
+      o[1] = make_float4(dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]);
+    }
   }
 }
 
-// dweight from the workgroups' sums: 16 columns per workgroup, 16 threads to a
+// dweight from the workgroups' sums: 32 columns per workgroup, 32 threads to a
 // column, each a run of partial sums in order, then the runs in order.
-__global__ void __launch_bounds__(256) k_norm_join(const float* __restrict__ part, int32_t blocks, int64_t cols,
-                                                   float* __restrict__ dweight) {
-  __shared__ float sum[16][17];
-  const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
-  const int64_t j = 16 * (int64_t)blockIdx.x + c;   // cols % 32 == 0: always a column
-  const int per = (blocks + 15) / 16;
+__global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ part, int32_t blocks, int64_t cols,
+                                                    float* __restrict__ dweight) {
+  __shared__ float sum[32][33];
+  const int c = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int64_t j = 32 * (int64_t)blockIdx.x + c;   // cols % 32 == 0: always a column
+  const int per = (blocks + 31) / 32;
   const int b1 = (run + 1) * per < blocks ? (run + 1) * per : blocks;
   float t = 0.0f;
 #pragma unroll 8
@@ -327,57 +335,51 @@ __global__ void __launch_bounds__(256) k_norm_join(const float* __restrict__ par
   sum[run][c] = t;
   __syncthreads();
   if (run == 0) {
-    for (int r = 1; r < 16; ++r) t += sum[r][c];
+    for (int r = 1; r < 32; ++r) t += sum[r][c];
     dweight[j] = t;
   }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr int64_t kMaxCols = 65536;
-constexpr int kCus = 256;   // MI355X
 
-// Threads per row (64, 256, 1024) and chunks per thread.
+// Chunks per thread, threads of a row, and the workgroups that run together at
+// most.  Two chunks to a thread above 4096 columns (backward at 32768 x 7168:
+// 299 us, with one 319), but for the fp32 stream's backward, whose registers
+// they overflow (911 us, with one 674).
 struct Split {
-  int g, n;
+  int n, threads;
+  int64_t most;
 };
 
-Split split_row(int64_t rows, int64_t cols) {
-  const int64_t chunks = (cols + 7) / 8;
-  int g = chunks <= 4 * 64 ? 64 : chunks <= 4 * 256 ? 256 : 1024;
-  // few rows: more threads to each
-  while (g < 1024 && chunks > g && rows * g < 1024 * (int64_t)kCus) g *= 4;
+Split split_row(int64_t cols, bool f32_bwd) {
+  const int64_t chunks = cols / 8;
   int n = 1;
-  while (n * g < chunks) n *= 2;
-  return Split{g, n};
+  while ((n == 1 && !f32_bwd ? 512 : 1024) * n < chunks) n *= 2;
+  // Few rows in flight, near each other: a CU takes one row of 4096 columns, or
+  // narrower ones of that size together.  32768 x 7168, backward: 299 us, with
+  // two workgroups per CU 347; 131072 x 512: 102 us with 8 and with 16, 120 with 4.
+  const int64_t per_cu = (512 + chunks / 2) / chunks;
+  return Split{n, (int)((chunks + 64 * n - 1) / (64 * n) * 64), kCus * (per_cu < 1 ? 1 : per_cu)};
 }
 
-int32_t bwd_band(int64_t rows, const Split& s) {
-  const int groups = s.g < 256 ? 256 / s.g : 1;
-  const int64_t want = (int64_t)kCus * (s.g == 1024 ? 1 : 3);
-  int64_t band = (rows + want - 1) / want;
-  band = (band + groups - 1) / groups * groups;
-  return (int32_t)band;
+int32_t bwd_blocks(int64_t rows, int64_t cols) {
+  const int64_t most = split_row(cols, false).most;
+  return (int32_t)(rows < most ? rows : most);
 }
 
-template <int G, int N, typename F>
+template <int N, typename F>
 int with_stream(bool f32, F f) {
-  return f32 ? f(std::integral_constant<int, G>(), std::integral_constant<int, N>(), std::true_type())
-             : f(std::integral_constant<int, G>(), std::integral_constant<int, N>(), std::false_type());
+  return f32 ? f(std::integral_constant<int, N>(), std::true_type()) : f(std::integral_constant<int, N>(), std::false_type());
 }
 
 template <typename F>
-int dispatch(const Split& s, bool f32, F f) {
-  switch (s.g * 16 + s.n) {
-    case 64 * 16 + 1: return with_stream<64, 1>(f32, f);
-    case 64 * 16 + 2: return with_stream<64, 2>(f32, f);
-    case 64 * 16 + 4: return with_stream<64, 4>(f32, f);
-    case 256 * 16 + 1: return with_stream<256, 1>(f32, f);
-    case 256 * 16 + 2: return with_stream<256, 2>(f32, f);
-    case 256 * 16 + 4: return with_stream<256, 4>(f32, f);
-    case 1024 * 16 + 1: return with_stream<1024, 1>(f32, f);
-    case 1024 * 16 + 2: return with_stream<1024, 2>(f32, f);
-    case 1024 * 16 + 4: return with_stream<1024, 4>(f32, f);
-    default: return with_stream<1024, 8>(f32, f);
+int dispatch(int n, bool f32, F f) {
+  switch (n) {
+    case 1: return with_stream<1>(f32, f);
+    case 2: return with_stream<2>(f32, f);
+    case 4: return with_stream<4>(f32, f);
+    default: return with_stream<8>(f32, f);
   }
 }
 
@@ -386,7 +388,7 @@ inline bool misaligned(const void* p, uintptr_t a) { return p && (reinterpret_ca
 // Arguments both directions share.
 int check(int32_t stream_dtype, const float* weight, int64_t rows, int64_t cols, double eps) {
   if (stream_dtype != MX_OUT_BF16 && stream_dtype != MX_OUT_F32) return MX_EINVAL;
-  if (rows < 0 || cols <= 0 || cols % 32 || !(eps > 0.0) || eps > 1e30 || misaligned(weight, 4)) return MX_EINVAL;
+  if (rows < 0 || cols <= 0 || cols % 32 || !(eps >= 1e-37) || eps > 1e30 || misaligned(weight, 4)) return MX_EINVAL;
   if (cols > kMaxCols || rows >= (1ll << 31)) return MX_EUNSUPPORTED;
   return MX_OK;
 }
@@ -406,19 +408,11 @@ extern "C" int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t strea
       misaligned(row_q, 8) || misaligned(row_s, 4))
     return MX_EINVAL;
   if (rc != MX_OK || rows == 0) return rc;
-  const Split s = split_row(rows, cols);
-  Norm p{x, residual, weight, rows, cols, (float)eps, sum, y, row_q, row_s, 1, false};
-  const int groups = s.g < 256 ? 256 / s.g : 1;
-  // bands of up to 32 rows, so that a panel's scales leave as whole lines, while the card is filled
-  int64_t band = (rows + 8 * kCus - 1) / (8 * kCus);
-  band = band > 32 ? 32 : (band + groups - 1) / groups * groups;
-  p.band = (int32_t)band;
-  p.staged = row_q && band > groups;
-  const size_t lds = p.staged ? (size_t)((cols + 127) / 128) * band * 4 : 0;
-  const dim3 grid((unsigned)((rows + band - 1) / band));
-  return dispatch(s, stream_dtype == MX_OUT_F32, [&](auto g, auto n, auto f32) {
-    constexpr int G = decltype(g)::value, N = decltype(n)::value;
-    hipLaunchKernelGGL((k_rmsnorm<G, N, decltype(f32)::value>), grid, dim3(kThreads<G>), lds,
+  const Split s = split_row(cols, false);
+  const Norm p{x, residual, weight, rows, cols, (float)eps, sum, y, row_q, row_s};
+  const dim3 grid((unsigned)(rows < s.most ? rows : s.most));
+  return dispatch(s.n, stream_dtype == MX_OUT_F32, [&](auto n, auto f32) {
+    hipLaunchKernelGGL((k_rmsnorm<decltype(n)::value, decltype(f32)::value>), grid, dim3(s.threads), 0,
                        reinterpret_cast<hipStream_t>(stream), p);
     return launch_status();
   });
@@ -426,8 +420,7 @@ extern "C" int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t strea
 
 extern "C" size_t mx_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols) {
   if (rows <= 0 || check(MX_OUT_BF16, nullptr, rows, cols, 1.0) != MX_OK) return 0;
-  const int32_t band = bwd_band(rows, split_row(rows, cols));
-  return (size_t)((rows + band - 1) / band * cols * 4);
+  return (size_t)(bwd_blocks(rows, cols) * cols * 4);
 }
 
 extern "C" int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_t stream_dtype,
@@ -444,19 +437,18 @@ extern "C" int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* d
   if (dweight && rows > 0 && (!workspace || workspace_bytes < mx_rmsnorm_bwd_workspace_size(rows, cols))) return MX_EINVAL;
   int32_t blocks = 0;
   if (rows > 0) {
-    const Split s = split_row(rows, cols);
-    NormBwd p{dy, sum, dsum, weight, rows, cols, (float)eps, dres, dx, dweight ? static_cast<float*>(workspace) : nullptr,
-              bwd_band(rows, s)};
-    blocks = (int32_t)((rows + p.band - 1) / p.band);
-    const int launched = dispatch(s, stream_dtype == MX_OUT_F32, [&](auto g, auto n, auto f32) {
-      constexpr int G = decltype(g)::value, N = decltype(n)::value;
-      hipLaunchKernelGGL((k_rmsnorm_bwd<G, N, decltype(f32)::value>), dim3((unsigned)blocks), dim3(kThreads<G>), 0, st, p);
+    const Split s = split_row(cols, stream_dtype == MX_OUT_F32);
+    blocks = bwd_blocks(rows, cols);
+    const NormBwd p{dy, sum, dsum, weight, rows, cols, (float)eps, dres, dx, dweight ? static_cast<float*>(workspace) : nullptr};
+    const int launched = dispatch(s.n, stream_dtype == MX_OUT_F32, [&](auto n, auto f32) {
+      hipLaunchKernelGGL((k_rmsnorm_bwd<decltype(n)::value, decltype(f32)::value>), dim3((unsigned)blocks),
+                         dim3(s.threads), 0, st, p);
       return launch_status();
     });
     if (launched != MX_OK) return launched;
   }
   if (!dweight) return MX_OK;
-  hipLaunchKernelGGL(k_norm_join, dim3((unsigned)(cols / 16)), dim3(256), 0, st,
+  hipLaunchKernelGGL(k_norm_join, dim3((unsigned)(cols / 32)), dim3(1024), 0, st,
                      static_cast<const float*>(workspace), blocks, cols, dweight);
   return launch_status();
 }
