@@ -343,28 +343,28 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ pa
 // ---------------------------------------------------------------- host side
 constexpr int64_t kMaxCols = 65536;
 
-// Chunks per thread, threads of a row, and the workgroups that run together at
-// most.  Two chunks to a thread above 4096 columns (backward at 32768 x 7168:
-// 299 us, with one 319), but for the fp32 stream's backward, whose registers
-// they overflow (911 us, with one 674).
+// Chunks per thread and threads of a row.  Two chunks to a thread above 4096
+// columns (backward at 32768 x 7168: 299 us, with one 319), but for the fp32
+// stream's backward, whose registers they overflow (911 us, with one 674).
 struct Split {
   int n, threads;
-  int64_t most;
 };
 
 Split split_row(int64_t cols, bool f32_bwd) {
   const int64_t chunks = cols / 8;
   int n = 1;
   while ((n == 1 && !f32_bwd ? 512 : 1024) * n < chunks) n *= 2;
-  // Few rows in flight, near each other: a CU takes one row of 4096 columns, or
-  // narrower ones of that size together.  32768 x 7168, backward: 299 us, with
-  // two workgroups per CU 347; 131072 x 512: 102 us with 8 and with 16, 120 with 4.
-  const int64_t per_cu = (512 + chunks / 2) / chunks;
-  return Split{n, (int)((chunks + 64 * n - 1) / (64 * n) * 64), kCus * (per_cu < 1 ? 1 : per_cu)};
+  return Split{n, (int)((chunks + 64 * n - 1) / (64 * n) * 64)};
 }
 
-int32_t bwd_blocks(int64_t rows, int64_t cols) {
-  const int64_t most = split_row(cols, false).most;
+// Workgroups for rows that move `bytes` an element: few rows in work, near each
+// other, 40 KB to a CU.  32768 x 7168, backward with dsum (8 bytes): 298 us with
+// one per CU, 345 with two; 32768 x 4096, x to y (4 bytes): 89 us with two, 124
+// with one; 131072 x 512 with all outputs (9 bytes): 103 us with 8, 150 with 4.
+int32_t blocks_for(int64_t rows, int64_t cols, int64_t bytes) {
+  const int64_t row = bytes * cols / 8;
+  const int64_t per_cu = (5000 + row / 2) / row;
+  const int64_t most = kCus * (per_cu < 1 ? 1 : per_cu);
   return (int32_t)(rows < most ? rows : most);
 }
 
@@ -410,7 +410,8 @@ extern "C" int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t strea
   if (rc != MX_OK || rows == 0) return rc;
   const Split s = split_row(cols, false);
   const Norm p{x, residual, weight, rows, cols, (float)eps, sum, y, row_q, row_s};
-  const dim3 grid((unsigned)(rows < s.most ? rows : s.most));
+  const int64_t wide = stream_dtype == MX_OUT_F32 ? 4 : 2;
+  const dim3 grid((unsigned)blocks_for(rows, cols, (x ? 2 : 0) + (residual ? wide : 0) + (sum ? wide : 0) + (y ? 2 : 0) + (row_q ? 1 : 0)));
   return dispatch(s.n, stream_dtype == MX_OUT_F32, [&](auto n, auto f32) {
     hipLaunchKernelGGL((k_rmsnorm<decltype(n)::value, decltype(f32)::value>), grid, dim3(s.threads), 0,
                        reinterpret_cast<hipStream_t>(stream), p);
@@ -420,7 +421,7 @@ extern "C" int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t strea
 
 extern "C" size_t mx_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols) {
   if (rows <= 0 || check(MX_OUT_BF16, nullptr, rows, cols, 1.0) != MX_OK) return 0;
-  return (size_t)(bwd_blocks(rows, cols) * cols * 4);
+  return (size_t)(blocks_for(rows, cols, 6) * cols * 4);   // (the most workgroups: bf16 without dsum)
 }
 
 extern "C" int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_t stream_dtype,
@@ -438,7 +439,9 @@ extern "C" int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* d
   int32_t blocks = 0;
   if (rows > 0) {
     const Split s = split_row(cols, stream_dtype == MX_OUT_F32);
-    blocks = bwd_blocks(rows, cols);
+    // (whatever outputs are asked for: dweight keeps its bits)
+    const int64_t wide = stream_dtype == MX_OUT_F32 ? 4 : 2;
+    blocks = blocks_for(rows, cols, 2 + wide * (dsum ? 3 : 2));
     const NormBwd p{dy, sum, dsum, weight, rows, cols, (float)eps, dres, dx, dweight ? static_cast<float*>(workspace) : nullptr};
     const int launched = dispatch(s.n, stream_dtype == MX_OUT_F32, [&](auto n, auto f32) {
       hipLaunchKernelGGL((k_rmsnorm_bwd<decltype(n)::value, decltype(f32)::value>), dim3((unsigned)blocks),
