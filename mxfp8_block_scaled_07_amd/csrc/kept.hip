@@ -23,12 +23,16 @@
 namespace mx {
 namespace {
 
-// 8 codes with their block's scale byte to bf16, as the dequantize does it.
+// 8 codes with their block's scale byte (not 255) to bf16, as the dequantize does it.
 __device__ __forceinline__ uint4 decode8(const uint2& c, uint32_t sb) {
   const float sc = e8m0_to_f32(sb);
   const uint2 a = cvt4_bf16(c.x, sc), b = cvt4_bf16(c.y, sc);
-  const uint4 v = make_uint4(a.x, a.y, b.x, b.y);
-  return sb == 255u ? make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u) : v;
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// A block of scale 255 is NaN: sets the block's 8 values to it.
+__device__ __forceinline__ void nan_scale(uint4& v, uint32_t sb) {
+  if (sb == 255u) v = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
 }
 
 // tq_store_rows for columns base + c0 .. of a matrix where base is a multiple of
@@ -49,14 +53,17 @@ __device__ __forceinline__ void store_rows_bytes(const uint4 (&v)[8], uint8_t* r
 }
 
 // Half (gate or up) of a matrix [rows, 2F], at the tile's columns c0 .. of it.
+// kWhole: F % 128 == 0, no panel holds columns of both halves.
+template <bool kWhole>
 __device__ __forceinline__ void store_half(const uint4 (&v)[8], uint8_t* q, uint8_t* s, int64_t rows, int64_t F, int64_t r,
                                            int64_t half, int64_t c0, bool col_ok) {
-  if (F % 128 == 0)
+  if constexpr (kWhole)
     tq_store_rows<true, false>(v, q, s, nullptr, rows, 2 * F, r, r, rows, half + c0, col_ok);
   else
     store_rows_bytes(v, q, s, rows, 2 * F, r, rows, half + c0 + 8 * (threadIdx.x & 15), col_ok);
 }
 
+template <bool kWhole>
 __global__ void __launch_bounds__(kTqThreads) k_swiglu_keep(const uint16_t* __restrict__ h, int64_t rows, int64_t F,
                                                             int32_t n_tc, uint8_t* __restrict__ row_q,
                                                             uint8_t* __restrict__ row_s, uint8_t* __restrict__ keep_q,
@@ -85,8 +92,8 @@ __global__ void __launch_bounds__(kTqThreads) k_swiglu_keep(const uint16_t* __re
     a[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   tq_store_rows<true, false>(a, row_q, row_s, nullptr, rows, F, r, r, rows, c0, col_ok);
-  store_half(g, keep_q, keep_s, rows, F, r, 0, c0, col_ok);
-  store_half(u, keep_q, keep_s, rows, F, r, F, c0, col_ok);
+  store_half<kWhole>(g, keep_q, keep_s, rows, F, r, 0, c0, col_ok);
+  store_half<kWhole>(u, keep_q, keep_s, rows, F, r, F, c0, col_ok);
 }
 
 struct KeptBwd {
@@ -111,6 +118,7 @@ __device__ __forceinline__ float row16_sum(float v) {
   return v;
 }
 
+template <bool kWhole>
 __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kTq * kTq * 2];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ch = lane & 15;
@@ -141,11 +149,19 @@ __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd
       us[i] = su[4 * i];
     }
   }
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, max(gs[i], us[i]));
+  const bool nans = __any(most == 255u);   // (looked at once for the wave: hardly ever)
   uint4 vg[8], vu[8], va[8];
   float mine = 0.0f;   // lane ch < 8: the dot of row r + ch
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint4 g4 = decode8(gq[i], gs[i]), u4 = decode8(uq[i], us[i]);
+    uint4 g4 = decode8(gq[i], gs[i]), u4 = decode8(uq[i], us[i]);
+    if (nans) {
+      nan_scale(g4, gs[i]);
+      nan_scale(u4, us[i]);
+    }
     float dot = 0.0f;
     uint32_t wg[4], wu[4], wa[4];
 #pragma unroll
@@ -172,8 +188,8 @@ __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd
   }
   if (p.dots && ch < 8 && r + ch < p.rows) p.dots[(int64_t)tc * p.rows + r + ch] = mine;
   if (p.row_q) {
-    store_half(vg, p.row_q, p.row_s, p.rows, F, r, 0, c0, col_ok);
-    store_half(vu, p.row_q, p.row_s, p.rows, F, r, F, c0, col_ok);
+    store_half<kWhole>(vg, p.row_q, p.row_s, p.rows, F, r, 0, c0, col_ok);
+    store_half<kWhole>(vu, p.row_q, p.row_s, p.rows, F, r, F, c0, col_ok);
   }
   if (p.col_q) {
     tq_store_cols<false>(vg, lds, p.col_q, p.col_s, 2 * F, c0, F - c0, p.rows, r0);
@@ -274,7 +290,11 @@ struct SrcMx {
     x.sb = s[scale_index(rows_in, w.r, col >> 5)];
     return x;
   }
-  __device__ uint4 finish(const Raw& x, const Row&, int64_t) const { return decode8(x.c, x.sb); }
+  __device__ uint4 finish(const Raw& x, const Row&, int64_t) const {
+    uint4 v = decode8(x.c, x.sb);
+    nan_scale(v, x.sb);
+    return v;
+  }
 };
 
 // 128 rows of H in bytes stay below the 2^31 of a buffer's offsets.
@@ -300,8 +320,8 @@ extern "C" int mx_swiglu_keep(const uint16_t* h, int64_t rows, int64_t F, uint8_
   TqShape sh;
   unsigned grid;
   if (!tq_shape(1, rows, F, sh, grid)) return MX_EINVAL;
-  hipLaunchKernelGGL(k_swiglu_keep, dim3(grid), dim3(kTqThreads), 0, reinterpret_cast<hipStream_t>(stream), h, rows, F,
-                     sh.n_tc, row_q, row_s, keep_q, keep_s);
+  hipLaunchKernelGGL((F % 128 ? k_swiglu_keep<false> : k_swiglu_keep<true>), dim3(grid), dim3(kTqThreads), 0,
+                     reinterpret_cast<hipStream_t>(stream), h, rows, F, sh.n_tc, row_q, row_s, keep_q, keep_s);
   return launch_status();
 }
 
@@ -331,7 +351,7 @@ extern "C" int mx_swiglu_bwd_kept(const uint8_t* keep_q, const uint8_t* keep_s, 
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const KeptBwd p{keep_q, keep_s, da, rows, F, sh.n_tc, row_q, row_s, col_q, col_s, a_col_q, a_col_s,
                   need ? static_cast<float*>(workspace) : dots};
-  hipLaunchKernelGGL(k_swiglu_bwd_kept, dim3(grid), dim3(kTqThreads), 0, st, p);
+  hipLaunchKernelGGL((F % 128 ? k_swiglu_bwd_kept<false> : k_swiglu_bwd_kept<true>), dim3(grid), dim3(kTqThreads), 0, st, p);
   if (need)
     hipLaunchKernelGGL(k_dots_join, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, st,
                        static_cast<const float*>(workspace), rows, sh.n_tc, dots);

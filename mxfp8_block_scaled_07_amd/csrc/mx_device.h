@@ -24,14 +24,14 @@ constexpr int kBlock = 32;
 // floor of log2 is its exponent field minus 127, so the byte is the exponent
 // field minus 8; zero and subnormal amax (field 0) clamp to byte 0.
 __device__ __forceinline__ uint32_t scale_byte_from_amax(uint32_t amax_bits) {
-  const uint32_t e = amax_bits >> 7;
-  return e > 8u ? e - 8u : 0u;
+  return __builtin_elementwise_sub_sat(amax_bits >> 7, 8u);
 }
 
 // fp32 holding 2^(byte-127) for byte in [0, 254]; byte 0 is the fp32
 // subnormal 2^-127 (never 0).
 __device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
-  return __uint_as_float(b ? (b << 23) : 0x00400000u);
+  const uint32_t e = b << 23;
+  return __uint_as_float(e > 0x00400000u ? e : 0x00400000u);
 }
 
 // Largest bf16 magnitude (bits, sign cleared) of the two halves of w.

@@ -80,22 +80,26 @@ __device__ __forceinline__ void tq_store_rows(const uint4 (&v)[8], uint8_t* row_
                                               int64_t cols, int64_t row, int64_t r, int64_t rows_out, int64_t c0,
                                               bool col_ok) {
   const int ch = threadIdx.x & 15;
-  const int64_t col = c0 + 8 * ch;
+  const int64_t at = row * cols + c0 + 8 * ch;
+  if (kY) y += at;
+  if (kRow) {
+    row_q += at;
+    row_s += ((c0 >> 7) * R + row) * 4;
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; ++i, y += kY ? cols : 0, row_q += kRow ? cols : 0) {
     const bool r_ok = r + i < rows_out;
-    const int64_t orow = row + i;
-    if (kY && r_ok && col_ok) *reinterpret_cast<uint4*>(y + orow * cols + col) = v[i];
+    if (kY && r_ok && col_ok) *reinterpret_cast<uint4*>(y) = v[i];
     if (kRow) {
       const uint32_t sb = scale_byte_from_amax(quad_max(amax8(v[i])));
       const float sc = e8m0_to_f32(sb);
       if (r_ok && col_ok)
-        *reinterpret_cast<uint2*>(row_q + orow * cols + col) =
+        *reinterpret_cast<uint2*>(row_q) =
             make_uint2(cvt4_e4m3(v[i].x, v[i].y, sc), cvt4_e4m3(v[i].z, v[i].w, sc));
       uint32_t d = sb << (8 * (ch >> 2));
       d |= dpp_row_shr(d, 4);
       d |= dpp_row_shr(d, 8);
-      if (r_ok && ch == 12) *reinterpret_cast<uint32_t*>(row_s + ((c0 >> 7) * R + orow) * 4) = d;
+      if (r_ok && ch == 12) *reinterpret_cast<uint32_t*>(row_s + 4 * i) = d;
     }
   }
 }
@@ -118,8 +122,8 @@ __device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds,
     uint32_t d[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const uint32_t a = tq_comp(v[2 * p], k), bb = tq_comp(v[2 * p + 1], k);
-      d[p] = (j & 1) ? (a >> 16) | (bb & 0xFFFF0000u) : (a & 0xFFFFu) | (bb << 16);
+      // the upper or the lower halves of two rows
+      d[p] = __builtin_amdgcn_perm(tq_comp(v[2 * p + 1], k), tq_comp(v[2 * p], k), (j & 1) ? 0x07060302u : 0x05040100u);
     }
     *reinterpret_cast<uint4*>(lds + cc * 256 + 16 * (slot ^ tq_swz(cc))) = make_uint4(d[0], d[1], d[2], d[3]);
   }
@@ -130,8 +134,9 @@ __device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds,
   // column's 4 scale bytes (lanes 0, 2, 4, 6 of the group) are merged with
   // row shifts into lane 6, which stores the panel dword.
   const int p = t & 7;
+  uint8_t* out = col_q + (crow + (t >> 3)) * rows_out + r0 + 16 * p;
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
+  for (int it = 0; it < 4; ++it, out += 32 * rows_out) {
     const int c = 32 * it + (t >> 3);
     const uint4 q0 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p) ^ tq_swz(c)));
     const uint4 q1 = *reinterpret_cast<const uint4*>(lds + c * 256 + 16 * ((2 * p + 1) ^ tq_swz(c)));
@@ -146,7 +151,7 @@ __device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds,
       typedef unsigned int v4u_ __attribute__((ext_vector_type(4)));
       const v4u_ cw = {cvt4_e4m3(q0.x, q0.y, sc), cvt4_e4m3(q0.z, q0.w, sc), cvt4_e4m3(q1.x, q1.y, sc),
                        cvt4_e4m3(q1.z, q1.w, sc)};
-      v4u_* dst = reinterpret_cast<v4u_*>(col_q + (crow + c) * rows_out + gr);
+      v4u_* dst = reinterpret_cast<v4u_*>(out);
       // Gathered sources walk the row bands of a column tile, so their
       // columnwise lines are written front to back: streamed (non-temporal)
       // stores are faster there (measured 7% on the gathered columnwise
