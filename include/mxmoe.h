@@ -471,7 +471,7 @@ int mx_router_bwd_dots(const float* dots, int64_t rows, const int32_t* dst_row, 
  *   gather   optional int32 [rows_out], rows_out as in mx_quantize
  *   col_q/col_s  codes [cols, rows_out], scales [cols, rows_out]
  * Requires cols % 32 == 0, rows_out % 32 == 0; q 8-byte, col_q 16-byte, scales
- * 4-byte aligned.
+ * 4-byte aligned.  MX_EUNSUPPORTED for rows >= 2^31.
  */
 int mx_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, const int32_t* gather,
                   int64_t rows_out, uint8_t* col_q, uint8_t* col_s, mx_stream_t stream);

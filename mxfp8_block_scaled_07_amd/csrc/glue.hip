@@ -30,7 +30,7 @@ struct SrcSwiglu {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
-  __device__ void fill_table(Table&, int64_t, int64_t, int64_t) const {}
+  __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
     const uint16_t* p;
@@ -73,7 +73,7 @@ struct SrcSwigluBwd {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
-  __device__ void fill_table(Table&, int64_t, int64_t, int64_t) const {}
+  __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
     const uint16_t* ph;
@@ -131,7 +131,7 @@ struct SrcCombineBwd {
   static constexpr bool kTable = true;
   static constexpr bool kGathered = true;
   static constexpr int kSub = 4;   // the pair table is built once for 4 column tiles
-  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out) const {
+  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out, int32_t) const {
     const int t = threadIdx.x;
     if (t < kTq) {
       const int64_t r = r0 + t;

@@ -250,52 +250,73 @@ __global__ void __launch_bounds__(256) k_router_bwd_dots(const float* __restrict
 }
 
 // Source of the tile quantizer: rowwise MX rows, decoded; gathered or in order.
-template <bool kGather>
+// The rows' scale dwords of the workgroup's column tiles come with the row table:
+// loaded a byte at a time beside the codes they cost more than these.
+template <bool kGather, int kTiles>
 struct SrcMx {
   const uint8_t* q;
   const uint8_t* s;
   const int32_t* gather;
   int64_t rows_in, cols;
   struct Table {
-    int32_t src[kGather ? kTq : 1];
+    int32_t src[kTq];
+    uint32_t sc[kTiles][kTq];
   };
-  static constexpr bool kTable = kGather;
+  static constexpr bool kTable = true;
   static constexpr bool kGathered = kGather;
-  static constexpr int kSub = 1;
+  static constexpr int kSub = kTiles;
   static constexpr bool kFetchAll = false;
-  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out) const {
-    const int t = threadIdx.x;
-    if (kGather && t < kTq) {
-      int32_t g = r0 + t < rows_out ? gather[r0 + t] : -1;
-      tb.src[t] = g < rows_in ? g : -1;
+  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out, int32_t tc0) const {
+    const int t = threadIdx.x & (kTq - 1), half = threadIdx.x / kTq;
+    const int64_t r = r0 + t;
+    int64_t g = r < rows_out ? (kGather ? gather[r] : r) : -1;
+    if (g >= rows_in) g = -1;
+    if (half == 0) tb.src[t] = (int32_t)g;
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(s) + (int64_t)tc0 * rows_in + g;
+#pragma unroll
+    for (int k = 0; k < (kTiles + 1) / 2; ++k) {
+      const int i = 2 * k + half;
+      if (i < kTiles) tb.sc[i][t] = g >= 0 && 128 * (int64_t)(tc0 + i) < cols ? sc[i * rows_in] : 0u;
     }
   }
   struct Row {
     bool ok;
-    int64_t r;
+    int32_t r;
+    uint32_t sc;   // the lane's scale bytes of the tiles
   };
-  __device__ Row row(const Table& tb, int64_t, int64_t r, int lr, bool in_range) const {
+  __device__ Row row(const Table& tb, int64_t, int64_t, int lr, bool in_range) const {
     Row w;
-    w.r = kGather ? tb.src[lr] : r;
-    w.ok = in_range && w.r >= 0 && w.r < rows_in;
+    w.r = tb.src[lr];
+    w.ok = in_range && w.r >= 0;
+    w.sc = 0;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) w.sc |= (tb.sc[i][lr] >> (8 * ((threadIdx.x & 15) >> 2)) & 0xFFu) << (8 * i);
     return w;
   }
-  struct Raw {
-    uint2 c;
-    uint32_t sb;
-  };
-  __device__ Raw fetch(const Row& w, int64_t col, bool) const {
-    Raw x;
-    x.c = *reinterpret_cast<const uint2*>(q + w.r * cols + col);
-    x.sb = s[scale_index(rows_in, w.r, col >> 5)];
-    return x;
-  }
-  __device__ uint4 finish(const Raw& x, const Row&, int64_t) const {
-    uint4 v = decode8(x.c, x.sb);
-    nan_scale(v, x.sb);
+  typedef uint2 Raw;
+  __device__ Raw fetch(const Row& w, int64_t col, bool) const { return *reinterpret_cast<const uint2*>(q + w.r * cols + col); }
+  __device__ uint4 finish(const Raw& x, const Row& w, int64_t col) const {
+    const uint32_t sb = w.sc >> (kTiles > 1 ? 8 * ((uint32_t)(col >> 7) % kTiles) : 0) & 0xFFu;
+    uint4 v = decode8(x, sb);
+    nan_scale(v, sb);
     return v;
   }
 };
+
+template <bool kGather>
+int launch_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, const int32_t* gather,
+                      const TqShape& sh, unsigned tiles, const TqOut& o, hipStream_t st) {
+  // four column tiles to a workgroup share the row table, where that leaves enough workgroups
+  if (tiles >= 4 * 4 * 256) {
+    const unsigned grid = (unsigned)((int64_t)sh.n_tr * ((sh.n_tc + 3) / 4));
+    hipLaunchKernelGGL((k_tile_quant<SrcMx<kGather, 4>, false, true, false>), dim3(grid), dim3(kTqThreads), 0, st,
+                       SrcMx<kGather, 4>{q, s, gather, rows, cols}, sh, o);
+  } else {
+    hipLaunchKernelGGL((k_tile_quant<SrcMx<kGather, 1>, false, true, false>), dim3(tiles), dim3(kTqThreads), 0, st,
+                       SrcMx<kGather, 1>{q, s, gather, rows, cols}, sh, o);
+  }
+  return launch_status();
+}
 
 // 128 rows of H in bytes stay below the 2^31 of a buffer's offsets.
 constexpr int64_t kMaxF = 1 << 22;
@@ -375,17 +396,13 @@ extern "C" int mx_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, i
                              int64_t rows_out, uint8_t* col_q, uint8_t* col_s, mx_stream_t stream) {
   if (!q || !s || !col_q || rows < 0 || cols <= 0 || cols % 32 || rows_out < 0 || rows_out % 32) return MX_EINVAL;
   if (bad_pair(q, s, 8) || bad_pair(col_q, col_s, 16) || misaligned(gather, 4)) return MX_EINVAL;
+  if (rows >= (1ll << 31)) return MX_EUNSUPPORTED;
   if (rows_out == 0) return MX_OK;
   TqShape sh;
   unsigned grid;
   if (!tq_shape(1, rows_out, cols, sh, grid)) return MX_EINVAL;
   const TqOut o = {nullptr, nullptr, col_q, col_s, nullptr};
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (gather)
-    hipLaunchKernelGGL((k_tile_quant<SrcMx<true>, false, true, false>), dim3(grid), dim3(kTqThreads), 0, st,
-                       SrcMx<true>{q, s, gather, rows, cols}, sh, o);
-  else
-    hipLaunchKernelGGL((k_tile_quant<SrcMx<false>, false, true, false>), dim3(grid), dim3(kTqThreads), 0, st,
-                       SrcMx<false>{q, s, gather, rows, cols}, sh, o);
-  return launch_status();
+  return gather ? launch_requantize<true>(q, s, rows, cols, gather, sh, grid, o, st)
+                : launch_requantize<false>(q, s, rows, cols, gather, sh, grid, o, st);
 }

@@ -28,7 +28,7 @@ struct SrcPlain {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
-  __device__ void fill_table(Table&, int64_t, int64_t, int64_t) const {}
+  __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
     const uint16_t* p;
@@ -55,7 +55,7 @@ struct SrcGather {
   static constexpr bool kGathered = true;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
-  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out) const {
+  __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out, int32_t) const {
     const int t = threadIdx.x;
     if (t < kTq) {
       const int64_t r = r0 + t;

@@ -172,7 +172,8 @@ __device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds,
 //   struct Table;                          LDS table filled once per tile (may be empty)
 //   static constexpr bool kTable;          whether fill_table must run
 //   static constexpr bool kGathered;       rows gathered from a source that other rows read again
-//   __device__ void fill_table(Table&, int64_t b, int64_t r0, int64_t rows_out) const;
+//   __device__ void fill_table(Table&, int64_t b, int64_t r0, int64_t rows_out, int32_t tc0) const;
+//                                          tc0: the workgroup's first column tile
 //   struct Row { bool ok; ... };
 //   __device__ Row row(const Table&, int64_t b, int64_t r, int local_r, bool in_range) const;
 //   struct Raw;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kTqThreads) k_tile_quant(const Src src, const 
   const int ch = lane & 15, ry = lane >> 4;
   const int lr0 = 32 * w + 8 * ry;
   if (Src::kTable) {
-    src.fill_table(table, b, r0, sh.rows_out);
+    src.fill_table(table, b, r0, sh.rows_out, tcg * kSub);
     __syncthreads();
   }
   typename Src::Row rw[8];
