@@ -30,6 +30,7 @@ struct SrcSwiglu {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
+  static constexpr bool kAhead = false;
   __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
@@ -73,6 +74,7 @@ struct SrcSwigluBwd {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
+  static constexpr bool kAhead = false;
   __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
@@ -190,6 +192,7 @@ struct SrcCombineBwd {
   // reads column 0, and the tile code discards both.  Without tokens, dout
   // may be null and nothing is read.
   static constexpr bool kFetchAll = true;
+  static constexpr bool kAhead = false;
   __device__ Raw fetch(const Row& x, int64_t col, bool col_ok) const {
     if (tokens == 0) return make_uint4(0, 0, 0, 0);
     const int64_t t = x.ok ? x.tok : 0;

@@ -266,6 +266,7 @@ struct SrcMx {
   static constexpr bool kGathered = kGather;
   static constexpr int kSub = kTiles;
   static constexpr bool kFetchAll = false;
+  static constexpr bool kAhead = kTiles > 1;
   __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out, int32_t tc0) const {
     const int t = threadIdx.x & (kTq - 1), half = threadIdx.x / kTq;
     const int64_t r = r0 + t;

@@ -28,6 +28,7 @@ struct SrcPlain {
   static constexpr bool kGathered = false;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
+  static constexpr bool kAhead = false;
   __device__ void fill_table(Table&, int64_t, int64_t, int64_t, int32_t) const {}
   struct Row {
     bool ok;
@@ -55,6 +56,7 @@ struct SrcGather {
   static constexpr bool kGathered = true;
   static constexpr int kSub = 1;
   static constexpr bool kFetchAll = false;
+  static constexpr bool kAhead = false;
   __device__ void fill_table(Table& tb, int64_t, int64_t r0, int64_t rows_out, int32_t) const {
     const int t = threadIdx.x;
     if (t < kTq) {

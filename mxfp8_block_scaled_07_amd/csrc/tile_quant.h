@@ -181,6 +181,7 @@ __device__ __forceinline__ void tq_store_cols(const uint4 (&v)[8], uint8_t* lds,
 //     unless kFetchAll (then for every row, and it must stay in bounds)
 //   static constexpr int kSub;             column tiles per workgroup
 //   static constexpr bool kFetchAll;
+//   static constexpr bool kAhead;          the next column tile is fetched while one is written (kSub > 1)
 //   __device__ uint4 finish(const Raw&, const Row&, int64_t col) const;   8 bf16
 // Rows or columns outside the output, and rows the source marks !ok, are
 // zero: they raise no amax and produce zero codes (and zero pad scales).
@@ -235,6 +236,19 @@ __global__ void __launch_bounds__(kTqThreads) k_tile_quant(const Src src, const 
     rw[i] = src.row(table, b, r, lr0 + i, r < sh.rows_out);
   }
 
+  auto fetch = [&](typename Src::Raw(&raw)[8], int64_t col, bool col_ok) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (Src::kFetchAll) raw[i] = src.fetch(rw[i], col, col_ok);
+      else if (rw[i].ok && col_ok) raw[i] = src.fetch(rw[i], col, true);
+    }
+  };
+  typename Src::Raw ahead[Src::kAhead ? 8 : 1];
+  if constexpr (Src::kAhead) {
+    const int64_t col = (int64_t)tcg * kSub * kTq + 8 * ch;
+    fetch(ahead, col, col < sh.cols);
+  }
+
 #pragma unroll 1
   for (int sub = 0; sub < kSub; ++sub) {
     const int32_t tc = tcg * kSub + sub;
@@ -246,14 +260,18 @@ __global__ void __launch_bounds__(kTqThreads) k_tile_quant(const Src src, const 
     uint4 v[8];
     {
       typename Src::Raw raw[8];
+      if constexpr (Src::kAhead) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (Src::kFetchAll) raw[i] = src.fetch(rw[i], col, col_ok);
-        else if (rw[i].ok && col_ok) raw[i] = src.fetch(rw[i], col, true);
+        for (int i = 0; i < 8; ++i) raw[i] = ahead[i];
+      } else {
+        fetch(raw, col, col_ok);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         v[i] = rw[i].ok && col_ok ? src.finish(raw[i], rw[i], col) : make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (Src::kAhead) {
+      if (sub + 1 < kSub && tc + 1 < sh.n_tc) fetch(ahead, col + kTq, col + kTq < sh.cols);
     }
 
     if (kRow || kY)
