@@ -17,6 +17,7 @@
 // The products run in the tiles of product.h.  Everything is added in a fixed
 // order: repeated calls give the same bits.
 
+#include "few_rows.h"
 #include "product.h"
 
 namespace mx {
@@ -105,35 +106,113 @@ struct XentEpi {
   }
 };
 
-// Joins a row's strips: 16 rows per workgroup, 16 threads to a row, each every
-// 16th strip in order, then the threads' sums in order.
-__global__ void __launch_bounds__(256) k_xent_join(const float2* __restrict__ part, int64_t rows, int32_t strips,
-                                                   const int32_t* __restrict__ targets, int64_t vocab,
-                                                   const float* __restrict__ zt, float* __restrict__ lse,
-                                                   float* __restrict__ lse_out, float* __restrict__ loss) {
-  __shared__ float2 sum[16][17];
+// (m, s) and another strip's (m, s) to those of both.  A sum of zero stands for
+// no words at all, whatever its m; a NaN is something.
+__device__ __forceinline__ void join_strip(float& m, float& s, float m2, float s2) {
+  const float n = fmaxf(s == 0.0f ? -INFINITY : m, s2 == 0.0f ? -INFINITY : m2);
+  s = (s == 0.0f ? 0.0f : s * exp_of(m - n)) + (s2 == 0.0f ? 0.0f : s2 * exp_of(m2 - n));
+  m = n;
+}
+
+// What k_skinny's sums become: a workgroup's strip of each row, in part [gridDim, M].
+struct FewXent {
+  const int32_t* targets;
+  float2* part;
+  float* zt;
+  struct Ahead {
+    int32_t t;
+  };
+  struct State {
+    float m = -INFINITY, s = 0.0f;
+  };
+  __device__ __forceinline__ Ahead fetch(bool in, int m, int64_t, int64_t) const { return Ahead{in ? targets[m] : -1}; }
+  __device__ __forceinline__ void finish(State& st, const Ahead& a, float (&v)[8], int m, int64_t j, int64_t N) const {
+    float top = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (j + k >= N) v[k] = -INFINITY;
+      else if (j + k == a.t) zt[m] = v[k];
+      top = fmaxf(top, v[k]);
+    }
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += exp_of(v[k] - ref);
+    join_strip(st.m, st.s, top, s);
+  }
+  __device__ __forceinline__ void end(State& st, float* lds, int m, int item, int64_t M) const {
+    float2* strips = reinterpret_cast<float2*>(lds);   // [2 kSkItems][kSkRows]
+    lds_barrier();   // (the sums have been read)
+    if (item < kSkItems && m < M) strips[(2 * item + (threadIdx.x & 1)) * kSkRows + m] = make_float2(st.m, st.s);
+    lds_barrier();
+    if ((int)threadIdx.x >= M) return;
+    float top = -INFINITY, s = 0.0f;
+    for (int k = 0; k < 2 * kSkItems; ++k) {
+      const float2 v = strips[k * kSkRows + threadIdx.x];
+      join_strip(top, s, v.x, v.y);
+    }
+    part[(int64_t)blockIdx.x * M + threadIdx.x] = make_float2(top, s);
+  }
+};
+
+// Joins the rows' strips, and beside that copies x with zeros in the rows without
+// a target: what they hold, infinities and NaN among it, must not reach dw (their
+// dz is zero, which does not hide them).
+struct JoinArgs {
+  const float2* part;       // [strips, rows]
+  int64_t rows;
+  int32_t strips;
+  const int32_t* targets;
+  int64_t vocab;
+  const float* zt;
+  float* lse;               // for the gradient, or null
+  float* lse_out;           // or null
+  float* loss;              // or null
+  uint32_t blocks;          // workgroups that join; those behind them copy
+  const uint16_t* x;
+  uint16_t* live;           // [rows, k]
+  int64_t k;
+};
+
+// 16 rows per workgroup, 64 threads to a row: each takes every 64th strip, eight
+// at a time, then the threads' strips are joined in a fixed order.
+__global__ void __launch_bounds__(1024) k_xent_join(const JoinArgs p) {
+  if (blockIdx.x >= p.blocks) {
+    const int64_t at = 8 * ((int64_t)(blockIdx.x - p.blocks) * 1024 + threadIdx.x);
+    if (at >= p.rows * p.k) return;
+    const int32_t t = p.targets[at / p.k];
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t >= 0 && t < p.vocab) v = *reinterpret_cast<const uint4*>(p.x + at);
+    *reinterpret_cast<uint4*>(p.live + at) = v;
+    return;
+  }
+  __shared__ float2 sum[16][16];
   const int rl = threadIdx.x & 15, sl = threadIdx.x >> 4;
   const int64_t i = 16 * (int64_t)blockIdx.x + rl;
   float m = -INFINITY, s = 0.0f;
-  auto add = [&](const float2& v) {
-    if (v.y == 0.0f) return;   // nothing in it (a NaN is something)
-    const float n = fmaxf(m, v.x);
-    s = (s == 0.0f ? 0.0f : s * exp_of(m - n)) + v.y * exp_of(v.x - n);
-    m = n;
-  };
-  if (i < rows) {
-#pragma unroll 4
-    for (int32_t k = sl; k < strips; k += 16) add(part[(int64_t)k * rows + i]);
+  if (i < p.rows) {
+    for (int32_t k0 = sl; k0 < p.strips; k0 += 8 * 64) {
+      float2 v[8];
+      float top = -INFINITY, add = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = k0 + 64 * k < p.strips ? p.part[(int64_t)(k0 + 64 * k) * p.rows + i] : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, v[k].y == 0.0f ? -INFINITY : v[k].x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add += v[k].y == 0.0f ? 0.0f : v[k].y * exp_of(v[k].x - top);
+      join_strip(m, s, top, add);
+    }
   }
-  sum[sl][rl] = make_float2(m, s);
+#pragma unroll
+  for (int d = 16; d < 64; d *= 2) join_strip(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64));
+  if ((threadIdx.x & 63) < 16) sum[threadIdx.x >> 6][rl] = make_float2(m, s);
   __syncthreads();
-  if (sl > 0 || i >= rows) return;
-  for (int k = 1; k < 16; ++k) add(sum[k][rl]);
+  if (sl > 0 || i >= p.rows) return;
+  for (int k = 1; k < 16; ++k) join_strip(m, s, sum[k][rl].x, sum[k][rl].y);
   const float l = m + logf(s);
-  const int32_t t = targets[i];
-  if (lse) lse[i] = l;
-  if (lse_out) lse_out[i] = l;
-  if (loss) loss[i] = t >= 0 && t < vocab ? l - zt[i] : 0.0f;
+  const int32_t t = p.targets[i];
+  if (p.lse) p.lse[i] = l;
+  if (p.lse_out) p.lse_out[i] = l;
+  if (p.loss) p.loss[i] = t >= 0 && t < p.vocab ? l - p.zt[i] : 0.0f;
 }
 
 // dz in place of the exponentials: a thread takes 8 columns of a row in each of
@@ -179,18 +258,6 @@ __global__ void __launch_bounds__(256) k_xent_dz(const float2* __restrict__ part
     }
     *reinterpret_cast<uint4*>(e + i * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
-}
-
-// x with zeros in the rows without a target: what they hold, infinities and NaN
-// among it, must not reach dw (their dz is zero, which does not hide them).
-__global__ void __launch_bounds__(256) k_live_rows(const uint16_t* __restrict__ x, const int32_t* __restrict__ targets,
-                                                   int64_t rows, int64_t vocab, int64_t k, uint16_t* __restrict__ out) {
-  const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-  if (at >= rows * k) return;
-  const int32_t t = targets[at / k];
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (t >= 0 && t < vocab) v = *reinterpret_cast<const uint4*>(x + at);
-  *reinterpret_cast<uint4*>(out + at) = v;
 }
 
 // The gradients' epilogue: out = add + sums, in bf16 or fp32.  J % 8 == 0.
@@ -276,8 +343,17 @@ struct XentSpace {
   int64_t e, part, row, x, acc, prod;   // bytes; row: of one float per row
 };
 
+// At most 16 rows without a gradient: w is streamed once through k_skinny.
+bool streamed(int64_t rows, int64_t k, bool grad) { return !grad && few_rows(rows, k); }
+
 XentSpace xent_space(int64_t rows, int64_t vocab, int64_t k, bool grad) {
   XentSpace s{};
+  if (streamed(rows, k, grad)) {
+    s.chunk = rows;
+    s.part = up(8 * (int64_t)skinny_grid(vocab) * rows, 256);
+    s.row = up(4 * rows, 256);
+    return s;
+  }
   s.chunk = chunk_rows(rows, vocab, k, grad);
   s.pitch = up(vocab, 8);
   const int64_t last = rows % s.chunk ? rows % s.chunk : s.chunk;
@@ -333,6 +409,7 @@ extern "C" int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t*
   if (!workspace || (int64_t)workspace_bytes < total(s)) return MX_EINVAL;
   for (int64_t r0 = 0; r0 < rows; r0 += s.chunk) {
     const int64_t r = rows - r0 < s.chunk ? rows - r0 : s.chunk;
+    if (streamed(rows, k, grad)) break;
     if (!tiles_fit(r, vocab, k) || (dx && !tiles_fit(r, k, vocab)) || (dw && !tiles_fit(vocab, k, r))) return MX_EUNSUPPORTED;
   }
   uint8_t* at = static_cast<uint8_t*>(workspace);
@@ -355,12 +432,20 @@ extern "C" int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t*
     const int32_t* tr = targets + r0;
     const XentArgs a{tr, part, zt, e, s.pitch};
     const Operand ox{xr, k}, ow{w, k};
-    int rc = grad ? launch_tiles<true, true, XentEpi<true>>(ox, ow, r, vocab, k, a, prod, st)
-                  : launch_tiles<true, true, XentEpi<false>>(ox, ow, r, vocab, k, a, prod, st);
+    JoinArgs j{part, r, 0, tr, vocab, zt, grad ? own_lse : nullptr, lse ? lse + r0 : nullptr, loss ? loss + r0 : nullptr,
+               (uint32_t)((r + 15) / 16), xr, xl, k};
+    int rc = MX_OK;
+    if (streamed(rows, k, grad)) {
+      j.strips = (int32_t)skinny_grid(vocab);
+      hipLaunchKernelGGL(k_skinny<FewXent>, dim3(j.strips), dim3(64 * kSkWaves), 0, st, xr, w, r, vocab, k, FewXent{tr, part, zt});
+    } else {
+      j.strips = strips_of(r, vocab, k);
+      rc = grad ? launch_tiles<true, true, XentEpi<true>>(ox, ow, r, vocab, k, a, prod, st)
+                : launch_tiles<true, true, XentEpi<false>>(ox, ow, r, vocab, k, a, prod, st);
+    }
     if (rc != MX_OK) return rc;
-    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((r + 15) / 16)), dim3(256), 0, st, part, r,
-                       strips_of(r, vocab, k), tr, vocab, zt, grad ? own_lse : nullptr, lse ? lse + r0 : nullptr,
-                       loss ? loss + r0 : nullptr);
+    const uint32_t copies = dw ? (uint32_t)((r * k / 8 + 1023) / 1024) : 0u;
+    hipLaunchKernelGGL(k_xent_join, dim3(j.blocks + copies), dim3(1024), 0, st, j);
     if (!grad) continue;
     const int tn = strip_cols(plan_product(r, vocab, k).shape), per = 256 / (tn / 8);
     const uint32_t bj = (uint32_t)((s.pitch + kDzStrips * tn - 1) / (kDzStrips * tn));
@@ -374,7 +459,6 @@ extern "C" int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t*
       if (rc != MX_OK) return rc;
     }
     if (dw) {
-      hipLaunchKernelGGL(k_live_rows, dim3((unsigned)((r * k / 8 + 255) / 256)), dim3(256), 0, st, xr, tr, r, vocab, k, xl);
       const bool last = r0 + r == rows;
       const SumArgs sum{r0 ? acc : nullptr, last ? static_cast<void*>(dw) : acc, !last};
       rc = launch_tiles<false, false, SumEpi>(dz, Operand{xl, k}, vocab, k, r, sum, prod, st);
