@@ -24,10 +24,12 @@ import torch
 from . import (MX_ACT_NONE, MX_OUT_BF16, MX_OUT_F32, _on, adamw_state, adamw_table, mx_adamw, mx_bf16_gather,
                mx_bf16_grouped_gemm_dgrad, mx_bf16_grouped_gemm_fwd, mx_bf16_grouped_gemm_wgrad, mx_bf16_linear,
                mx_bf16_linear_bwd, mx_bf16_linear_bwd_workspace_size, mx_bf16_linear_workspace_size,
-               mx_bf16_moe_tokens, mx_combine, mx_combine_bwd_quantize, mx_grouped_gemm_dgrad, mx_grouped_gemm_fwd,
-               mx_grouped_gemm_wgrad, mx_moe_tokens, mx_moe_tokens_workspace_size, mx_permute,
-               mx_permute_workspace_size, mx_quantize, mx_route_topk, mx_router_bwd, mx_swiglu_bwd_quantize,
-               mx_swiglu_quantize, scale_shape)
+               mx_bf16_moe_tokens, mx_bf16_xent, mx_bf16_xent_workspace_size, mx_combine, mx_combine_bwd_quantize,
+               mx_grouped_gemm_dgrad, mx_grouped_gemm_fwd, mx_grouped_gemm_wgrad, mx_moe_tokens,
+               mx_moe_tokens_workspace_size, mx_permute, mx_permute_workspace_size, mx_quantize, mx_requantize,
+               mx_rmsnorm, mx_rmsnorm_bwd, mx_rmsnorm_bwd_workspace_size, mx_route_topk, mx_router_bwd,
+               mx_router_bwd_dots, mx_swiglu_bwd_kept, mx_swiglu_bwd_kept_workspace_size, mx_swiglu_bwd_quantize,
+               mx_swiglu_keep, mx_swiglu_quantize, scale_shape)
 
 STAGES = ("quant_x", "permute", "quant_w", "gemm_fwd", "quant_dy", "gemm_dgrad", "quant_xt", "gemm_wgrad")
 
@@ -503,3 +505,136 @@ def token_step(b, x, wg, bg, w1, w2, residual=None, stream=None):
         mx_moe_tokens(x, b.logits, T, k, E, H, F, *w1, *w2, residual, b.out, b.ws, b.wsb, stream)
     else:
         mx_bf16_moe_tokens(x, b.logits, T, k, E, H, F, w1, w2, residual, b.out, b.ws, b.wsb, stream)
+
+
+# ---------------------------------------------------------------------------
+# A stack of such layers from the residual stream to the loss.  Each layer takes
+# the norm of the stream and adds its rows to it; behind the last stand a norm
+# and the cross entropy over a vocabulary.  What a layer keeps from its forward
+# to its backward is the stream in bf16, its tokens and its gate/up product in
+# MXFP8 and the routing tables; everything else is shared by the layers.
+# ---------------------------------------------------------------------------
+class LayerKept:
+    """What one layer of a stack keeps, and its gradients."""
+
+    def __init__(self, T, H, F, E, topk, device="cuda:0"):
+        cap = -(-(T * topk + 31 * E) // 32) * 32
+        bf, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        e = lambda *s, dt=u8: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        self.sum = e(T, H, dt=bf)                                  # the stream in front of the norm
+        self.xq, self.xs = e(T, H), e(*scale_shape(T, H))          # its norm, the layer's tokens
+        self.hq, self.hs = e(cap, 2 * F), e(*scale_shape(cap, 2 * F))
+        self.ids, self.weights = e(T, topk, dt=i32), e(T, topk, dt=f32)
+        self.off, self.dst, self.src = e(E + 1, dt=i32), e(T * topk, dt=i32), e(cap, dt=i32)
+        self.dnorm, self.dwg, self.dbg = e(H, dt=f32), e(E, H, dt=bf), e(E, dt=f32)
+        self.dw1, self.dw2 = e(E, 2 * F, H, dt=bf), e(E, H, F, dt=bf)
+
+
+class StackBuffers:
+    """Device buffers of a stack of `layers` layers over T tokens, allocated once: b.kept per layer, the rest shared."""
+
+    def __init__(self, T, H, F, E, topk, vocab, layers, device="cuda:0", eps=1e-6):
+        self.T, self.H, self.F, self.E, self.topk, self.vocab, self.eps = T, H, F, E, topk, vocab, eps
+        self.cap = cap = -(-(T * topk + 31 * E) // 32) * 32
+        bf, f32 = torch.bfloat16, torch.float32
+        e = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        pair = lambda r, c: (e(r, c), e(*scale_shape(r, c)))  # noqa: E731
+        self.kept = [LayerKept(T, H, F, E, topk, device) for _ in range(layers)]
+        self.x, self.logits, self.dlogits = e(T, H, dt=bf), e(T, E, dt=f32), e(T, E, dt=f32)
+        self.xp, self.xt = pair(cap, H), pair(H, cap)
+        self.w1, self.w1t = pair(E * 2 * F, H), pair(E * H, 2 * F)
+        self.w2, self.w2t = pair(E * H, F), pair(E * F, H)
+        # zeros where a grouped GEMM does not write and the next kernel reads
+        self.h, self.da = torch.zeros((cap, 2 * F), dtype=bf, device=device), torch.zeros((cap, F), dtype=bf, device=device)
+        self.a, self.at = pair(cap, F), pair(F, cap)
+        self.y, self.out, self.dxp = e(cap, H, dt=bf), e(T, H, dt=bf), e(cap, H, dt=bf)
+        self.dy, self.dyt = pair(cap, H), pair(H, cap)
+        self.dh, self.dht = pair(cap, 2 * F), pair(2 * F, cap)
+        self.dots, self.dx = e(cap, dt=f32), e(T, H, dt=bf)
+        self.sum, self.dsum, self.dnorm = e(T, H, dt=bf), e(T, H, dt=bf), e(H, dt=f32)
+        self.loss, self.lse, self.dwv = e(T, dt=f32), e(T, dt=f32), e(vocab, H, dt=bf)
+        self.wsb = max(mx_permute_workspace_size(T, topk, E), mx_bf16_linear_workspace_size(T, E, H),
+                       mx_bf16_linear_bwd_workspace_size(T, E, H, MX_ACT_NONE), mx_rmsnorm_bwd_workspace_size(T, H),
+                       mx_swiglu_bwd_kept_workspace_size(cap, F), mx_bf16_xent_workspace_size(T, vocab, H, True))
+        self.ws = e(max(self.wsb, 16))   # (the calls of a step are ordered: one workspace serves them all)
+
+
+def stack_layer_forward(b, kept, x, residual, norm, wg, bg, w1, w2, stream=None):
+    """One layer: the stream kept.sum = x + residual (x None: the residual alone), the layer of its norm into b.out.
+    wg, w1, w2 bf16 and norm, bg fp32, as in the layers above."""
+    T, H, F, E, k, cap, bf = b.T, b.H, b.F, b.E, b.topk, b.cap, MX_OUT_BF16
+    mx_rmsnorm(x, residual, bf, norm, T, H, b.eps, kept.sum, b.x, kept.xq, kept.xs, stream)
+    mx_bf16_linear(b.x, wg, bg, None, T, E, H, MX_ACT_NONE, None, b.logits, MX_OUT_F32, b.ws, b.wsb, stream)
+    mx_route_topk(b.logits, T, E, k, kept.ids, kept.weights, stream)
+    mx_permute(kept.xq, kept.xs, T, H, kept.ids, k, E, cap, *b.xp, kept.off, kept.dst, kept.src, b.ws, b.wsb, stream)
+    mx_quantize(w1, E, 2 * F, H, None, 2 * F, *b.w1, None, None, stream)
+    mx_grouped_gemm_fwd(*b.xp, *b.w1, kept.off, E, cap, 2 * F, H, b.h, bf, stream)
+    mx_swiglu_keep(b.h, cap, F, *b.a, kept.hq, kept.hs, stream)
+    mx_quantize(w2, E, H, F, None, H, *b.w2, None, None, stream)
+    mx_grouped_gemm_fwd(*b.a, *b.w2, kept.off, E, cap, H, F, b.y, bf, stream)
+    mx_combine(b.y, cap, H, kept.dst, kept.weights, T, k, b.out, stream)
+
+
+def stack_layer_backward(b, kept, norm, wg, w1, w2, stream=None):
+    """Backward of stack_layer_forward from what it kept: b.dsum, the gradient of the stream behind the layer, becomes
+    that of the stream in front of it; the weights' gradients go to kept."""
+    T, H, F, E, k, cap, bf = b.T, b.H, b.F, b.E, b.topk, b.cap, MX_OUT_BF16
+    mx_combine_bwd_quantize(b.dsum, kept.weights, kept.dst, kept.src, T, k, cap, H, None, *b.dy, *b.dyt, stream)
+    mx_quantize(w2, E, H, F, None, H, None, None, *b.w2t, stream)
+    mx_grouped_gemm_dgrad(*b.dy, *b.w2t, kept.off, E, cap, F, H, b.da, bf, stream)
+    mx_swiglu_bwd_kept(kept.hq, kept.hs, b.da, cap, F, *b.dh, *b.dht, *b.at, b.dots, b.ws, b.wsb, stream)
+    mx_router_bwd_dots(b.dots, cap, kept.dst, kept.ids, kept.weights, T, E, k, b.dlogits, stream)
+    mx_grouped_gemm_wgrad(*b.dyt, *b.at, kept.off, E, cap, H, F, kept.dw2, bf, stream)
+    mx_quantize(w1, E, 2 * F, H, None, 2 * F, None, None, *b.w1t, stream)
+    mx_grouped_gemm_dgrad(*b.dh, *b.w1t, kept.off, E, cap, H, 2 * F, b.dxp, bf, stream)
+    mx_requantize(kept.xq, kept.xs, T, H, kept.src, cap, *b.xt, stream)
+    mx_grouped_gemm_wgrad(*b.dht, *b.xt, kept.off, E, cap, 2 * F, H, kept.dw1, bf, stream)
+    mx_combine(b.dxp, cap, H, kept.dst, None, T, k, b.dx, stream)
+    # the gate's operand is the norm in bf16: formed again from the kept stream, bit for bit
+    mx_rmsnorm(kept.sum, None, bf, norm, T, H, b.eps, None, b.x, None, None, stream)
+    mx_bf16_linear_bwd(b.dlogits, MX_OUT_F32, None, b.x, wg, b.dx, T, E, H, MX_ACT_NONE, b.dx, kept.dwg, kept.dbg, b.ws,
+                       b.wsb, stream)
+    mx_rmsnorm_bwd(b.dx, kept.sum, b.dsum, bf, norm, T, H, b.eps, b.dsum, None, kept.dnorm, b.ws, b.wsb, stream)
+
+
+def stack_step(b, x, layers, norm, wv, targets, row_weight=None, stream=None):
+    """One forward + backward pass of the stack: x bf16 [T, H], layers a sequence of (norm, wg, bg, w1, w2) per layer,
+    norm fp32 [H] and wv bf16 [vocab, H] of the head, targets int32 [T], row_weight fp32 [T] (the gradient is that of
+    sum_i row_weight[i] b.loss[i]).  Leaves b.loss, b.dsum (of x), b.dwv, b.dnorm and the layers' gradients in b.kept."""
+    if len(layers) != len(b.kept):
+        raise ValueError(f"stack_step: {len(layers)} layers, buffers for {len(b.kept)}")
+    T, H, bf = b.T, b.H, MX_OUT_BF16
+    out, total = None, x
+    for kept, (n, wg, bg, w1, w2) in zip(b.kept, layers):
+        stack_layer_forward(b, kept, out, total, n, wg, bg, w1, w2, stream)
+        out, total = b.out, kept.sum
+    mx_rmsnorm(out, total, bf, norm, T, H, b.eps, b.sum, b.x, None, None, stream)
+    mx_bf16_xent(b.x, wv, targets, row_weight, T, b.vocab, H, b.loss, b.lse, b.dx, b.dwv, b.ws, b.wsb, stream)
+    mx_rmsnorm_bwd(b.dx, b.sum, None, bf, norm, T, H, b.eps, b.dsum, None, b.dnorm, b.ws, b.wsb, stream)
+    for kept, (n, wg, _, w1, w2) in reversed(list(zip(b.kept, layers))):
+        stack_layer_backward(b, kept, n, wg, w1, w2, stream)
+
+
+class TokenStackBuffers(TokenBuffers):
+    """Device buffers of the stack for T <= 64 tokens (scoring): TokenBuffers with the stream, its norm and the loss."""
+
+    def __init__(self, T, H, F, E, topk, vocab, device="cuda:0", eps=1e-6):
+        super().__init__(T, H, F, E, topk, device)
+        self.vocab, self.eps = vocab, eps
+        self.sum, self.x = (torch.empty((T, H), dtype=torch.bfloat16, device=device) for _ in range(2))
+        self.loss, self.lse = (torch.empty(T, dtype=torch.float32, device=device) for _ in range(2))
+        self.xent_wsb = mx_bf16_xent_workspace_size(T, vocab, H, False)
+        self.xent_ws = torch.empty(max(self.xent_wsb, 16), dtype=torch.uint8, device=device)
+
+
+def token_stack_step(b, x, layers, norm, wv, targets, stream=None):
+    """The stack's forward for a few tokens: layers of (norm, wg, bg, w1, w2) with w1, w2 as in token_step.  Leaves
+    b.loss, minus the log probability of each target, and b.lse."""
+    T, H, bf = b.T, b.H, MX_OUT_BF16
+    out, total = None, x
+    for n, wg, bg, w1, w2 in layers:
+        mx_rmsnorm(out, total, bf, n, T, H, b.eps, b.sum, b.x, None, None, stream)
+        token_step(b, b.x, wg, bg, w1, w2, None, stream)
+        out, total = b.out, b.sum
+    mx_rmsnorm(out, total, bf, norm, T, H, b.eps, b.sum, b.x, None, None, stream)
+    mx_bf16_xent(b.x, wv, targets, None, T, b.vocab, H, b.loss, b.lse, None, None, b.xent_ws, b.xent_wsb, stream)
