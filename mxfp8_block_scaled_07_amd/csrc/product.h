@@ -192,14 +192,19 @@ constexpr int kStageBytes = 32 * (kStageCols<TN> * 4 + 16);
 // row of tiles): its loads are non-temporal.
 enum { kOnceNone, kOnceA, kOnceB };
 
-// BM x BN result tile, kWm x kWn waves, kSlots LDS tiles of kC contraction
-// elements in flight.
+// BM x BN result tile, kWm x kWn waves, LDS for kSlots tiles of kC contraction
+// elements; kSlots 0: for two and a half tiles, five halves (A or B) in a ring, so
+// that A is on the way for two tiles' time, B for one, and only B's loads are
+// waited for at short notice (two whole slots: one tile's time for both).
 template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, class E, int kOnce>
 __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::Args> p) {
   constexpr int kNw = kWm * kWn;
   constexpr int TM = BM / kWm, TN = BN / kWn, FM = TM / 32, FN = TN / 32;
   constexpr int kABytes = BM * kC * 2, kSlot = (BM + BN) * kC * 2;
-  constexpr int kLds = kSlots * kSlot > kNw * kStageBytes<TN> ? kSlots * kSlot : kNw * kStageBytes<TN>;
+  constexpr bool kHalves = kSlots == 0;
+  static_assert(!kHalves || BM == BN, "halves of one size");
+  constexpr int kRing = kHalves ? 5 * kABytes : kSlots * kSlot;
+  constexpr int kLds = kRing > kNw * kStageBytes<TN> ? kRing : kNw * kStageBytes<TN>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -241,82 +246,143 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.f;
 
-  // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.
-  constexpr int kLa = decltype(la)::kLoads;
+  // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
+  // are read during the part before it, and the loads into what the last tile
+  // left are spread over a tile's parts, all placed between the products: a
+  // burst of either stalls the products behind it.
+  constexpr int kLa = decltype(la)::kLoads, kLb = decltype(lb)::kLoads;
+  constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
   typename decltype(la)::Tile ta;
   typename decltype(lb)::Tile tb;
-  uint32_t dst = 0;
-  auto load = [&](int i) {   // load i of the tile in hand
-    if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, dst);
-    else lb.template load<kOnce == kOnceB>(tb, i - kLa, dst + kABytes);
-  };
-  auto hand = [&](int64_t t, int s) {
-    ta = la.prepare(t, p.C);
-    tb = lb.prepare(t, p.C);
-    dst = base + (uint32_t)s * kSlot;
-  };
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s)
-    if (t0 + s < t1) {
-      hand(t0 + s, s);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(i);
-    }
-  if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
-  else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  bare_barrier();
-
-  // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
-  // are read during the part before it, and the loads into the slot that the
-  // last tile left are spread over a tile's parts, all placed between the
-  // products: a burst of either stalls the products behind it.
-  constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
-  // with two slots a tile has one tile's time to arrive: its loads all go into the first part
-  constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
   v8bf a[2][FM], b[2][FN];
-  // part of fragments q; `tile` and kk: where part 1 - q is read; loads from `first` on
-  auto part = [&](int q, const uint8_t* tile, int kk, bool fill, int first) {
+  // part of fragments q; ap, bp and kk: where part 1 - q is read; loads: `count` of load(first ..)
+  auto part = [&](int q, const uint8_t* ap, const uint8_t* bp, int kk, bool fill, int first, int count, auto load) {
 #pragma unroll
     for (int i = 0; i < kMfma; ++i) {
       const int m = i / FN, n = i % FN;
       acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[q][n], a[q][m], acc[m][n], 0, 0, 0);
 #pragma unroll
       for (int f = i * kFrags / kMfma; f < (i + 1) * kFrags / kMfma; ++f) {
-        if (f < FN) b[1 - q][f] = fb.read(tile + kABytes, wn * TN + 32 * f, kk);
-        else a[1 - q][f - FN] = fa.read(tile, wm * TM + 32 * (f - FN), kk);
+        if (f < FN) b[1 - q][f] = fb.read(bp, wn * TN + 32 * f, kk);
+        else a[1 - q][f - FN] = fa.read(ap, wm * TM + 32 * (f - FN), kk);
       }
       if (fill) {
 #pragma unroll
-        for (int l = i * kPerPart / kMfma; l < (i + 1) * kPerPart / kMfma; ++l)
-          if (first + l < kLoads) load(first + l);
+        for (int l = i * count / kMfma; l < (i + 1) * count / kMfma; ++l) load(first + l);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // the first tile's first fragments
+  auto start = [&] {
 #pragma unroll
-  for (int n = 0; n < FN; ++n) b[0][n] = fb.read(lds + kABytes, wn * TN + 32 * n, 0);
+    for (int n = 0; n < FN; ++n) b[0][n] = fb.read(lds + kABytes, wn * TN + 32 * n, 0);
 #pragma unroll
-  for (int m = 0; m < FM; ++m) a[0][m] = fa.read(lds, wm * TM + 32 * m, 0);
-  int slot = 0;
-  bool fill = false;   // whether the tile in hand is loaded
-  for (int64_t t = t0; t < t1; ++t) {
-    const uint8_t* tile = lds + slot * kSlot;
-    const int next = slot + 1 == kSlots ? 0 : slot + 1;
+    for (int m = 0; m < FM; ++m) a[0][m] = fa.read(lds, wm * TM + 32 * m, 0);
+  };
+
+  if constexpr (kHalves) {
+    // The ring takes A(t0), B(t0), A(t0 + 1), B(t0 + 1), ...: tile t's A in place
+    // 2 (t - t0) mod 5, its B behind it.
+    uint32_t da = 0, db = 0;
+    auto load_a = [&](int i) {
+      if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, da);
+    };
+    auto load_b = [&](int i) { lb.template load<kOnce == kOnceB>(tb, i, db); };
+    auto hand_a = [&](int64_t t, int at) {
+      ta = la.prepare(t, p.C);
+      da = base + (uint32_t)(at * kABytes);
+    };
+    auto hand_b = [&](int64_t t, int at) {
+      tb = lb.prepare(t, p.C);
+      db = base + (uint32_t)(at * kABytes);
+    };
 #pragma unroll
-    for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, kk, fill, kk * kPerPart);
-    // this wave has read its share of the slot, and its loads of tile t + 1
-    // are done (the kSlots - 2 tiles after it may be in flight; near the end
-    // fewer are, so everything is waited for) ...
-    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-    if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
+    for (int s = 0; s < 3; ++s)
+      if (t0 + s < t1) {
+        hand_a(t0 + s, 2 * s);
+#pragma unroll
+        for (int i = 0; i < kLa; ++i) load_a(i);
+        if (s < 2) {
+          hand_b(t0 + s, 2 * s + 1);
+#pragma unroll
+          for (int i = 0; i < kLb; ++i) load_b(i);
+        }
+      }
+    if (t0 + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kLa + kLb));   // tile t0 is there
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    // ... and after the barrier every wave's: the slot takes tile t + kSlots
     bare_barrier();
-    fill = t + kSlots < t1;
-    hand(t + kSlots, slot);
-    // (after the last tile this reads an old slot, which is not used)
-    part(1, lds + next * kSlot, 0, fill, 0);
-    slot = next;
+    start();
+    int at = 0;          // A's place
+    bool fill = false;   // whether A of tile t + 2 is still to be loaded
+    auto place = [](int v) { return v >= 5 ? v - 5 : v; };
+    constexpr int kPer = (kLa + kParts - 2) / (kParts - 1);
+    for (int64_t t = t0; t < t1; ++t) {
+      const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
+#pragma unroll
+      for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, ap, bp, kk, fill, (kk - 1) * kPer, kPer, load_a);
+      // this wave has read its share of tile t, and its loads of tile t + 1 are
+      // done (A of tile t + 2 may be in flight) ...
+      __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+      if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
+      else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      // ... and after the barrier every wave's: B of tile t + 2 goes where A of
+      // tile t was, A of tile t + 3 where its B was
+      bare_barrier();
+      hand_b(t + 2, at);
+      hand_a(t + 3, place(at + 1));
+      fill = t + 3 < t1;
+      at = place(at + 2);
+      // (after the last tile this reads old halves, which are not used)
+      part(1, lds + at * kABytes, lds + place(at + 1) * kABytes, 0, t + 2 < t1, 0, kLb, load_b);
+    }
+  } else {
+    // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.
+    uint32_t dst = 0;
+    auto load = [&](int i) {   // load i of the tile in hand
+      if (i >= kLoads) return;
+      if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, dst);
+      else lb.template load<kOnce == kOnceB>(tb, i - kLa, dst + kABytes);
+    };
+    auto hand = [&](int64_t t, int s) {
+      ta = la.prepare(t, p.C);
+      tb = lb.prepare(t, p.C);
+      dst = base + (uint32_t)s * kSlot;
+    };
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+      if (t0 + s < t1) {
+        hand(t0 + s, s);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i);
+      }
+    if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    bare_barrier();
+    // with two slots a tile has one tile's time to arrive: its loads all go into the first part
+    constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
+    start();
+    int slot = 0;
+    bool fill = false;   // whether the tile in hand is loaded
+    for (int64_t t = t0; t < t1; ++t) {
+      const uint8_t* tile = lds + slot * kSlot;
+      const int next = slot + 1 == kSlots ? 0 : slot + 1;
+#pragma unroll
+      for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, tile + kABytes, kk, fill, kk * kPerPart, kPerPart, load);
+      // this wave has read its share of the slot, and its loads of tile t + 1
+      // are done (the kSlots - 2 tiles after it may be in flight; near the end
+      // fewer are, so everything is waited for) ...
+      __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+      if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
+      else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      // ... and after the barrier every wave's: the slot takes tile t + kSlots
+      bare_barrier();
+      fill = t + kSlots < t1;
+      hand(t + kSlots, slot);
+      // (after the last tile this reads an old slot, which is not used)
+      part(1, lds + next * kSlot, lds + next * kSlot + kABytes, 0, fill, 0, kPerPart, load);
+      slot = next;
+    }
   }
   __syncthreads();
 
@@ -467,7 +533,7 @@ int launch_tiles(const Operand& a, const Operand& b, int64_t I, int64_t J, int64
   p.split_c = pl.split_c;
   p.part = part;
   switch (pl.shape) {
-    case k256x256: launch_shape<256, 256, 2, 4, 64, 2, kARows, kBRows, E>(p, st); break;
+    case k256x256: launch_shape<256, 256, 2, 4, 64, 0, kARows, kBRows, E>(p, st); break;
     case k128x128: launch_shape<128, 128, 2, 2, 64, 2, kARows, kBRows, E>(p, st); break;
     case k128x64: launch_narrow<128, 64, 5, kARows, kBRows, E>(p, st); break;
     case k64x128: launch_narrow<64, 128, 5, kARows, kBRows, E>(p, st); break;
