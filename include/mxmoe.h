@@ -427,6 +427,7 @@ int mx_bf16_linear_bwd(const void* dout, int32_t dout_dtype, const uint16_t* z, 
  *   row_q/row_s    rowwise MX of A [rows, F], as mx_swiglu_quantize gives it
  *   keep_q/keep_s  rowwise MX of h [rows, 2F], as mx_quantize gives it
  * Requires F % 32 == 0; h 16-byte, codes 8-byte, scales 4-byte aligned.
+ * MX_EUNSUPPORTED for F > 2^22 and about rows * F >= 2^35.
  */
 int mx_swiglu_keep(const uint16_t* h, int64_t rows, int64_t F, uint8_t* row_q, uint8_t* row_s, uint8_t* keep_q,
                    uint8_t* keep_s, mx_stream_t stream);

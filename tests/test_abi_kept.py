@@ -62,4 +62,5 @@ def test_sizes(lib):  # noqa: F811
     assert n(64, 128) == 0 and n(64, 160) == 64 * 2 * 4 and n(64, 1408) == 64 * 11 * 4
     for bad in ((0, 160), (-1, 160), (64, 0), (64, 40), (64, (1 << 22) + 32)):
         assert n(*bad) == 0
-    assert bwd(lib, F=(1 << 22) + 32) == mxa.MX_EUNSUPPORTED
+    assert bwd(lib, F=(1 << 22) + 32) == mxa.MX_EUNSUPPORTED and keep(lib, F=(1 << 22) + 32) == mxa.MX_EUNSUPPORTED
+    assert keep(lib, R=1 << 28, F=128) == mxa.MX_EUNSUPPORTED and keep(lib, R=1 << 62, F=32) == mxa.MX_EUNSUPPORTED
