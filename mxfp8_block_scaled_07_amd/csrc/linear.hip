@@ -234,6 +234,7 @@ __device__ __forceinline__ void epilogue(const Epi& e, v16f (&acc)[TM / 32][TN /
 template <int kAct>
 struct Dense {
   typedef Epi Args;
+  static constexpr int kSide = 32;   // (the other shape's sums run in another order)
   template <int TM, int TN, typename Sums>
   __device__ static __forceinline__ void run(const Epi& e, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
                                              int64_t j0, int64_t I, int64_t J, Sums sums) {

@@ -11,6 +11,7 @@
 //
 // What becomes of the sums is an epilogue's matter, a class E with
 //   struct Args;                     passed by value to the kernels
+//   kSide                            32 or 16: the 256 x 256 tiles' matrix instruction
 //   template <int TM, int TN, typename Sums>
 //   static void run(const Args&, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0, int64_t j0, int64_t I,
 //                   int64_t J, Sums sums);
@@ -26,6 +27,7 @@ namespace mx {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
@@ -74,11 +76,14 @@ __device__ __forceinline__ void bare_barrier() {
 // consecutive c at once, which the swizzle moves to different 64-byte banks.
 template <int kC>
 __device__ __forceinline__ int row_swizzle(int r) { return kC == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
-template <int R>
-__device__ __forceinline__ int col_swizzle(int c) { return R >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2; }
+// (Fragments of 16 columns take 32 bytes of c and of c + 8, which it parts too.)
+template <int R, int kSide>
+__device__ __forceinline__ int col_swizzle(int c) {
+  return (R >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2) | (kSide == 16 ? ((c >> 3) & 1) << 1 : 0);
+}
 
 // The LDS-direct loads of one operand tile: kLoads per wave and 64-c tile.
-template <bool kRows, int R, int kNw, int kC>
+template <bool kRows, int R, int kNw, int kC, int kSide = 32>
 struct TileLoads {
   static constexpr int kLoads = R * kC * 2 / 1024 / kNw;
   static_assert(R * kC * 2 % (1024 * kNw) == 0, "whole loads per wave");
@@ -115,7 +120,7 @@ struct TileLoads {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int c = kRowsPer * (w + kNw * i) + lane / kPer;
-        const int ch = (lane % kPer) ^ col_swizzle<R>(c);
+        const int ch = (lane % kPer) ^ col_swizzle<R, kSide>(c);
         // columns past the operand's are other rows' data, or past the end: masked
         voff[i] = first + 8 * ch < n ? (uint32_t)c * (uint32_t)o.ld * 2u + 16u * (uint32_t)ch : kOob;
       }
@@ -150,32 +155,34 @@ struct TileLoads {
   }
 };
 
-// Lane offsets of a 32 (i) x 16 (c) fragment; kk = 0..3 in a 64-c tile.
-template <bool kRows, int R, int kC>
+// Lane offsets of a fragment of kSide (i) x 512 / kSide (c), its number in the
+// tile's contraction kk: 32 x 16 or 16 x 32.
+template <bool kRows, int R, int kC, int kSide = 32>
 struct FragAt {
+  static constexpr int kK = 512 / kSide;
   int row, sw, lo, hi;
   __device__ void init() {
     const int lane = threadIdx.x & 63;
     if constexpr (kRows) {
-      row = (lane & 31) * (2 * kC);
-      sw = row_swizzle<kC>(lane & 31);
-      lo = lane >> 5;
+      row = (lane & (kSide - 1)) * (2 * kC);
+      sw = row_swizzle<kC>(lane & (kSide - 1));
+      lo = lane / kSide;
     } else {
-      const int l = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
+      const int l = lane & 15, half = kSide == 32 ? (lane >> 4) & 1 : 0, h = lane / kSide;
       const int c = 8 * h + (l >> 2);
       row = c * (2 * R);
-      sw = col_swizzle<R>(c);
-      lo = 2 * half + ((l & 3) >> 1);   // 16-byte chunk inside the fragment's 32 columns
+      sw = col_swizzle<R, kSide>(c);
+      lo = 2 * half + ((l & 3) >> 1);   // 16-byte chunk inside the fragment's columns
       hi = 8 * (l & 1);
     }
   }
-  // i0: the fragment's first row inside the tile, a multiple of 32
+  // i0: the fragment's first row inside the tile, a multiple of kSide
   __device__ v8bf read(const uint8_t* tile, int i0, int kk) const {
     if constexpr (kRows) {
-      return *reinterpret_cast<const v8bf*>(tile + i0 * (2 * kC) + row + 16 * ((2 * kk + lo) ^ sw));
+      return *reinterpret_cast<const v8bf*>(tile + i0 * (2 * kC) + row + 16 * ((kK / 8 * kk + lo) ^ sw));
     } else {
-      const uint8_t* p = tile + kk * 16 * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
-      // c .. c + 3 and c + 4 .. c + 7: the swizzle depends on c & 3 only
+      const uint8_t* p = tile + kk * kK * 2 * R + row + 16 * ((i0 / 8 + lo) ^ sw) + hi;
+      // c .. c + 3 and c + 4 .. c + 7: the swizzle does not depend on c & 4
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
       const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * R));
       return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -196,6 +203,13 @@ enum { kOnceNone, kOnceA, kOnceB };
 // elements; kSlots 0: for two and a half tiles, five halves (A or B) in a ring, so
 // that A is on the way for two tiles' time, B for one, and only B's loads are
 // waited for at short notice (two whole slots: one tile's time for both).
+//
+// What bounds the large products is the power of the matrix units: 4096 x 65536 x
+// 5120 takes 2.05 ms with normal values and 1.52 ms with zeros, all else alike.
+// From registers 16 x 16 x 32 reaches 2.1 PFLOP/s where 32 x 32 x 16 reaches 1.85
+// (zeros: 2.4 both); in this loop they take 1.99 ms and 2.09 ms.  4 waves of 128 x
+// 128 read a third less from LDS and take 2.17 ms (one wave of a SIMD has nothing
+// beside it at a wait).
 template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, class E, int kOnce>
 __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::Args> p) {
   constexpr int kNw = kWm * kWn;
@@ -227,14 +241,15 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
   const int64_t t0 = whole ? 0 : (int64_t)split * (p.split_c / kC);
   const int64_t t1 = whole || t0 + p.split_c / kC > all ? all : t0 + p.split_c / kC;
 
-  TileLoads<kARows, BM, kNw, kC> la;
-  TileLoads<kBRows, BN, kNw, kC> lb;
+  constexpr int kSide = kHalves ? E::kSide : 32;
+  TileLoads<kARows, BM, kNw, kC, kSide> la;
+  TileLoads<kBRows, BN, kNw, kC, kSide> lb;
   la.init(p.a, i0, p.I, p.C);
   lb.init(p.b, j0, p.J, p.C);
-  constexpr int kLoads = TileLoads<kARows, BM, kNw, kC>::kLoads + TileLoads<kBRows, BN, kNw, kC>::kLoads;
+  constexpr int kLoads = decltype(la)::kLoads + decltype(lb)::kLoads;
   const uint32_t base = (uint32_t)(uintptr_t)(const lds_void*)lds;
-  FragAt<kARows, BM, kC> fa;
-  FragAt<kBRows, BN, kC> fb;
+  FragAt<kARows, BM, kC, kSide> fa;
+  FragAt<kBRows, BN, kC, kSide> fb;
   fa.init();
   fb.init();
 
@@ -312,29 +327,110 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
     if (t0 + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kLa + kLb));   // tile t0 is there
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     bare_barrier();
-    start();
     int at = 0;          // A's place
     bool fill = false;   // whether A of tile t + 2 is still to be loaded
     auto place = [](int v) { return v >= 5 ? v - 5 : v; };
-    constexpr int kPer = (kLa + kParts - 2) / (kParts - 1);
-    for (int64_t t = t0; t < t1; ++t) {
-      const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
+    if constexpr (kSide == 16) {
+      // Two parts of 32 c.  A fragment of A is used by one row of products and read
+      // anew behind it; those of B have two sets.
+      constexpr int GM = TM / 16, GN = TN / 16, kAhead = 2, kLeft = GM - kAhead;
+      static_assert(kParts == 4, "two parts of 32 c");
+      v4f s[GM][GN];
+      v8bf x[GM], y[2][GN];
 #pragma unroll
-      for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, ap, bp, kk, fill, (kk - 1) * kPer, kPer, load_a);
-      // this wave has read its share of tile t, and its loads of tile t + 1 are
-      // done (A of tile t + 2 may be in flight) ...
-      __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-      if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
-      else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-      // ... and after the barrier every wave's: B of tile t + 2 goes where A of
-      // tile t was, A of tile t + 3 where its B was
-      bare_barrier();
-      hand_b(t + 2, at);
-      hand_a(t + 3, place(at + 1));
-      fill = t + 3 < t1;
-      at = place(at + 2);
-      // (after the last tile this reads old halves, which are not used)
-      part(1, lds + at * kABytes, lds + place(at + 1) * kABytes, 0, t + 2 < t1, 0, kLb, load_b);
+      for (int n = 0; n < GN; ++n) y[0][n] = fb.read(lds + kABytes, wn * TN + 16 * n, 0);
+#pragma unroll
+      for (int m = 0; m < GM; ++m) {
+        x[m] = fa.read(lds, wm * TM + 16 * m, 0);
+#pragma unroll
+        for (int n = 0; n < GN; ++n) s[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+      auto row = [&](int q, int m) {
+#pragma unroll
+        for (int i = 0; i < GN; ++i) {
+          const int n = m & 1 ? GN - 1 - i : i;
+          s[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[q][n], x[m], s[m][n], 0, 0, 0);
+        }
+      };
+      for (int64_t t = t0; t < t1; ++t) {
+        const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
+#pragma unroll
+        for (int m = 0; m < GM; ++m) {
+          row(0, m);
+#pragma unroll
+          for (int n = m * GN / GM; n < (m + 1) * GN / GM; ++n) y[1][n] = fb.read(bp, wn * TN + 16 * n, 1);
+          x[m] = fa.read(ap, wm * TM + 16 * m, 1);
+          if (fill) {
+#pragma unroll
+            for (int l = m * kLa / GM; l < (m + 1) * kLa / GM; ++l) load_a(l);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) row(1, m);
+        // as below: the waits stand behind the second part's first products
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+        if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        bare_barrier();
+        hand_b(t + 2, at);
+        hand_a(t + 3, place(at + 1));
+        fill = t + 3 < t1;
+        at = place(at + 2);
+        ap = lds + at * kABytes;
+        bp = lds + place(at + 1) * kABytes;
+#pragma unroll
+        for (int m = kAhead; m < GM; ++m) {
+          row(1, m);
+          const int k = m - kAhead;
+#pragma unroll
+          for (int n = k * GN / kLeft; n < (k + 1) * GN / kLeft; ++n) y[0][n] = fb.read(bp, wn * TN + 16 * n, 0);
+#pragma unroll
+          for (int i = k * GM / kLeft; i < (k + 1) * GM / kLeft; ++i) x[i] = fa.read(ap, wm * TM + 16 * i, 0);
+          if (t + 2 < t1) {
+#pragma unroll
+            for (int l = k * kLb / kLeft; l < (k + 1) * kLb / kLeft; ++l) load_b(l);
+          }
+        }
+      }
+      // to the layout of the 32 x 32 instruction: there the lane's bits 4 and 5 are
+      // i's bit 4 and j's bit 2, here j's bits 2 and 3
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const auto u = __builtin_amdgcn_permlane16_swap(__float_as_uint(s[2 * m][2 * n + g][r]),
+                                                              __float_as_uint(s[2 * m + 1][2 * n + g][r]), false, false);
+              const auto v = __builtin_amdgcn_permlane32_swap(u[0], u[1], false, false);
+              acc[m][n][8 * g + r] = __uint_as_float(v[0]);
+              acc[m][n][8 * g + 4 + r] = __uint_as_float(v[1]);
+            }
+    } else {
+      start();
+      constexpr int kPer = (kLa + kParts - 2) / (kParts - 1);
+      for (int64_t t = t0; t < t1; ++t) {
+        const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
+#pragma unroll
+        for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, ap, bp, kk, fill, (kk - 1) * kPer, kPer, load_a);
+        // this wave has read its share of tile t, and its loads of tile t + 1 are
+        // done (A of tile t + 2 may be in flight) ...
+        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+        if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        // ... and after the barrier every wave's: B of tile t + 2 goes where A of
+        // tile t was, A of tile t + 3 where its B was
+        bare_barrier();
+        hand_b(t + 2, at);
+        hand_a(t + 3, place(at + 1));
+        fill = t + 3 < t1;
+        at = place(at + 2);
+        // (after the last tile this reads old halves, which are not used)
+        part(1, lds + at * kABytes, lds + place(at + 1) * kABytes, 0, t + 2 < t1, 0, kLb, load_b);
+      }
     }
   } else {
     // Tiles t0 .. t0 + kSlots - 1 into the slots; tile t0 has to be there.

@@ -45,6 +45,7 @@ struct XentArgs {
 template <bool kGrad>
 struct XentEpi {
   typedef XentArgs Args;
+  static constexpr int kSide = 16;
   template <int TM, int TN, typename Sums>
   __device__ static __forceinline__ void run(const XentArgs& p, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
                                              int64_t j0, int64_t I, int64_t J, Sums sums) {
@@ -269,6 +270,7 @@ struct SumArgs {
 
 struct SumEpi {
   typedef SumArgs Args;
+  static constexpr int kSide = 16;
   template <int TM, int TN, typename Sums>
   __device__ static __forceinline__ void run(const SumArgs& p, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
                                              int64_t j0, int64_t I, int64_t J, Sums sums) {
