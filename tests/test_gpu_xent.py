@@ -92,6 +92,12 @@ def test_tiles_of_256():
     Case(2100, 8200, 64).check()
 
 
+@pytest.mark.parametrize("M,V,K", [(2050, 6100, 2080), (4100, 1030, 4128), (1030, 4100, 4128)])
+def test_long_contractions_in_tiles_of_256(M, V, K):
+    """The three products, whole tiles and split ones, contractions that end inside a step."""
+    Case(M, V, K).check()
+
+
 @pytest.mark.parametrize("kw", [dict(ignored=0.0, weighted=False), dict(ignored=1.0), dict(std=0.0), dict(std=40.0),
                                 dict(ignored=0.0, std=12.0)])
 def test_inputs(kw):
