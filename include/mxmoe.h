@@ -489,8 +489,9 @@ int mx_requantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols
  *   y        optional bf16 [rows, cols]
  *   row_q/row_s  optional rowwise MX of y (exactly the quantize of the bf16 y,
  *            whether or not y is written): codes [rows, cols], scales
- * fp32 sums in a fixed order.  At least one output; cols % 32 == 0; eps >= 1e-37;
- * tensors 16-byte, row_q 8-byte, weight and row_s 4-byte aligned.
+ * fp32 sums in a fixed order (a row whose squares add up past fp32's range gives
+ * y = 0).  At least one output; cols % 32 == 0; eps >= 1e-37; tensors 16-byte,
+ * row_q 8-byte, weight and row_s 4-byte aligned.
  * MX_EUNSUPPORTED for cols > 65536 or rows >= 2^31.
  */
 int mx_rmsnorm(const uint16_t* x, const void* residual, int32_t stream_dtype, const float* weight, int64_t rows,

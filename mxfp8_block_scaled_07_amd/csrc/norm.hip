@@ -150,7 +150,8 @@ struct Norm {
 
 // Workgroup b takes rows b, b + gridDim, ...: the card walks through the rows
 // together, the next row on the way while one is finished (two rows ahead
-// measure the same).
+// measure the same).  32768 x 7168 with every output: 372 us, 5.7 TB/s (a copy
+// reaches 6.6); rows above 32768 columns overflow the registers, 2.9 TB/s at 65536.
 template <int N, bool kF32>
 __global__ void __launch_bounds__(1024) k_rmsnorm(const Norm p) {
   __shared__ float slots[2][kMaxWaves][1];
@@ -236,6 +237,9 @@ struct NormBwd {
   float* part;             // [workgroups, cols] or null
 };
 
+// The same walk; a thread adds up its columns of dw over the workgroup's rows, and
+// k_norm_join the workgroups' sums.  32768 x 7168 with dsum: 298 us, 6.3 TB/s; rows
+// above 16384 columns overflow the registers (1.7 TB/s at 32768, 0.7 at 65536).
 template <int N, bool kF32>
 __global__ void __launch_bounds__(1024) k_rmsnorm_bwd(const NormBwd p) {
   __shared__ float slots[2][kMaxWaves][2];

@@ -541,7 +541,7 @@ constexpr struct {
   double us;            // microseconds per 64 c of a round with all slots busy and operands in L2
   double stream;        // bytes per microsecond at which it streams operands that are read once
 } kShape[kShapes] = {
-    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 570 us, against 710 with 128 x 128 and 1240 with 64 x 64
+    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 535 us, against 710 with 128 x 128 and 1240 with 64 x 64
     {128, 128, 2, 1.13, 4.9e6},
     {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 107 with 128 x 128
     {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
