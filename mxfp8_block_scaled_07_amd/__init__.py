@@ -104,11 +104,17 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+_current = None   # torch's (raw stream of a device, current device)
+
+
 def _s(stream):
     if stream is not None:
         return int(stream)
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # torch.cuda.current_stream().cuda_stream
+    global _current
+    if _current is None:
+        import torch
+        _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _current[0](_current[1]())   # torch.cuda.current_stream().cuda_stream
 
 
 def _check(rc, name):
