@@ -138,16 +138,21 @@ __device__ __forceinline__ float row16_sum(float v) {
 
 // The backward in the quantizer's tiles of 128 rows x 128 columns: dH's two halves
 // and A' are made from one reading of the codes and of dA, held in registers as
-// bf16, and go out by rows and, through LDS, by columns.  67,584 x 2048: 275 us,
-// 4.6 TB/s; the arithmetic bounds it (65 instructions an element, exponential and
-// five quantizes among them: 240 us of the vector units' issue).  Left to itself
+// bf16, and go out by rows and, through LDS, by columns.  67,584 x 2048: 271 us,
+// 4.7 TB/s; the arithmetic bounds it (65 instructions an element, exponential and
+// five quantizes among them: 230 us of the vector units' issue).  Left to itself
 // the compiler took 512 registers and spilled; bound to three tiles a CU it does not.
+// A row's tiles on one XCD and non-temporal columns leave whole lines as they are
+// and mend shared ones: 67,584 x 2080 takes 295 us, 343 without.
 template <bool kWhole>
 __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kTq * kTq * 2];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ch = lane & 15;
-  const int32_t tc = (int32_t)(blockIdx.x % (uint32_t)p.n_tc);
-  const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)p.n_tc) * kTq, r = r0 + 32 * w + 8 * (lane >> 4);
+  // workgroup b runs on XCD b % 8: each takes a run of the tiles, by rows
+  const uint32_t xcd = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8;
+  const uint32_t b = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8;
+  const int32_t tc = (int32_t)(b % (uint32_t)p.n_tc);
+  const int64_t r0 = (int64_t)(b / (uint32_t)p.n_tc) * kTq, r = r0 + 32 * w + 8 * (lane >> 4);
   const int64_t F = p.F, c0 = (int64_t)tc * kTq, col = c0 + 8 * ch;
   const bool col_ok = col < F;
   uint2 gq[8], uq[8];
@@ -216,13 +221,13 @@ __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd
     store_half<kWhole>(vu, p.row_q, p.row_s, p.rows, F, r, F, c0, col_ok);
   }
   if (p.col_q) {
-    tq_store_cols<false>(vg, lds, p.col_q, p.col_s, 2 * F, c0, F - c0, p.rows, r0);
+    tq_store_cols<true>(vg, lds, p.col_q, p.col_s, 2 * F, c0, F - c0, p.rows, r0);
     __syncthreads();
-    tq_store_cols<false>(vu, lds, p.col_q, p.col_s, 2 * F, F + c0, F - c0, p.rows, r0);
+    tq_store_cols<true>(vu, lds, p.col_q, p.col_s, 2 * F, F + c0, F - c0, p.rows, r0);
   }
   if (p.a_q) {
     if (p.col_q) __syncthreads();
-    tq_store_cols<false>(va, lds, p.a_q, p.a_s, F, c0, F - c0, p.rows, r0);
+    tq_store_cols<true>(va, lds, p.a_q, p.a_s, F, c0, F - c0, p.rows, r0);
   }
 }
 
