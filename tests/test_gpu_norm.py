@@ -175,6 +175,15 @@ def test_rows_of_zeros_infinities_and_nan():
     assert torch.isnan(dres[5]).all()
 
 
+def test_a_row_past_the_squares_range():
+    """|r| = 2^70: the squares add up to infinity, y is zero; |r| = 2^60: they do not."""
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device=DEV)
+    x[0], x[1] = -2.0 ** 70, -2.0 ** 60
+    total, y, _, _ = mxa.rmsnorm(x)
+    torch.cuda.synchronize()
+    assert torch.equal(total, x) and not y[0].any() and (y[1] == -1).all() and (y[2] == 1).all()
+
+
 def test_no_rows():
     c = Case(1, 64)
     dw = torch.full((64,), 7.0, device=DEV)

@@ -118,6 +118,41 @@ def test_against_autograd():
             assert rel(got, want.grad) < 3 * noise, name
 
 
+@pytest.mark.parametrize("T", [1, 37])
+def test_a_batch_without_targets(T):
+    """Every target masked: no loss, and gradients that are exactly zero."""
+    x, layers, norm, wv, t, _ = model(T, 128, 64, 4, 300, 2, seed=4)
+    b = moe.StackBuffers(T, 128, 64, 4, 2, 300, 2)
+    moe.stack_step(b, x, layers, norm, wv, torch.full_like(t, -1))
+    torch.cuda.synchronize()
+    assert torch.isfinite(b.lse).all() and not b.loss.any()
+    for grad in (b.dsum, b.dwv, b.dnorm):
+        assert not grad.any()
+    for kept in b.kept:
+        for grad in (kept.dnorm, kept.dwg, kept.dbg, kept.dw1, kept.dw2):
+            assert not grad.any()
+
+
+def test_two_stacks_at_once():
+    """Steps on two streams, each with its own buffers, give what each gives alone."""
+    T, H, F, E, k, V, L = 200, 256, 128, 8, 2, 3000, 2
+    made = [model(T, H, F, E, V, L, seed=s) for s in (11, 12)]
+    want, got = ([moe.StackBuffers(T, H, F, E, k, V, L) for _ in made] for _ in range(2))
+    streams = [torch.cuda.Stream() for _ in made]
+    for b, (x, layers, norm, wv, t, rw) in zip(want, made):
+        moe.stack_step(b, x, layers, norm, wv, t, rw)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for b, s, (x, layers, norm, wv, t, rw) in zip(got, streams, made):
+            moe.stack_step(b, x, layers, norm, wv, t, rw, s.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for name in ("loss", "lse", "dsum", "dwv", "dnorm"):
+            assert torch.equal(getattr(a, name), getattr(b, name)), name
+        for p, q in zip(a.kept, b.kept):
+            assert all(torch.equal(getattr(p, n), getattr(q, n)) for n in ("dnorm", "dwg", "dbg", "dw1", "dw2"))
+
+
 def trained(seed=5):
     T, H, F, E, k, V, L = 120, 128, 64, 6, 2, 260, 2
     x, layers, norm, wv, t, rw = model(T, H, F, E, V, L, seed)
