@@ -15,8 +15,8 @@
 // with several, dw is added up in fp32.
 //
 // The products run in the tiles of product.h and bound the call: 4096 rows, 65536
-// words, k 5120 with both gradients takes 6.7 ms (1.23 PFLOP/s), 2.0 the loss, 2.2
-// dx, 2.3 dw, 0.2 k_xent_dz; a library's three plain products of these shapes take
+// words, k 5120 with both gradients takes 6.5 ms (1.27 PFLOP/s), 2.0 the loss, 2.1
+// dx, 2.2 dw, 0.2 k_xent_dz; a library's three plain products of these shapes take
 // 7.24.  Everything is added in a fixed order: repeated calls give the same bits.
 
 #include "few_rows.h"
@@ -40,8 +40,8 @@ struct XentArgs {
   const int32_t* targets;   // [I]
   float2* part;             // [strips, I]: a strip's largest logit and sum of exponentials
   float* zt;                // [I]: the target's logit
-  uint16_t* e;              // fp16 [I, pitch]: exp(z - m)
-  int64_t pitch;            // J rounded up to 8: the columns past J are zeros
+  uint16_t* e;              // fp16 [I, pitch]: exp(z - m), zeros to the next multiple of 8 columns
+  int64_t pitch;
 };
 
 template <bool kGrad>
@@ -94,7 +94,7 @@ struct XentEpi {
           const int row = kRpp * it + lane / kLpr, c = 8 * (lane % kLpr);
           const uint4 v = *reinterpret_cast<const uint4*>(slice + row * kPitch + 2 * c);
           const int64_t ri = i0 + 32 * m + row;
-          if (ri < I && j0 + c < p.pitch) *reinterpret_cast<uint4*>(p.e + ri * p.pitch + j0 + c) = v;
+          if (ri < I && j0 + c < J) *reinterpret_cast<uint4*>(p.e + ri * p.pitch + j0 + c) = v;
         }
         asm volatile("" ::: "memory");
       }
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256) k_xent_dz(const float2* __restrict__ part
 #pragma unroll
   for (int s = 0; s < kDzStrips; ++s) {
     const int64_t c = (int64_t)(s0 + s) * TN + 8 * (threadIdx.x % kLpr);
-    if (c < pitch) {
+    if (c < vocab) {
       v[s] = *reinterpret_cast<const uint4*>(e + i * pitch + c);
       m[s] = part[(int64_t)(s0 + s) * rows + i].x;
     }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(256) k_xent_dz(const float2* __restrict__ part
 #pragma unroll
   for (int s = 0; s < kDzStrips; ++s) {
     const int64_t c = (int64_t)(s0 + s) * TN + 8 * (threadIdx.x % kLpr);
-    if (c >= pitch) break;
+    if (c >= vocab) break;
     const float f = g * exp_of(m[s] - l);
     const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
     uint32_t o[4];
@@ -332,10 +332,16 @@ int32_t strips_of(int64_t rows, int64_t vocab, int64_t k) {
   return (int32_t)((vocab + bn - 1) / bn * (bn / strip_cols(shape)));
 }
 
+// Elements between the rows of exponentials.  Long rows take whole lines, an odd
+// number of 256 bytes, so that a column of rows falls on all of the memory's channels
+// (4096 rows of 65536, k 5120, both gradients: 6.50 ms, with a pitch of 65536 6.65);
+// of short ones that would be a large part.
+int64_t pitch_of(int64_t vocab) { return vocab < 4096 ? up(vocab, 8) : 128 * ((vocab + 127) / 128 | 1); }
+
 // Rows that are in work together: their exponentials and their copies of x
 // (without a gradient: the strips' sums) take 2 GiB at most.
 int64_t chunk_rows(int64_t rows, int64_t vocab, int64_t k, bool grad) {
-  const int64_t row_bytes = grad ? 2 * (vocab > k ? up(vocab, 8) : k) : (vocab + 255) / 256 * 8 * 8;
+  const int64_t row_bytes = grad ? 2 * (vocab > k ? pitch_of(vocab) : k) : (vocab + 255) / 256 * 8 * 8;
   int64_t most = (2ll << 30) / row_bytes / 256 * 256;
   if (most < 256) most = 256;
   if (rows <= most) return rows;
@@ -361,7 +367,7 @@ XentSpace xent_space(int64_t rows, int64_t vocab, int64_t k, bool grad) {
     return s;
   }
   s.chunk = chunk_rows(rows, vocab, k, grad);
-  s.pitch = up(vocab, 8);
+  s.pitch = pitch_of(vocab);
   const int64_t last = rows % s.chunk ? rows % s.chunk : s.chunk;
   for (const int64_t r : {s.chunk, last}) {
     const int64_t part = up(8 * (int64_t)strips_of(r, vocab, k) * r, 256);
@@ -454,7 +460,7 @@ extern "C" int mx_bf16_xent(const uint16_t* x, const uint16_t* w, const int32_t*
     hipLaunchKernelGGL(k_xent_join, dim3(j.blocks + copies), dim3(1024), 0, st, j);
     if (!grad) continue;
     const int tn = strip_cols(plan_product(r, vocab, k).shape), per = 256 / (tn / 8);
-    const uint32_t bj = (uint32_t)((s.pitch + kDzStrips * tn - 1) / (kDzStrips * tn));
+    const uint32_t bj = (uint32_t)((vocab + kDzStrips * tn - 1) / (kDzStrips * tn));
     const dim3 grid((unsigned)(bj * ((r + per - 1) / per)));
     const float* rw = row_weight ? row_weight + r0 : nullptr;
     if (tn == 64) hipLaunchKernelGGL(k_xent_dz<64>, grid, dim3(256), 0, st, part, own_lse, tr, rw, r, vocab, s.pitch, bj, e);
