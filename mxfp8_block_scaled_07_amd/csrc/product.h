@@ -89,13 +89,14 @@ struct TileLoads {
   static_assert(R * kC * 2 % (1024 * kNw) == 0, "whole loads per wave");
   uint32_t voff[kLoads];
   int32_t kc;   // rows: the lane's first c in a tile
+  int32_t w;    // the wave
   const uint8_t* base;
   int64_t bytes, step;
 
   // first: the tile's first row (i or j), n: rows of the operand, C: contraction length
   __device__ void init(const Operand& o, int64_t first, int64_t n, int64_t C) {
     const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (kRows) {
       const int64_t rows = n - first < R ? n - first : R;
       base = reinterpret_cast<const uint8_t*>(o.p + first * o.ld);
@@ -148,7 +149,6 @@ struct TileLoads {
   }
   template <bool kOnce>
   __device__ void load(const Tile& t, int i, uint32_t lds) const {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t to = lds + 1024u * (uint32_t)(w + kNw * i), from = kRows && !t.ok ? kOob : voff[i];
     if constexpr (kOnce) dma16_nt(t.r, to, from, t.soff);
     else dma16(t.r, to, from, t.soff);
@@ -209,7 +209,7 @@ enum { kOnceNone, kOnceA, kOnceB };
 // From registers 16 x 16 x 32 reaches 2.1 PFLOP/s where 32 x 32 x 16 reaches 1.85
 // (zeros: 2.4 both); in this loop they take 1.99 ms and 2.09 ms.  4 waves of 128 x
 // 128 read a third less from LDS and take 2.17 ms (one wave of a SIMD has nothing
-// beside it at a wait).
+// beside it at a wait).  As it stands the loop takes 1.95 ms, 1.59 with zeros.
 template <int BM, int BN, int kWm, int kWn, int kC, int kSlots, bool kARows, bool kBRows, class E, int kOnce>
 __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::Args> p) {
   constexpr int kNw = kWm * kWn;
@@ -299,23 +299,31 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
   if constexpr (kHalves) {
     // The ring takes A(t0), B(t0), A(t0 + 1), B(t0 + 1), ...: tile t's A in place
     // 2 (t - t0) mod 5, its B behind it.
+    const int32_t n = (int32_t)(t1 - t0);
     uint32_t da = 0, db = 0;
     auto load_a = [&](int i) {
       if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, da);
     };
     auto load_b = [&](int i) { lb.template load<kOnce == kOnceB>(tb, i, db); };
+    // (With 16 x 16 fragments the loads behind the last tile are issued too, of
+    // nothing: without branches between the products the places of everything else
+    // can be set.)
+    constexpr bool kAlways = kSide == 16;
     auto hand_a = [&](int64_t t, int at) {
       ta = la.prepare(t, p.C);
+      if (kAlways && (int32_t)(t - t0) >= n) ta.r[2] = 0;
       da = base + (uint32_t)(at * kABytes);
     };
     auto hand_b = [&](int64_t t, int at) {
       tb = lb.prepare(t, p.C);
+      if (kAlways && (int32_t)(t - t0) >= n) tb.r[2] = 0;
       db = base + (uint32_t)(at * kABytes);
     };
 #pragma unroll
     for (int s = 0; s < 3; ++s)
-      if (t0 + s < t1) {
+      if (kAlways || t0 + s < t1) {
         hand_a(t0 + s, 2 * s);
+        if (kAlways && s == 2) break;   // (the loop's first loads)
 #pragma unroll
         for (int i = 0; i < kLa; ++i) load_a(i);
         if (s < 2) {
@@ -324,7 +332,8 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
           for (int i = 0; i < kLb; ++i) load_b(i);
         }
       }
-    if (t0 + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kLa + kLb));   // tile t0 is there
+    if (kAlways) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa + kLb));   // tile t0 is there
+    else if (t0 + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kLa + kLb));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     bare_barrier();
     int at = 0;          // A's place
@@ -332,7 +341,11 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
     auto place = [](int v) { return v >= 5 ? v - 5 : v; };
     if constexpr (kSide == 16) {
       // Two parts of 32 c.  A fragment of A is used by one row of products and read
-      // anew behind it; those of B have two sets.
+      // anew behind it; those of B have two sets.  Nothing is moved past two rows, or
+      // one where a fragment of A takes two reads: 4096 x 65536 x 5120 with both
+      // gradients 6.33 ms, one row for all 6.39, left to the compiler 6.62, branches
+      // around the loads instead 6.50.  kAhead: the rows of the second part in front
+      // of the waits; 1 takes 6.46, 3 and 4 6.38.
       constexpr int GM = TM / 16, GN = TN / 16, kAhead = 2, kLeft = GM - kAhead;
       static_assert(kParts == 4, "two parts of 32 c");
       v4f s[GM][GN];
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
           s[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[q][n], x[m], s[m][n], 0, 0, 0);
         }
       };
-      for (int64_t t = t0; t < t1; ++t) {
+      for (int32_t t = 0; t < n; ++t) {
         const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
 #pragma unroll
         for (int m = 0; m < GM; ++m) {
@@ -360,22 +373,21 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
 #pragma unroll
           for (int n = m * GN / GM; n < (m + 1) * GN / GM; ++n) y[1][n] = fb.read(bp, wn * TN + 16 * n, 1);
           x[m] = fa.read(ap, wm * TM + 16 * m, 1);
-          if (fill) {
 #pragma unroll
-            for (int l = m * kLa / GM; l < (m + 1) * kLa / GM; ++l) load_a(l);
-          }
+          for (int l = m * kLa / GM; l < (m + 1) * kLa / GM; ++l) load_a(l);
+          if (m & 1 || !kARows) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int m = 0; m < kAhead; ++m) row(1, m);
-        // as below: the waits stand behind the second part's first products
+        // This wave has read its share of tile t, and its loads of tile t + 1 are done
+        // (A of tile t + 2 is in flight); after the barrier every wave's: B of tile t +
+        // 2 goes where A of tile t was, A of tile t + 3 where its B was.
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-        if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
         bare_barrier();
-        hand_b(t + 2, at);
-        hand_a(t + 3, place(at + 1));
-        fill = t + 3 < t1;
+        hand_b(t0 + t + 2, at);
+        hand_a(t0 + t + 3, place(at + 1));
         at = place(at + 2);
         ap = lds + at * kABytes;
         bp = lds + place(at + 1) * kABytes;
@@ -387,12 +399,12 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
           for (int n = k * GN / kLeft; n < (k + 1) * GN / kLeft; ++n) y[0][n] = fb.read(bp, wn * TN + 16 * n, 0);
 #pragma unroll
           for (int i = k * GM / kLeft; i < (k + 1) * GM / kLeft; ++i) x[i] = fa.read(ap, wm * TM + 16 * i, 0);
-          if (t + 2 < t1) {
 #pragma unroll
-            for (int l = k * kLb / kLeft; l < (k + 1) * kLb / kLeft; ++l) load_b(l);
-          }
+          for (int l = k * kLb / kLeft; l < (k + 1) * kLb / kLeft; ++l) load_b(l);
+          if (m & 1 || !kARows) __builtin_amdgcn_sched_barrier(0);
         }
       }
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));   // (the loads of nothing too are done with the LDS)
       // to the layout of the 32 x 32 instruction: there the lane's bits 4 and 5 are
       // i's bit 4 and j's bit 2, here j's bits 2 and 3
 #pragma unroll
