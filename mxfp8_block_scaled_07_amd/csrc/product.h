@@ -264,14 +264,16 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
   // A tile's products go in kC / 16 parts of 16 c.  The fragments of a part
   // are read during the part before it, and the loads into what the last tile
   // left are spread over a tile's parts, all placed between the products: a
-  // burst of either stalls the products behind it.
+  // burst of either stalls the products behind it.  The loads behind the last
+  // tile are issued too, of nothing: no branch stands between the products.
   constexpr int kLa = decltype(la)::kLoads, kLb = decltype(lb)::kLoads;
   constexpr int kParts = kC / 16, kMfma = FM * FN, kFrags = FM + FN;
   typename decltype(la)::Tile ta;
   typename decltype(lb)::Tile tb;
   v8bf a[2][FM], b[2][FN];
+  const int32_t tn = (int32_t)(t1 - t0);
   // part of fragments q; ap, bp and kk: where part 1 - q is read; loads: `count` of load(first ..)
-  auto part = [&](int q, const uint8_t* ap, const uint8_t* bp, int kk, bool fill, int first, int count, auto load) {
+  auto part = [&](int q, const uint8_t* ap, const uint8_t* bp, int kk, int first, int count, auto load) {
 #pragma unroll
     for (int i = 0; i < kMfma; ++i) {
       const int m = i / FN, n = i % FN;
@@ -281,10 +283,8 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
         if (f < FN) b[1 - q][f] = fb.read(bp, wn * TN + 32 * f, kk);
         else a[1 - q][f - FN] = fa.read(ap, wm * TM + 32 * (f - FN), kk);
       }
-      if (fill) {
 #pragma unroll
-        for (int l = i * count / kMfma; l < (i + 1) * count / kMfma; ++l) load(first + l);
-      }
+      for (int l = i * count / kMfma; l < (i + 1) * count / kMfma; ++l) load(first + l);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -299,45 +299,34 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
   if constexpr (kHalves) {
     // The ring takes A(t0), B(t0), A(t0 + 1), B(t0 + 1), ...: tile t's A in place
     // 2 (t - t0) mod 5, its B behind it.
-    const int32_t n = (int32_t)(t1 - t0);
     uint32_t da = 0, db = 0;
     auto load_a = [&](int i) {
       if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, da);
     };
     auto load_b = [&](int i) { lb.template load<kOnce == kOnceB>(tb, i, db); };
-    // (With 16 x 16 fragments the loads behind the last tile are issued too, of
-    // nothing: without branches between the products the places of everything else
-    // can be set.)
-    constexpr bool kAlways = kSide == 16;
-    auto hand_a = [&](int64_t t, int at) {
-      ta = la.prepare(t, p.C);
-      if (kAlways && (int32_t)(t - t0) >= n) ta.r[2] = 0;
+    auto hand_a = [&](int32_t t, int at) {
+      ta = la.prepare(t0 + t, p.C);
+      if (t >= tn) ta.r[2] = 0;
       da = base + (uint32_t)(at * kABytes);
     };
-    auto hand_b = [&](int64_t t, int at) {
-      tb = lb.prepare(t, p.C);
-      if (kAlways && (int32_t)(t - t0) >= n) tb.r[2] = 0;
+    auto hand_b = [&](int32_t t, int at) {
+      tb = lb.prepare(t0 + t, p.C);
+      if (t >= tn) tb.r[2] = 0;
       db = base + (uint32_t)(at * kABytes);
     };
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
-      if (kAlways || t0 + s < t1) {
-        hand_a(t0 + s, 2 * s);
-        if (kAlways && s == 2) break;   // (the loop's first loads)
+    for (int s = 0; s < 2; ++s) {
+      hand_a(s, 2 * s);
 #pragma unroll
-        for (int i = 0; i < kLa; ++i) load_a(i);
-        if (s < 2) {
-          hand_b(t0 + s, 2 * s + 1);
+      for (int i = 0; i < kLa; ++i) load_a(i);
+      hand_b(s, 2 * s + 1);
 #pragma unroll
-          for (int i = 0; i < kLb; ++i) load_b(i);
-        }
-      }
-    if (kAlways) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa + kLb));   // tile t0 is there
-    else if (t0 + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * kLa + kLb));
-    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      for (int i = 0; i < kLb; ++i) load_b(i);
+    }
+    hand_a(2, 4);   // (loaded in the first tile's time)
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa + kLb));   // the first tile is there
     bare_barrier();
     int at = 0;          // A's place
-    bool fill = false;   // whether A of tile t + 2 is still to be loaded
     auto place = [](int v) { return v >= 5 ? v - 5 : v; };
     if constexpr (kSide == 16) {
       // Two parts of 32 c.  A fragment of A is used by one row of products and read
@@ -365,7 +354,7 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
           s[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[q][n], x[m], s[m][n], 0, 0, 0);
         }
       };
-      for (int32_t t = 0; t < n; ++t) {
+      for (int32_t t = 0; t < tn; ++t) {
         const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
 #pragma unroll
         for (int m = 0; m < GM; ++m) {
@@ -386,8 +375,8 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
         __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
         bare_barrier();
-        hand_b(t0 + t + 2, at);
-        hand_a(t0 + t + 3, place(at + 1));
+        hand_b(t + 2, at);
+        hand_a(t + 3, place(at + 1));
         at = place(at + 2);
         ap = lds + at * kABytes;
         bp = lds + place(at + 1) * kABytes;
@@ -404,7 +393,6 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
           if (m & 1 || !kARows) __builtin_amdgcn_sched_barrier(0);
         }
       }
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));   // (the loads of nothing too are done with the LDS)
       // to the layout of the 32 x 32 instruction: there the lane's bits 4 and 5 are
       // i's bit 4 and j's bit 2, here j's bits 2 and 3
 #pragma unroll
@@ -424,24 +412,22 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
     } else {
       start();
       constexpr int kPer = (kLa + kParts - 2) / (kParts - 1);
-      for (int64_t t = t0; t < t1; ++t) {
+      for (int32_t t = 0; t < tn; ++t) {
         const uint8_t *ap = lds + at * kABytes, *bp = lds + place(at + 1) * kABytes;
 #pragma unroll
-        for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, ap, bp, kk, fill, (kk - 1) * kPer, kPer, load_a);
+        for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, ap, bp, kk, (kk - 1) * kPer, kPer, load_a);
         // this wave has read its share of tile t, and its loads of tile t + 1 are
         // done (A of tile t + 2 may be in flight) ...
         __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-        if (t + 2 < t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLa));
         // ... and after the barrier every wave's: B of tile t + 2 goes where A of
         // tile t was, A of tile t + 3 where its B was
         bare_barrier();
         hand_b(t + 2, at);
         hand_a(t + 3, place(at + 1));
-        fill = t + 3 < t1;
         at = place(at + 2);
         // (after the last tile this reads old halves, which are not used)
-        part(1, lds + at * kABytes, lds + place(at + 1) * kABytes, 0, t + 2 < t1, 0, kLb, load_b);
+        part(1, lds + at * kABytes, lds + place(at + 1) * kABytes, 0, 0, kLb, load_b);
       }
     }
   } else {
@@ -452,46 +438,42 @@ __global__ void __launch_bounds__(64 * kWm * kWn) k_product(Product<typename E::
       if (i < kLa) la.template load<kOnce == kOnceA>(ta, i, dst);
       else lb.template load<kOnce == kOnceB>(tb, i - kLa, dst + kABytes);
     };
-    auto hand = [&](int64_t t, int s) {
-      ta = la.prepare(t, p.C);
-      tb = lb.prepare(t, p.C);
+    auto hand = [&](int32_t t, int s) {
+      ta = la.prepare(t0 + t, p.C);
+      tb = lb.prepare(t0 + t, p.C);
+      if (t >= tn) ta.r[2] = tb.r[2] = 0;
       dst = base + (uint32_t)s * kSlot;
     };
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      if (t0 + s < t1) {
-        hand(t0 + s, s);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) load(i);
-      }
-    if (t0 + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots - 1)));
-    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    bare_barrier();
     // with two slots a tile has one tile's time to arrive: its loads all go into the first part
     constexpr int kPerPart = kSlots == 2 ? kLoads : (kLoads + kParts - 1) / kParts;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      hand(s, s);
+#pragma unroll
+      for (int i = 0; i < (s + 1 < kSlots ? kLoads : kPerPart); ++i) load(i);   // (the last tile's others: in the first's time)
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0) + kPerPart));
+    bare_barrier();
     start();
     int slot = 0;
-    bool fill = false;   // whether the tile in hand is loaded
-    for (int64_t t = t0; t < t1; ++t) {
+    for (int32_t t = 0; t < tn; ++t) {
       const uint8_t* tile = lds + slot * kSlot;
       const int next = slot + 1 == kSlots ? 0 : slot + 1;
 #pragma unroll
-      for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, tile + kABytes, kk, fill, kk * kPerPart, kPerPart, load);
+      for (int kk = 1; kk < kParts; ++kk) part((kk & 1) ^ 1, tile, tile + kABytes, kk, kk * kPerPart, kPerPart, load);
       // this wave has read its share of the slot, and its loads of tile t + 1
-      // are done (the kSlots - 2 tiles after it may be in flight; near the end
-      // fewer are, so everything is waited for) ...
+      // are done (the kSlots - 2 tiles after it may be in flight) ...
       __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-      if (kSlots > 2 && t + kSlots <= t1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
-      else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kSlots > 2 ? kSlots - 2 : 0)));
       // ... and after the barrier every wave's: the slot takes tile t + kSlots
       bare_barrier();
-      fill = t + kSlots < t1;
       hand(t + kSlots, slot);
       // (after the last tile this reads an old slot, which is not used)
-      part(1, lds + next * kSlot, lds + next * kSlot + kABytes, 0, fill, 0, kPerPart, load);
+      part(1, lds + next * kSlot, lds + next * kSlot + kABytes, 0, 0, kPerPart, load);
       slot = next;
     }
   }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));   // (the loads of nothing too are done with the LDS)
   __syncthreads();
 
   if (!whole) {
@@ -553,7 +535,7 @@ constexpr struct {
   double us;            // microseconds per 64 c of a round with all slots busy and operands in L2
   double stream;        // bytes per microsecond at which it streams operands that are read once
 } kShape[kShapes] = {
-    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 535 us, against 710 with 128 x 128 and 1240 with 64 x 64
+    {256, 256, 1, 1.75, 4.9e6},   // 8192 x 5120 x 8192: 530 us, against 710 with 128 x 128 and 1240 with 64 x 64
     {128, 128, 2, 1.13, 4.9e6},
     {128, 64, 1, 0.70, 6.3e6},    // 32768 x 64 x 7168: 75 us, against 107 with 128 x 128
     {64, 128, 1, 0.70, 5.0e6},    // 64 x 7168 x 8191: 31 us, against 36 with 64 x 64
