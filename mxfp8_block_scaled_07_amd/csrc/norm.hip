@@ -150,8 +150,8 @@ struct Norm {
 
 // Workgroup b takes rows b, b + gridDim, ...: the card walks through the rows
 // together, the next row on the way while one is finished (two rows ahead
-// measure the same).  32768 x 7168 with every output: 372 us, 5.7 TB/s (a copy
-// reaches 6.6); rows above 32768 columns overflow the registers, 2.9 TB/s at 65536.
+// measure the same).  32768 x 7168 with every output: 370 us, 5.7 TB/s, 32768 x
+// 4096 197 us, 6.2 TB/s (a copy reaches 6.6); rows above 32768 columns overflow the registers, 2.9 TB/s at 65536.
 template <int N, bool kF32>
 __global__ void __launch_bounds__(1024) k_rmsnorm(const Norm p) {
   __shared__ float slots[2][kMaxWaves][1];
@@ -173,9 +173,13 @@ __global__ void __launch_bounds__(1024) k_rmsnorm(const Norm p) {
       rr[i].load(br, 16u * (t + T * i));
     }
   };
-  load(blockIdx.x);
+  // workgroup b runs on XCD b % 8: each takes a run of the rows in work, so that the
+  // lines of scales, 4 bytes of each of 32 rows, are written in one L2 (131072 x 512:
+  // 96 us against 111; 32768 x 5120: 253 against 260)
+  const uint32_t b = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+  load(b);
   int odd = 0;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, odd ^= 1) {
+  for (int64_t r = b; r < p.rows; r += gridDim.x, odd ^= 1) {
     const __amdgpu_buffer_rsrc_t bs = row_of(p.sum, r, (kF32 ? 4 : 2) * p.cols, true), by = row_of(p.y, r, 2 * p.cols, true);
     const __amdgpu_buffer_rsrc_t bq = row_of(p.row_q, r, p.cols, true);
     Raw<kF32> v[N];   // r as it is stored
@@ -364,7 +368,7 @@ Split split_row(int64_t cols, bool f32_bwd) {
 // Workgroups for rows that move `bytes` an element: few rows in work, near each
 // other, 40 KB to a CU.  32768 x 7168, backward with dsum (8 bytes): 298 us with
 // one per CU, 345 with two; 32768 x 4096, x to y (4 bytes): 89 us with two, 124
-// with one; 131072 x 512 with all outputs (9 bytes): 103 us with 8, 150 with 4.
+// with one; 131072 x 512 with all outputs (9 bytes): 97 us with 8, 139 with 4.
 int32_t blocks_for(int64_t rows, int64_t cols, int64_t bytes) {
   const int64_t row = bytes * cols / 8;
   const int64_t per_cu = (5000 + row / 2) / row;
