@@ -15,8 +15,8 @@
 // with several, dw is added up in fp32.
 //
 // The products run in the tiles of product.h and bound the call: 4096 rows, 65536
-// words, k 5120 with both gradients takes 6.5 ms (1.27 PFLOP/s), 2.0 the loss, 2.1
-// dx, 2.2 dw, 0.2 k_xent_dz; a library's three plain products of these shapes take
+// words, k 5120 with both gradients takes 6.3 ms (1.3 PFLOP/s), 2.0 the loss, 2.0 dx,
+// 2.1 dw, 0.2 k_xent_dz; a library's three plain products of these shapes take
 // 7.24.  Everything is added in a fixed order: repeated calls give the same bits.
 
 #include "few_rows.h"
@@ -334,7 +334,7 @@ int32_t strips_of(int64_t rows, int64_t vocab, int64_t k) {
 
 // Elements between the rows of exponentials.  Long rows take whole lines, an odd
 // number of 256 bytes, so that a column of rows falls on all of the memory's channels
-// (4096 rows of 65536, k 5120, both gradients: 6.50 ms, with a pitch of 65536 6.65);
+// (4096 rows of 65536, k 5120, both gradients: 2.3% less time than a pitch of 65536);
 // of short ones that would be a large part.
 int64_t pitch_of(int64_t vocab) { return vocab < 4096 ? up(vocab, 8) : 128 * ((vocab + 127) / 128 | 1); }
 
