@@ -520,7 +520,7 @@ int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_
 
 /*
  * Softmax cross entropy over a vocabulary, from the hidden rows and the output
- * weights, with its gradient; the logits are not kept.
+ * weights, with its gradient, without a matrix of all logits.
  *   z = x w^T;  lse_i = log sum_v exp z[i,v];  loss_i = lse_i - z[i, targets[i]]
  *   dz[i] = row_weight[i] (softmax(z[i]) - onehot(targets[i]))
  *   dx = dz w,  dw = dz^T x      (the gradient of sum_i row_weight[i] loss[i])
@@ -535,11 +535,14 @@ int mx_rmsnorm_bwd(const uint16_t* dy, const void* sum, const void* dsum, int32_
  *            backward != 0 with dx or dw; calls that overlap in time need their
  *            own.  The size is 0 for arguments of its own that the call refuses.
  * fp32 sums; dz is rounded to bf16 once for the two products (the matrix
- * instruction's operand).  At least one output.  Any rows >= 0 (with 0, dw is
+ * instruction's operand).  For it, z - m of each logit, m the largest of 32 or 64
+ * consecutive ones of its row, waits in 16 bits for the row's lse: softmax is off
+ * by a factor of 2^(2^-11) at most, and zero where exp(z - m) < 2^-63.9.
+ * At least one output.  Any rows >= 0 (with 0, dw is
  * zero) and vocab >= 1; k % 32 == 0; x, w, dx, dw and workspace 16-byte, the
  * others 4-byte aligned.  MX_EUNSUPPORTED for vocab or k >= 2^21, rows >= 2^31 or
  * a launch of 2^32 threads.  With gradients, rows are taken in chunks whose
- * exponentials (2 bytes a logit) fill at most 2 GiB of the workspace (256 rows at
+ * z - m (2 bytes a logit) fill at most 2 GiB of the workspace (256 rows at
  * least); with several, 4 vocab k bytes of it hold the sum of dw.  Repeated calls
  * give the same bits.
  */

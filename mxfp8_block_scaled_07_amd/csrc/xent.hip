@@ -4,15 +4,18 @@
 //   z = x w^T,  lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_{i, t_i}
 //   dz = g_i (softmax(z_i) - onehot(t_i)),  dx = dz w,  dw = dz^T x
 //
-// The logits are never kept.  The product's epilogue reduces a wave's columns of
-// a row to their largest value m and the sum of exp(z - m) (a strip of 32 or 64
-// columns); a second launch joins a row's strips.  For the gradient the epilogue
-// also leaves exp(z - m) of a chunk of rows in fp16: a value in [0, 1] to 11
-// bits (2^-12 of it, or 2^-25 of the strip's largest), an eighth of what dz is
-// rounded by afterwards, so that a second product of the logits (a quarter of
-// all the work) is saved and dz = g (exp(z - m) exp(m - lse) - onehot) is rounded
-// to bf16, the matrix instruction's operand, once.  Chunks bound the workspace;
-// with several, dw is added up in fp32.
+// The product's epilogue reduces a wave's columns of a row to their largest value
+// m and the sum of exp(z - m) (a strip of 32 or 64 columns); a second launch joins
+// a row's strips.  Without a gradient no logit is kept.  For the gradient the
+// epilogue also leaves log2 exp(z - m) of a chunk of rows in 16 bits, so that a
+// second product of the logits (a quarter of all the work) is saved; dz = g
+// (exp(z - lse) - onehot) is rounded to bf16, the matrix instruction's operand,
+// once.  The logarithm goes in even steps of 2^-10 from 0 to -64: half a step is
+// 2^-11.5 of an exponential however small, an eleventh of the most that dz is rounded
+// by afterwards, and one below 2^-64 of its strip's largest is zero.  (As fp16 the
+// exponentials of the same 16 bits lose theirs from 2^-14 on and are zero below
+// 2^-25: the gradients of words 10 to 17 nats under a neighbour.)  Chunks bound
+// the workspace; with several, dw is added up in fp32.
 //
 // The products run in the tiles of product.h and bound the call: 4096 rows, 65536
 // words, k 5120 with both gradients takes 6.3 ms (1.3 PFLOP/s), 2.0 the loss, 2.0 dx,
@@ -25,13 +28,17 @@
 namespace mx {
 namespace {
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }   // x <= 0
 
-__device__ __forceinline__ uint32_t half2_rne(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2h));
+// Differences x <= 0 of logits as they are kept: -x log2 e in steps of kStep, to
+// nearest; kNone and what is past it stand for exponentials of zero.  NaN may
+// become anything (its row's lse is NaN).
+constexpr float kStep = 64.0f / 65535.0f;
+constexpr uint32_t kNone = 65535;
+__device__ __forceinline__ uint32_t keep2(float a, float b) {
+  constexpr float f = -kLog2e / 64.0f;
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(a * f, b * f));   // of 65535, clamped
 }
 
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
@@ -40,7 +47,7 @@ struct XentArgs {
   const int32_t* targets;   // [I]
   float2* part;             // [strips, I]: a strip's largest logit and sum of exponentials
   float* zt;                // [I]: the target's logit
-  uint16_t* e;              // fp16 [I, pitch]: exp(z - m), zeros to the next multiple of 8 columns
+  uint16_t* e;              // [I, pitch]: z - m as keep2 gives it, kNone to the next multiple of 8 columns
   int64_t pitch;
 };
 
@@ -52,7 +59,7 @@ struct XentEpi {
   __device__ static __forceinline__ void run(const XentArgs& p, v16f (&acc)[TM / 32][TN / 32], uint8_t* slice, int64_t i0,
                                              int64_t j0, int64_t I, int64_t J, Sums sums) {
     constexpr int FM = TM / 32, FN = TN / 32, kPitch = 2 * TN + 16;
-    static_assert(32 * kPitch <= kStageBytes<TN>, "the slice holds 32 rows of fp16");
+    static_assert(32 * kPitch <= kStageBytes<TN>, "the slice holds 32 rows of 16 bits");
     const int lane = threadIdx.x & 63, h = lane >> 5;
     sums();
 #pragma unroll
@@ -81,12 +88,12 @@ struct XentEpi {
       }
       const float ref = top == -INFINITY ? 0.0f : top;   // (a strip of nothing: exponentials of zero)
 #pragma unroll
-      for (int r = 0; r < FN * 16; ++r) z[r] = exp_of(z[r] - ref);
+      for (int r = 0; r < FN * 16; ++r) z[r] -= ref;
       if constexpr (kGrad) {
 #pragma unroll
         for (int g = 0; g < FN * 4; ++g)
           *reinterpret_cast<uint2*>(slice + (lane & 31) * kPitch + 2 * (at(4 * g) + 4 * h)) =
-              make_uint2(half2_rne(z[4 * g], z[4 * g + 1]), half2_rne(z[4 * g + 2], z[4 * g + 3]));
+              make_uint2(keep2(z[4 * g], z[4 * g + 1]), keep2(z[4 * g + 2], z[4 * g + 3]));
         asm volatile("" ::: "memory");   // exchanged between the wave's lanes, whose LDS accesses run in order
         constexpr int kLpr = TN / 8, kRpp = 64 / kLpr;
 #pragma unroll
@@ -98,6 +105,8 @@ struct XentEpi {
         }
         asm volatile("" ::: "memory");
       }
+#pragma unroll
+      for (int r = 0; r < FN * 16; ++r) z[r] = exp_of(z[r]);
 #pragma unroll
       for (int w = FN * 8; w > 0; w /= 2)
 #pragma unroll
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(1024) k_xent_join(const JoinArgs p) {
   if (p.loss) p.loss[i] = t >= 0 && t < p.vocab ? l - p.zt[i] : 0.0f;
 }
 
-// dz in place of the exponentials: a thread takes 8 columns of a row in each of
+// dz in place of the kept logarithms: a thread takes 8 columns of a row in each of
 // kDzStrips strips.  Rows without a target are zeros whatever they held.  HBM-bound:
 // 4096 x 65536 takes 184 us, 5.8 TB/s.
 constexpr int kDzStrips = 8;
@@ -250,13 +259,13 @@ __global__ void __launch_bounds__(256) k_xent_dz(const float2* __restrict__ part
   for (int s = 0; s < kDzStrips; ++s) {
     const int64_t c = (int64_t)(s0 + s) * TN + 8 * (threadIdx.x % kLpr);
     if (c >= vocab) break;
-    const float f = g * exp_of(m[s] - l);
+    const float f = (m[s] - l) * kLog2e, none = f - INFINITY;   // (NaN in a row whose lse is NaN)
+    auto exp_at = [&](uint32_t n) { return __builtin_amdgcn_exp2f(n == kNone ? none : fmaf((float)n, -kStep, f)); };
     const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const v2h x = __builtin_bit_cast(v2h, w[k]);
-      float lo = (float)x[0] * f, hi = (float)x[1] * f;
+      float lo = g * exp_at(w[k] & 0xFFFFu), hi = g * exp_at(w[k] >> 16);
       if (c + 2 * k == t) lo -= g;
       if (c + 2 * k + 1 == t) hi -= g;
       o[k] = live ? bf16x2_rne(lo, hi) : 0u;
@@ -332,13 +341,13 @@ int32_t strips_of(int64_t rows, int64_t vocab, int64_t k) {
   return (int32_t)((vocab + bn - 1) / bn * (bn / strip_cols(shape)));
 }
 
-// Elements between the rows of exponentials.  Long rows take whole lines, an odd
+// Elements between the rows of z - m.  Long rows take whole lines, an odd
 // number of 256 bytes, so that a column of rows falls on all of the memory's channels
 // (4096 rows of 65536, k 5120, both gradients: 2.3% less time than a pitch of 65536);
 // of short ones that would be a large part.
 int64_t pitch_of(int64_t vocab) { return vocab < 4096 ? up(vocab, 8) : 128 * ((vocab + 127) / 128 | 1); }
 
-// Rows that are in work together: their exponentials and their copies of x
+// Rows that are in work together: their z - m and their copies of x
 // (without a gradient: the strips' sums) take 2 GiB at most.
 int64_t chunk_rows(int64_t rows, int64_t vocab, int64_t k, bool grad) {
   const int64_t row_bytes = grad ? 2 * (vocab > k ? pitch_of(vocab) : k) : (vocab + 255) / 256 * 8 * 8;

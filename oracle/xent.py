@@ -7,7 +7,7 @@ TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``).  Plain NumPy in fp64.
 import numpy as np
 
 F32 = 2.0 ** -24
-F16 = 2.0 ** -11
+LOG = np.log(2.0) * 2.0 ** -11 * 1.001
 BF16 = 2.0 ** -8
 TINY = 2.0 ** -126
 
@@ -18,9 +18,11 @@ def run(x, w, targets, row_weight=None):
     Bounds: a logit is an fp32 sum of K products, off by K + 16 roundings of
     their magnitudes; an exponential of a difference d by |d| + 16 roundings,
     which against e^d is 17 at most, and a sum of positive terms by a few more:
-    128 roundings of the logarithm's argument in all.  dz keeps exp(z - m) in
-    fp16: half a step of it (2^-11), or of fp16's smallest step (2^-25 of the
-    largest term), is then rounded to bf16, and summed in fp32."""
+    128 roundings of the logarithm's argument in all.  For dz, log2 of exp(z - m)
+    is kept in steps of 2^-10, half a step of which is a factor of 2^(2^-11), down
+    to 2^-63.9 of the strip's largest, 32 or 64 words that lie in one aligned group
+    of 64, and zero below; dz is then rounded to bf16, and summed in fp32.  What is
+    below fp32's normal range may be lost on the way."""
     M, V = len(x), len(w)
     t = np.asarray(targets, np.int64)
     live = (t >= 0) & (t < V)
@@ -40,8 +42,9 @@ def run(x, w, targets, row_weight=None):
     out = {"loss": (loss, eloss * 1.01 + TINY), "lse": (lse[:, 0], elz[:, 0] * 1.01 + TINY)}
     xl = np.where(live[:, None], x, 0.0)
     p, ep = (np.where(live[:, None], a, 0.0) for a in (p, ez + elz))
-    e = np.abs(g) * (p * (ep + F16 + 64 * F32 * (1 + np.abs(np.where(live[:, None], z - lse, 0.0)))) +
-                     p.max(1, keepdims=True) * 2.0 ** -25)
+    groups = np.pad(p, ((0, 0), (0, -V % 64))).reshape(M, -1, 64).max(2)
+    e = np.abs(g) * (p * (ep + LOG + 64 * F32 * (1 + np.abs(np.where(live[:, None], z - lse, 0.0)))) +
+                     groups.repeat(64, 1)[:, :V] * 2.0 ** -63.9) + (1 + np.abs(g)) * TINY
     dz = p
     dz[rows[live], t[live]] -= 1.0
     dz = dz * g

@@ -243,3 +243,45 @@ def test_helper():
     for name, t in zip(("loss", "lse", "dx", "dw", "loss", "lse"), (loss, lse, dx, dw, l2, s2)):
         within(host(t), *want[name], name)
     assert a is None and b is None
+
+
+@pytest.mark.parametrize("M,V", [(1, 64), (96, 640), (300, 4099), (2100, 8192)])
+def test_improbable_words_keep_their_gradient(M, V):
+    """Words of up to 31.5 nats below the most probable of their 64, and of 40 nats between the 64s: a word's row of dw
+    is a sum of terms of one sign, so it is off by a rounding of dz and one of itself to bf16 (2^-8 each, ln 2 2^-11 of
+    the kept logarithm beside them), however improbable the word."""
+    K = 32
+    c = Case(M, V, K, ignored=0.0)
+    one, at = mx.f64_to_bf16(np.array(1.0)), np.arange(V)
+    c.x[:, 0] = one
+    c.w[:] = 0
+    c.w[:, 0] = mx.f64_to_bf16(-0.5 * (at % 64) - 8.0 * (at // 64 % 6))
+    c.t[:] = 0
+    c.rw = c.rw + np.float32(0.01)
+    c.put()
+    want = c.check()["dw"]
+    o = c.outs()
+    c.call(*o)
+    torch.cuda.synchronize()
+    got = val(host(o[3][:V]))[1:, 0]
+    err = np.abs(got / want[0][1:, 0] - 1)
+    print("relative error", float(err.max()), "at word", 1 + int(err.argmax()), flush=True)
+    assert (err < 2 * 2.0 ** -8 + 2.0 ** -11).all() and (want[1][1:, 0] < 0.01 * want[0][1:, 0]).all()
+
+
+def test_words_past_what_is_kept_are_zero():
+    """The documented floor: exp(z - m) of 2^-63.9 and more below its strip's largest has no gradient, nothing else does."""
+    M, V, K = 70, 320, 32
+    c = Case(M, V, K, ignored=0.0, weighted=False)
+    c.x[:, 0] = mx.f64_to_bf16(np.array(1.0))
+    c.w[:] = 0
+    c.w[:, 0] = mx.f64_to_bf16(np.where(np.arange(V) % 32 == 5, 0.0, np.where(np.arange(V) % 2, -44.0, -45.0)))
+    c.t[:] = 5
+    c.put()
+    want = c.check()["dw"][0][:, 0]
+    o = c.outs()
+    c.call(*o)
+    torch.cuda.synchronize()
+    got = val(host(o[3][:V]))[:, 0]
+    low = c.w[:, 0] == mx.f64_to_bf16(np.array(-45.0))
+    assert not got[low].any() and (np.abs(got / want - 1)[~low] < 0.01).all()

@@ -34,3 +34,13 @@ def test_differences_and_rows_left_out():
     with_nan = xent.run(x, w, t)
     assert with_nan["loss"][0][2] == 0 and (with_nan["dx"][0][2] == 0).all()
     assert np.array_equal(with_nan["dw"][0], got["dw"][0]) and np.isfinite(with_nan["dw"][1]).all()
+
+
+def test_the_bound_of_an_improbable_word_is_its_own():
+    """Not the row's largest probability's: words 20 and 40 nats below one of their row, alone in their 64 or beside it."""
+    x, w = np.ones((1, 1)), np.zeros((256, 1))
+    w[1:64], w[64:128], w[128:192], w[192:] = -20.0, -40.0, -12.0, -43.0
+    value, bound = (a[:, 0] for a in xent.run(x, w, [0])["dw"])
+    assert np.allclose(value[1:], np.exp(w[1:, 0]) / np.exp(w).sum(), rtol=1e-12)
+    # a rounding of dz and one of dw to bf16, half a step of the logarithm and fp32's
+    assert (bound[1:] > 2.0 ** -7 * value[1:]).all() and (bound[1:] < (2.0 ** -7 + 2.0 ** -11) * 1.02 * value[1:]).all()
