@@ -273,3 +273,54 @@ def test_codes_past_32_bits():
     rq, rs = mxa.swiglu_keep(mxa.dequantize(kq, ks))[2:]
     torch.cuda.synchronize()
     assert torch.equal(rq[-64:], mxa.swiglu_keep(mxa.dequantize(dev(q), dev(spanels(s))))[2]) and not rq[:-64].any()
+
+
+@pytest.mark.parametrize("rows,F", [(4001, 160), (2100, 1056), (2085, 256)])
+def test_keep_of_many_workgroups(rows, F):
+    """More than one run of 256 workgroups, the last one partial; panels of both halves, and of one."""
+    assert rows * F // 8 > 256 * 256 and rows * F // 8 % (256 * 256)
+    g = np.random.default_rng([rows, F])
+    hd = dev(h_input(g, rows, F, range(rows - rows // 8, rows)))
+    guard = lambda *sh: torch.full(sh, 0x55, dtype=torch.uint8, device=DEV)  # noqa: E731
+    rq, rs, kq, ks = guard(rows + 1, F), guard(*mxa.scale_shape(rows, F)), guard(rows + 1, 2 * F), guard(*mxa.scale_shape(rows, 2 * F))
+    mxa.mx_swiglu_keep(hd, rows, F, rq, rs, kq, ks)
+    a = mxa.swiglu_quantize(hd, colwise=False, want_bf16=True)[0]
+    torch.cuda.synchronize()
+    same_mx(a, rq[:rows], rs)
+    same_mx(hd, kq[:rows], ks)
+    assert (rq[rows] == 0x55).all() and (kq[rows] == 0x55).all()
+
+
+# four column tiles to a workgroup (from 4096 tiles on): a last group of two, one, four and three, the last column tile
+# partial or whole, the last row tile partial
+@pytest.mark.parametrize("rows,cols,out", [(3000, 672, 90016), (2000, 640, 105056), (90000, 928, 66016), (7, 352, 175040)])
+@pytest.mark.parametrize("gathered", [True, False])
+def test_requantize_of_many_tiles(rows, cols, out, gathered):
+    assert -(-out // 128) * -(-cols // 128) >= 4096
+    if not gathered:
+        rows = out - 40 if cols != 640 else out     # (rows past the last are zeros)
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    x = torch.randn(rows, cols, device=DEV, generator=g).mul_(torch.randn(rows, cols // 32, device=DEV, generator=g)
+                                                              .exp_().repeat_interleave(32, 1)).to(torch.bfloat16)
+    q, s = mxa.quantize(x)[:2]
+    q[5, 40], q[rows - 1, cols - 1] = 0x7F, 0xFF                              # NaN codes
+    s[(cols - 1) // 128, 3, (cols // 32 - 1) % 4] = 255                       # a block of NaN: the last of row 3
+    idx = None
+    if gathered:
+        idx = torch.randint(0, rows, (out,), device=DEV, generator=g, dtype=torch.int32)
+        idx[::7], idx[3::11], idx[-1] = -1, rows + 5, rows - 1
+    cq = torch.full((cols + 1, out), 0x55, dtype=torch.uint8, device=DEV)
+    cs = torch.full(mxa.scale_shape(cols, out), 0x55, dtype=torch.uint8, device=DEV)
+    mxa.mx_requantize(q, s, rows, cols, idx, out, cq, cs)
+    want = mxa.quantize(mxa.dequantize(q, s), False, True, out, idx)[2:]
+    torch.cuda.synchronize()
+    assert torch.equal(cq[:cols], want[0]) and torch.equal(cs, want[1]) and (cq[cols] == 0x55).all()
+    # a sample of columns against the oracle, where no NaN is near
+    clean = mxa.quantize(x)[:2]
+    mxa.mx_requantize(*clean, rows, cols, idx, out, cq, cs)
+    torch.cuda.synchronize()
+    at = np.unique([0, 31, 32, 127, 128, 200, 257, cols - 33, cols - 1])
+    d = host(mxa.dequantize(*clean)[:, torch.from_numpy(at).to(DEV)].contiguous())
+    i = None if idx is None else np.where(host(idx) >= rows, -1, host(idx))
+    wq, wsc = mx.quantize_colwise(d, rows_out=out, gather=i)
+    assert np.array_equal(host(cq)[at], wq) and np.array_equal(srows(cs, out)[at], wsc)
