@@ -285,3 +285,28 @@ def test_words_past_what_is_kept_are_zero():
     got = val(host(o[3][:V]))[:, 0]
     low = c.w[:, 0] == mx.f64_to_bf16(np.array(-45.0))
     assert not got[low].any() and (np.abs(got / want - 1)[~low] < 0.01).all()
+
+
+@pytest.mark.parametrize("M,chunk", [(8500, 4352), (9000, 4608)])
+def test_chunks_of_rows_without_a_gradient(M, chunk):
+    """More rows than the strips' sums of the workspace hold: each chunk's rows as a call on them alone gives them."""
+    V, K = 1000000, 32
+    assert mxa.mx_bf16_xent_workspace_size(M, V, K, False) == mxa.mx_bf16_xent_workspace_size(chunk, V, K, False)
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x = torch.randn(M, K, device=DEV, generator=g).to(torch.bfloat16)
+    w = (torch.randn(V, K, device=DEV, generator=g) * 0.5).to(torch.bfloat16)
+    t = torch.randint(-20000, V, (M,), device=DEV, generator=g, dtype=torch.int32)
+    loss, lse, dx, dw = mxa.bf16_xent(x, w, t)
+    for r in (slice(0, chunk), slice(chunk, M)):
+        a = mxa.bf16_xent(x[r], w, t[r])
+        assert torch.equal(a[0], loss[r]) and torch.equal(a[1], lse[r])
+    out = t < 0
+    assert out.any() and not loss[out].any() and (loss[~out] > 0).all() and dx is None and dw is None
+    # rows on both sides of the border in fp64: a logit is off by K + 16 roundings of its terms, the logarithm's argument
+    # by 128, the largest logit's sum with it by a few of either
+    for i in (0, chunk - 1, chunk, M - 1):
+        z, mag = (a.double() @ b.double().T for a, b in ((x[i], w), (x[i].abs(), w.abs())))
+        want = torch.logsumexp(z, 0)
+        assert (lse[i] - want).abs() <= 2.0 ** -24 * ((K + 16) * mag.max() + 128 + 8 * want.abs()), i
+        if t[i] >= 0:
+            assert (loss[i] - (want - z[t[i]])).abs() <= 2.0 ** -24 * (2 * (K + 16) * mag.max() + 128 + 16 * want.abs()), i
