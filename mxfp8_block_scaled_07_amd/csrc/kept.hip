@@ -65,7 +65,8 @@ __device__ __forceinline__ void store_half(const uint4 (&v)[8], uint8_t* q, uint
 
 // The forward: a thread takes 8 columns of a row, so that a wave's accesses are
 // 1 KB of it (the tile quantizer's are four pieces of 256 bytes: 194 us at 67,584
-// x 2048, where this takes 173, 5.7 TB/s; 2 rows a thread the same, 4 rows 193).
+// x 2048, where this took 173 in turn with it, 5.7 TB/s; 2 rows a thread the same, 4
+// rows 193; over processes and buffers this form's calls vary from 173 to 210).
 // Workgroups go to the XCDs in runs of 32, so that the lines of scales, 4 bytes of
 // each of 32 rows, are written in one L2 (8192 x 2048: 23.2 us against 25.9).
 template <bool kWhole>
@@ -138,12 +139,15 @@ __device__ __forceinline__ float row16_sum(float v) {
 
 // The backward in the quantizer's tiles of 128 rows x 128 columns: dH's two halves
 // and A' are made from one reading of the codes and of dA, held in registers as
-// bf16, and go out by rows and, through LDS, by columns.  67,584 x 2048: 271 us,
-// 4.7 TB/s; the arithmetic bounds it (65 instructions an element, exponential and
-// five quantizes among them: 230 us of the vector units' issue).  Left to itself
-// the compiler took 512 registers and spilled; bound to three tiles a CU it does not.
+// bf16, and go out by rows and, through LDS, by columns.  67,584 x 2048: 273 us by
+// itself, 4.7 TB/s; the arithmetic bounds it (65 instructions an element, exponential
+// and five quantizes among them: 230 us of the vector units' issue).  67,520 rows take
+// 284, as every second column's run of codes starts inside a line, and 312 between
+// the other kernels of a backward, with the time of what they left to write.  Left to
+// itself the compiler took 512 registers and spilled; bound to three tiles a CU,
+// whole halves fit, and halves that share panels spill 13 registers.
 // A row's tiles on one XCD and non-temporal columns leave whole lines as they are
-// and mend shared ones: 67,584 x 2080 takes 295 us, 343 without.
+// and mend shared ones: 67,584 x 2080 takes 295 us, 343 without (67,520: 314).
 template <bool kWhole>
 __global__ void __launch_bounds__(kTqThreads, 3) k_swiglu_bwd_kept(const KeptBwd p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kTq * kTq * 2];
@@ -282,8 +286,10 @@ __global__ void __launch_bounds__(256) k_router_bwd_dots(const float* __restrict
 // Source of the tile quantizer: rowwise MX rows, decoded; gathered or in order.
 // The rows' scale dwords of the workgroup's column tiles come with the row table:
 // loaded a byte at a time beside the codes they cost more than these.  8192 x 7168
-// gathered to 67,584 rows: 129 us by itself, 175 behind kernels whose writes are
-// still in the last cache; 560 MB in pieces of 128 bytes, which alone reach 5.3 TB/s.
+// gathered to 67,584 rows: 129 us by itself, 184 between the other kernels of a
+// backward, whose writes are still on their way (67,520 rows, whose columns start
+// inside lines: 131 and 206); 560 MB in pieces of 128 bytes, which alone reach 5.3
+// TB/s.  In order, 67,584 x 2048: 55 us, 5.1 TB/s; 67,520: 62.
 template <bool kGather, int kTiles>
 struct SrcMx {
   const uint8_t* q;

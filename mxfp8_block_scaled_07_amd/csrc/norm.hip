@@ -151,7 +151,9 @@ struct Norm {
 // Workgroup b takes rows b, b + gridDim, ...: the card walks through the rows
 // together, the next row on the way while one is finished (two rows ahead
 // measure the same).  32768 x 7168 with every output: 370 us, 5.7 TB/s, 32768 x
-// 4096 197 us, 6.2 TB/s (a copy reaches 6.6); rows above 32768 columns overflow the registers, 2.9 TB/s at 65536.
+// 4096 197 us, 6.2 TB/s (a copy reaches 6.6).  Rows above 16384 columns overflow the
+// registers: by 6 of them, 61 with the fp32 stream, up to 32768 (5.5 and 4.3 TB/s
+// there), by 218 and 316 above (2.9 and 1.9 TB/s at 65536).
 template <int N, bool kF32>
 __global__ void __launch_bounds__(1024) k_rmsnorm(const Norm p) {
   __shared__ float slots[2][kMaxWaves][1];
@@ -242,8 +244,10 @@ struct NormBwd {
 };
 
 // The same walk; a thread adds up its columns of dw over the workgroup's rows, and
-// k_norm_join the workgroups' sums.  32768 x 7168 with dsum: 298 us, 6.3 TB/s; rows
-// above 16384 columns overflow the registers (1.7 TB/s at 32768, 0.7 at 65536).
+// k_norm_join the workgroups' sums.  32768 x 7168 with dsum: 298 us, 6.3 TB/s.  Rows
+// above 16384 columns, 8192 with the fp32 stream, overflow the registers: the latter
+// by 20 up to 16384 (3.9 TB/s there), both by 144 to 194 up to 32768 (1.7 TB/s) and by
+// 526 and 701 above (0.7 and 0.9 TB/s at 65536).
 template <int N, bool kF32>
 __global__ void __launch_bounds__(1024) k_rmsnorm_bwd(const NormBwd p) {
   __shared__ float slots[2][kMaxWaves][2];
@@ -368,7 +372,9 @@ Split split_row(int64_t cols, bool f32_bwd) {
 // Workgroups for rows that move `bytes` an element: few rows in work, near each
 // other, 40 KB to a CU.  32768 x 7168, backward with dsum (8 bytes): 298 us with
 // one per CU, 345 with two; 32768 x 4096, x to y (4 bytes): 89 us with two, 124
-// with one; 131072 x 512 with all outputs (9 bytes): 97 us with 8, 139 with 4.
+// with one; 131072 x 512 with all outputs (9 bytes): 97 us with 9, 139 with 4.  (A row
+// takes a wave at least: of 128 columns 16 lanes of 64 are at work, 524288 x 128 takes
+// 155 us, 3.9 TB/s; 262144 x 256 takes 105, 5.8 TB/s.)
 int32_t blocks_for(int64_t rows, int64_t cols, int64_t bytes) {
   const int64_t row = bytes * cols / 8;
   const int64_t per_cu = (5000 + row / 2) / row;
