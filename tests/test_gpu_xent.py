@@ -310,3 +310,36 @@ def test_chunks_of_rows_without_a_gradient(M, chunk):
         assert (lse[i] - want).abs() <= 2.0 ** -24 * ((K + 16) * mag.max() + 128 + 8 * want.abs()), i
         if t[i] >= 0:
             assert (loss[i] - (want - z[t[i]])).abs() <= 2.0 ** -24 * (2 * (K + 16) * mag.max() + 128 + 16 * want.abs()), i
+
+
+def test_row_weights_of_any_size_and_sign():
+    c = Case(90, 700, 64, ignored=0.1)
+    c.rw = np.resize(np.array([-2.0, 0.0, 1e-20, 1e20, 1.0, -1e-3], np.float32), 90)
+    c.put()
+    c.check()
+    o = c.outs()
+    c.call(*o)
+    torch.cuda.synchronize()
+    assert not o[2][:90][torch.from_numpy(c.rw == 0).to(DEV)].any()
+
+
+@pytest.mark.parametrize("M,V", [(3, 40), (70, 1000), (2100, 8200)])
+def test_logits_near_the_range_of_fp32(M, V):
+    """One word of 2^100 and all others of -2^100: their differences overflow to exponentials of exactly zero."""
+    K, top = 32, V // 2
+    c = Case(M, V, K, ignored=0.0, weighted=False)
+    c.x[:], c.w[:] = 0, 0
+    c.x[:, 0] = mx.f64_to_bf16(np.array(2.0 ** 50))
+    c.w[:, 0] = mx.f64_to_bf16(np.where(np.arange(V) == top, 2.0 ** 50, -2.0 ** 50))
+    c.t[:] = np.arange(M) % 2 * (V - 1 - top) + top         # the word itself, the last word
+    c.put()
+    o = c.outs()
+    c.call(*o)
+    torch.cuda.synchronize()
+    odd = np.arange(M) % 2
+    assert (host(o[1])[:M] == 2.0 ** 100).all() and np.array_equal(host(o[0])[:M], (odd * 2.0 ** 101).astype(np.float32))
+    dx, dw = np.zeros((M, K)), np.zeros((V, K))
+    dx[:, 0] = odd * 2.0 ** 51
+    dw[top, 0], dw[V - 1, 0] = odd.sum() * 2.0 ** 50, -odd.sum() * 2.0 ** 50
+    assert np.array_equal(val(host(o[2][:M])), dx)
+    assert np.array_equal(val(host(o[3][:V])), mx.bf16_to_f64(mx.f64_to_bf16(dw)))
